@@ -11,4 +11,7 @@ from .nvfp4 import (  # noqa: F401
     MXTensor, NVFP4_MX_E4M3, NVFP4_MX_E2M1, NVFP4_MX_ACC_NATIVE, NVFP4_MX_ACC_EXACT,
     nvfp4_mx_quantize, nvfp4_mx_dequantize,
     nvfp4_mx_gemm, nvfp4_mx_gemm_workspace_size,
+    NVFP4_ROUTE_SOFTMAX, NVFP4_ROUTE_SIGMOID, NVFP4_GROUP_MAX, NVFP4_GROUP_TOP2,
+    RMSNormOutput, nvfp4_rmsnorm, nvfp4_rmsnorm_backward, nvfp4_rmsnorm_backward_workspace_size,
+    RouteOutput, nvfp4_route, nvfp4_route_workspace_size, nvfp4_route_backward,
 )

@@ -98,4 +98,76 @@ GemmSplit mx_gemm_split_plan(int64_t M, int64_t N, int64_t K, double tile_us, in
 // A lone last-round tile's time per 1024 K for this element format and accumulation mode, in µs.
 double mx_split_tile_us(int elem, bool exact);
 
+// RMS norm (see nvfp4_rmsnorm); cols in [1, kMaxNormCols], codes NULL for no
+// MX output.
+constexpr int64_t kMaxNormCols = 32768;
+struct RmsNorm {
+    const void* x;
+    const void* residual;
+    const void* weight;
+    bool bf16, w_bf16;
+    int64_t rows, cols, ldx, ldr, ldh, ldy;
+    float eps;
+    void* h;
+    void* y;
+    uint8_t* codes;
+    uint8_t* scales;
+    int elem;
+    float* rstd;
+};
+hipError_t launch_rmsnorm(const RmsNorm& n, hipStream_t s);
+
+struct RmsNormBackward {
+    const void* dy;
+    const void* h;
+    const void* dh;
+    const float* rstd;
+    const void* weight;
+    bool bf16, w_bf16;
+    int64_t rows, cols, lddy, ldh, lddh, lddx;
+    void* dx;
+    float* dweight;
+    float* ws;  // rmsnorm_backward_workspace_floats
+};
+int64_t rmsnorm_backward_workspace_floats(int64_t rows, int64_t cols);
+hipError_t launch_rmsnorm_backward(const RmsNormBackward& n, hipStream_t s);
+
+// Expert routing (see nvfp4_route).
+constexpr int kMaxExperts = 2048, kMaxTopK = 16, kMaxRouteGroups = 64;
+struct RouteShape {
+    int experts, groups, group_size, top_groups, top_k;
+    int lanes_per_group;  // set by the launcher
+    bool group_top2;
+};
+struct RouteArgs {
+    const void* logits;
+    bool bf16;
+    int64_t tokens, ld;
+    const float* bias;
+    RouteShape shape;
+    bool sigmoid, renorm;
+    int* ids;
+    float* weights;
+    int64_t* offsets;  // NULL: no dispatch plan (order and position unused)
+    int* order;
+    int* position;
+    int* counts;   // route_workspace_ints
+    int64_t span;  // set by the launcher
+};
+bool route_shape_fits(int experts, int groups);
+int64_t route_workspace_ints(int64_t tokens, int experts);
+hipError_t launch_route(RouteArgs a, hipStream_t s);
+
+struct RouteBackward {
+    const float* dweights;
+    const void* logits;
+    const int* ids;
+    const float* dscores;  // nullable
+    void* dlogits;
+    int64_t tokens, ld, ldds, lddl;
+    int experts, top_k;
+    bool sigmoid, renorm;
+};
+hipError_t launch_route_backward(const RouteBackward& a, bool bf16, hipStream_t s);
+
 }  // namespace nvfp4

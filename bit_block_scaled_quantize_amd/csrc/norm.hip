@@ -1,0 +1,362 @@
+// RMS norm with the residual's addition and an MX output, and its backward
+// pass, for gfx950.
+//
+// Forward, per row of n elements:
+//   h = round(x + residual)            (the row type: the residual stream as stored)
+//   rstd = 1 / sqrt(sum h^2 / n + eps)
+//   y = (h * rstd) * weight
+// y is written in the row type, as MX codes and scales of the binary32 y, or
+// both.  Backward, with g = dy * weight and xhat = h * rstd:
+//   dx = rstd * (g - xhat * mean(g * xhat)) + dh
+//   dweight = sum over rows of dy * xhat
+// All sums are binary32 in a fixed order.
+//
+// Both are HBM-bound streams.  A row's elements stay in registers between the
+// sum and the outputs, so every array is read or written once: TPR threads
+// share a row (16, 64, 256 or 1024), each holding NC chunks of 8 consecutive
+// elements (chunk i of thread t starts at 8 (i TPR + t)), so a wave's 16-byte
+// accesses are contiguous and four lanes hold one 32-element MX block.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "launch.hpp"
+#include "nvfp4_device.hpp"
+#include "row_device.hpp"
+
+namespace nvfp4 {
+
+namespace {
+
+constexpr int kMaxNC = 4;
+
+template <typename T>
+struct NormFwd {
+    const T* x;
+    const T* residual;  // nullable
+    const void* weight;
+    T* h;               // nullable
+    T* y;               // nullable
+    uint8_t* codes;     // nullable
+    uint8_t* scales;
+    float* rstd;        // nullable
+    int64_t rows, cols, ldx, ldr, ldh, ldy;
+    float eps;
+    bool w_bf16, mx_e2m1;
+};
+
+__device__ __forceinline__ void load_weight(const void* w, bool bf16, int64_t c, int64_t n, float v[8]) {
+    if (bf16) load_upto8(static_cast<const uint16_t*>(w) + c, n, v);
+    else load_upto8(static_cast<const float*>(w) + c, n, v);
+}
+
+constexpr int block_of(int tpr) { return tpr > 256 ? tpr : 256; }
+
+template <typename T, int TPR, int NC>
+__global__ void __launch_bounds__(block_of(TPR)) k_rmsnorm(const NormFwd<T> a) {
+    __shared__ float red[TPR > 64 ? TPR / 64 : 1];
+    const int t = threadIdx.x % TPR;
+    const int64_t row = (int64_t)blockIdx.x * (block_of(TPR) / TPR) + threadIdx.x / TPR;
+    // groups past the last row repeat it and store nothing
+    const bool live = row < a.rows;
+    const int64_t r = live ? row : a.rows - 1;
+    float v[NC][8];
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        const int64_t c = 8 * ((int64_t)i * TPR + t), n = a.cols - c;
+        if (n > 0) load_upto8(a.x + r * a.ldx + c, n, v[i]);
+        else
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+    }
+    if (a.residual) {
+        float q[NC][8];
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int64_t c = 8 * ((int64_t)i * TPR + t), n = a.cols - c;
+            if (n > 0) load_upto8(a.residual + r * a.ldr + c, n, q[i]);
+            else
+#pragma unroll
+                for (int j = 0; j < 8; ++j) q[i][j] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] = rounded_to<T>(v[i][j] + q[i][j]);
+    }
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        const int64_t c = 8 * ((int64_t)i * TPR + t), n = a.cols - c;
+        if (a.h && live && n > 0) store_upto8(a.h + r * a.ldh + c, n, v[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss = __builtin_fmaf(v[i][j], v[i][j], ss);
+    }
+    ss = row_sum<TPR>(ss, red);
+    const float rstd = 1.0f / __builtin_sqrtf(ss / (float)a.cols + a.eps);
+    if (a.rstd && live && t == 0) a.rstd[r] = rstd;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        const int64_t c = 8 * ((int64_t)i * TPR + t), n = a.cols - c;
+        if (n <= 0) continue;
+        float w[8], y[8];
+        load_weight(a.weight, a.w_bf16, c, n, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = (v[i][j] * rstd) * w[j];
+        if (a.y && live) store_upto8(a.y + r * a.ldy + c, n, y);
+        if (a.codes) {  // cols % 32 == 0: the four lanes of a block agree on n > 0
+            uint32_t cw[2];
+            const uint32_t sb = a.mx_e2m1 ? mx_block_rne8<kMxE2M1>(y, cw) : mx_block_rne8<kMxE4M3>(y, cw);
+            if (live) {
+                if (a.mx_e2m1)
+                    *reinterpret_cast<uint32_t*>(a.codes + r * (a.cols / 2) + c / 2) = cw[0];
+                else
+                    *reinterpret_cast<uint2*>(a.codes + r * a.cols + c) = make_uint2(cw[0], cw[1]);
+                if ((t & 3) == 0) a.scales[r * (a.cols / 32) + c / 32] = (uint8_t)sb;
+            }
+        }
+    }
+}
+
+template <typename T>
+struct NormBwd {
+    const T* dy;
+    const T* h;
+    const T* dh;  // nullable
+    const float* rstd;
+    const void* weight;
+    T* dx;
+    float* parts;  // groups x cols
+    int64_t rows, cols, lddy, ldh, lddh, lddx, groups;
+    bool w_bf16;
+};
+
+// Row group g takes rows g, g + groups, ... and leaves its sum of dy * xhat in
+// parts[g]; the next row's elements are loaded before the current row's sum is
+// waited for.
+template <typename T, int TPR, int NC>
+__global__ void __launch_bounds__(block_of(TPR)) k_rmsnorm_backward(const NormBwd<T> a) {
+    __shared__ float red[2][TPR > 64 ? TPR / 64 : 1];
+    const int t = threadIdx.x % TPR;
+    const int64_t g = (int64_t)blockIdx.x * (block_of(TPR) / TPR) + threadIdx.x / TPR;
+    float w[NC][8], dw[NC][8];
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        const int64_t c = 8 * ((int64_t)i * TPR + t), n = a.cols - c;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[i][j] = dw[i][j] = 0.0f;
+        if (n > 0) load_weight(a.weight, a.w_bf16, c, n, w[i]);
+    }
+    // every group of a workgroup makes the same number of turns (row_sum needs
+    // all lanes); turns past the last row read it again and add nothing
+    const int64_t turns = (a.rows + a.groups - 1) / a.groups;
+    const float inv_n = 1.0f / (float)a.cols;
+    int buf = 0;
+    for (int64_t k = 0; k < turns; ++k) {
+        const int64_t row = g + k * a.groups;
+        const bool live = row < a.rows;
+        const int64_t r = live ? row : a.rows - 1;
+        float dy[NC][8], h[NC][8];
+        const float rstd = a.rstd[r];
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int64_t c = 8 * ((int64_t)i * TPR + t), n = a.cols - c;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dy[i][j] = h[i][j] = 0.0f;
+            if (n > 0) {
+                load_upto8(a.dy + r * a.lddy + c, n, dy[i]);
+                load_upto8(a.h + r * a.ldh + c, n, h[i]);
+            }
+        }
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float xh = h[i][j] * rstd;
+                if (live) dw[i][j] = __builtin_fmaf(dy[i][j], xh, dw[i][j]);
+                dy[i][j] = dy[i][j] * w[i][j];
+                h[i][j] = xh;
+                s = __builtin_fmaf(dy[i][j], xh, s);
+            }
+        s = row_sum<TPR>(s, red[buf]) * inv_n;
+        buf ^= 1;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int64_t c = 8 * ((int64_t)i * TPR + t), n = a.cols - c;
+            if (n <= 0 || !live) continue;
+            float q[8];
+            if (a.dh) load_upto8(a.dh + r * a.lddh + c, n, q);
+            else
+#pragma unroll
+                for (int j = 0; j < 8; ++j) q[j] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) q[j] = __builtin_fmaf(rstd, __builtin_fmaf(-h[i][j], s, dy[i][j]), q[j]);
+            store_upto8(a.dx + r * a.lddx + c, n, q);
+        }
+    }
+    if (g < a.groups)
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int64_t c = 8 * ((int64_t)i * TPR + t), n = a.cols - c;
+            if (n > 0) store_upto8(a.parts + g * a.cols + c, n, dw[i]);
+        }
+}
+
+// dweight[c] = sum over g of parts[g][c] in a fixed order: 32 columns a
+// workgroup, 8 threads a column.
+__global__ void __launch_bounds__(256) k_sum_parts(const float* __restrict__ parts, int64_t groups, int64_t cols,
+                                                   float* __restrict__ out) {
+    __shared__ float s[8][32];
+    const int cx = threadIdx.x & 31, gy = threadIdx.x >> 5;
+    const int64_t c = (int64_t)blockIdx.x * 32 + cx;
+    float v = 0.0f;
+    if (c < cols) {
+#pragma unroll 8
+        for (int64_t g = gy; g < groups; g += 8) v += parts[g * cols + c];
+    }
+    s[gy][cx] = v;
+    __syncthreads();
+    if (gy == 0 && c < cols) {
+#pragma unroll
+        for (int k = 1; k < 8; ++k) v += s[k][cx];
+        out[c] = v;
+    }
+}
+
+inline int64_t n_cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Threads per row: the fewest whose kMaxNC chunks hold the row; more where
+// there are too few rows to give every SIMD a wave (the row's latency then
+// counts).
+int threads_per_row(int64_t rows, int64_t cols) {
+    const int64_t chunks = n_cdiv(cols, 8);
+    int tpr = 16;
+    while (chunks > (int64_t)tpr * kMaxNC) tpr *= 4;
+    while (tpr < 1024 && tpr < chunks && rows * tpr < 64 * 1024) tpr *= 4;
+    return tpr;
+}
+
+struct BwdPlan {
+    int tpr;
+    int64_t blocks, groups;
+};
+
+// Row groups of the backward pass: two workgroups a compute unit at most, and
+// at least four rows a group where there are that many (each group costs a
+// row of binary32 partial sums, written and read again).
+BwdPlan bwd_plan(int64_t rows, int64_t cols) {
+    BwdPlan p;
+    p.tpr = threads_per_row(rows, cols);
+    const int64_t per = block_of(p.tpr) / p.tpr;
+    p.blocks = std::min<int64_t>(512, n_cdiv(n_cdiv(rows, 4), per));
+    p.groups = std::min(rows, p.blocks * per);
+    return p;
+}
+
+#define NVFP4_NORM_NC(K, T, TPR, ...)                                                                       \
+    do {                                                                                                    \
+        const int64_t nc = n_cdiv(n_cdiv(a.cols, 8), TPR);                                                  \
+        if (nc <= 1) hipLaunchKernelGGL((K<T, TPR, 1>), __VA_ARGS__, a);                                    \
+        else if (nc <= 2) hipLaunchKernelGGL((K<T, TPR, 2>), __VA_ARGS__, a);                               \
+        else hipLaunchKernelGGL((K<T, TPR, kMaxNC>), __VA_ARGS__, a);                                       \
+    } while (0)
+
+template <typename T>
+hipError_t norm_typed(const NormFwd<T>& a, hipStream_t s) {
+    const int tpr = threads_per_row(a.rows, a.cols);
+    const dim3 g((unsigned)n_cdiv(a.rows, block_of(tpr) / tpr)), b(block_of(tpr));
+    switch (tpr) {
+        case 16: NVFP4_NORM_NC(k_rmsnorm, T, 16, g, b, 0, s); break;
+        case 64: NVFP4_NORM_NC(k_rmsnorm, T, 64, g, b, 0, s); break;
+        case 256: NVFP4_NORM_NC(k_rmsnorm, T, 256, g, b, 0, s); break;
+        default: NVFP4_NORM_NC(k_rmsnorm, T, 1024, g, b, 0, s);
+    }
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t norm_bwd_typed(NormBwd<T> a, float* dweight, hipStream_t s) {
+    const BwdPlan p = bwd_plan(a.rows, a.cols);
+    a.groups = p.groups;
+    const dim3 g((unsigned)p.blocks), b(block_of(p.tpr));
+    switch (p.tpr) {
+        case 16: NVFP4_NORM_NC(k_rmsnorm_backward, T, 16, g, b, 0, s); break;
+        case 64: NVFP4_NORM_NC(k_rmsnorm_backward, T, 64, g, b, 0, s); break;
+        case 256: NVFP4_NORM_NC(k_rmsnorm_backward, T, 256, g, b, 0, s); break;
+        default: NVFP4_NORM_NC(k_rmsnorm_backward, T, 1024, g, b, 0, s);
+    }
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(k_sum_parts, dim3((unsigned)n_cdiv(a.cols, 32)), dim3(256), 0, s, a.parts, p.groups, a.cols,
+                       dweight);
+    return hipGetLastError();
+}
+#undef NVFP4_NORM_NC
+
+template <typename T>
+hipError_t norm_any(const RmsNorm& n, hipStream_t s) {
+    NormFwd<T> a;
+    a.x = static_cast<const T*>(n.x);
+    a.residual = static_cast<const T*>(n.residual);
+    a.weight = n.weight;
+    a.h = static_cast<T*>(n.h);
+    a.y = static_cast<T*>(n.y);
+    a.codes = n.codes;
+    a.scales = n.scales;
+    a.rstd = n.rstd;
+    a.rows = n.rows;
+    a.cols = n.cols;
+    a.ldx = n.ldx;
+    a.ldr = n.ldr;
+    a.ldh = n.ldh;
+    a.ldy = n.ldy;
+    a.eps = n.eps;
+    a.w_bf16 = n.w_bf16;
+    a.mx_e2m1 = n.elem == kMxE2M1;
+    return norm_typed(a, s);
+}
+
+template <typename T>
+hipError_t norm_bwd_any(const RmsNormBackward& n, hipStream_t s) {
+    NormBwd<T> a;
+    a.dy = static_cast<const T*>(n.dy);
+    a.h = static_cast<const T*>(n.h);
+    a.dh = static_cast<const T*>(n.dh);
+    a.rstd = n.rstd;
+    a.weight = n.weight;
+    a.dx = static_cast<T*>(n.dx);
+    a.parts = n.ws;
+    a.rows = n.rows;
+    a.cols = n.cols;
+    a.lddy = n.lddy;
+    a.ldh = n.ldh;
+    a.lddh = n.lddh;
+    a.lddx = n.lddx;
+    a.w_bf16 = n.w_bf16;
+    return norm_bwd_typed(a, n.dweight, s);
+}
+
+}  // namespace
+
+int64_t rmsnorm_backward_workspace_floats(int64_t rows, int64_t cols) {
+    return rows == 0 ? 0 : bwd_plan(rows, cols).groups * cols;
+}
+
+hipError_t launch_rmsnorm(const RmsNorm& n, hipStream_t s) {
+    if (n.rows == 0) return hipSuccess;
+    return n.bf16 ? norm_any<uint16_t>(n, s) : norm_any<float>(n, s);
+}
+
+hipError_t launch_rmsnorm_backward(const RmsNormBackward& n, hipStream_t s) {
+    if (n.rows == 0) {
+        // no rows: the weight's gradient is zero (the sum over no parts)
+        hipLaunchKernelGGL(k_sum_parts, dim3((unsigned)n_cdiv(n.cols, 32)), dim3(256), 0, s, n.ws, (int64_t)0,
+                           n.cols, n.dweight);
+        return hipGetLastError();
+    }
+    return n.bf16 ? norm_bwd_any<uint16_t>(n, s) : norm_bwd_any<float>(n, s);
+}
+
+}  // namespace nvfp4

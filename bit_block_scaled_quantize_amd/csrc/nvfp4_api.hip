@@ -389,6 +389,145 @@ nvfp4_status nvfp4_mx_gemm(const nvfp4_mx_tensor* A, const nvfp4_mx_tensor* B, v
     return e == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
 }
 
+// ---------------------------------------------------------------- RMS norm
+namespace {
+
+// A matrix argument of the row operators: any element alignment and stride.
+nvfp4_status check_matrix(const void* p, int64_t rows, int64_t cols, int64_t ld, int32_t dt) {
+    if (ld < cols) return NVFP4_ERR_SHAPE;
+    if (rows > 0 && !p) return NVFP4_ERR_NULL;
+    return aligned(p, dtype_size(dt)) ? NVFP4_OK : NVFP4_ERR_ALIGN;
+}
+
+}  // namespace
+
+nvfp4_status nvfp4_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight,
+                           int32_t w_dt /* nvfp4_dtype */, int32_t dt /* nvfp4_dtype */, int64_t rows, int64_t cols,
+                           float eps, void* h, int64_t ldh, void* y, int64_t ldy, nvfp4_mx_tensor* mx, float* rstd,
+                           void* stream) {
+    if (!valid_dtype(dt) || !valid_dtype(w_dt)) return NVFP4_ERR_ENUM;
+    if (mx && mx->elem != NVFP4_MX_E4M3 && mx->elem != NVFP4_MX_E2M1) return NVFP4_ERR_ENUM;
+    if (rows < 0 || cols < 1) return NVFP4_ERR_SHAPE;
+    if (!y && !mx) return NVFP4_ERR_NULL;
+    if (!weight) return NVFP4_ERR_NULL;
+    if (!aligned(weight, dtype_size(w_dt)) || !aligned(rstd, 4)) return NVFP4_ERR_ALIGN;
+    nvfp4_status st = check_matrix(x, rows, cols, ldx, dt);
+    if (st == NVFP4_OK && residual) st = check_matrix(residual, rows, cols, ldr, dt);
+    if (st == NVFP4_OK && h) st = check_matrix(h, rows, cols, ldh, dt);
+    if (st == NVFP4_OK && y) st = check_matrix(y, rows, cols, ldy, dt);
+    if (st != NVFP4_OK) return st;
+    if (mx) {
+        if (cols % 32 || mx->rows != rows || mx->cols != cols) return NVFP4_ERR_SHAPE;
+        if (rows > 0 && (!mx->codes || !mx->scales)) return NVFP4_ERR_NULL;
+        if (!aligned(mx->codes, 16)) return NVFP4_ERR_ALIGN;
+    }
+    if (!(eps > 0.0f) || cols > kMaxNormCols || rows > 0x7FFFFFFF) return NVFP4_ERR_UNSUPPORTED;
+    RmsNorm n = {x, residual, weight, dt == NVFP4_BF16, w_dt == NVFP4_BF16, rows, cols, ldx, ldr, ldh, ldy, eps, h, y,
+                 mx ? mx->codes : nullptr, mx ? mx->scales : nullptr,
+                 mx && mx->elem == NVFP4_MX_E2M1 ? kMxE2M1 : kMxE4M3, rstd};
+    return launch_rmsnorm(n, static_cast<hipStream_t>(stream)) == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
+}
+
+size_t nvfp4_rmsnorm_backward_workspace_size(int64_t rows, int64_t cols) {
+    if (rows < 0 || cols < 1 || cols > kMaxNormCols) return 0;
+    return (size_t)rmsnorm_backward_workspace_floats(rows, cols) * sizeof(float);
+}
+
+nvfp4_status nvfp4_rmsnorm_backward(const void* dy, int64_t lddy, const void* h, int64_t ldh, const float* rstd,
+                                    const void* weight, int32_t w_dt /* nvfp4_dtype */, const void* dh, int64_t lddh,
+                                    int32_t dt /* nvfp4_dtype */, int64_t rows, int64_t cols, void* dx, int64_t lddx,
+                                    float* dweight, void* ws, size_t ws_bytes, void* stream) {
+    if (!valid_dtype(dt) || !valid_dtype(w_dt)) return NVFP4_ERR_ENUM;
+    if (rows < 0 || cols < 1) return NVFP4_ERR_SHAPE;
+    if (!weight || !dweight || (rows > 0 && !rstd)) return NVFP4_ERR_NULL;
+    if (!aligned(weight, dtype_size(w_dt)) || !aligned(rstd, 4) || !aligned(dweight, 4)) return NVFP4_ERR_ALIGN;
+    nvfp4_status st = check_matrix(dy, rows, cols, lddy, dt);
+    if (st == NVFP4_OK) st = check_matrix(h, rows, cols, ldh, dt);
+    if (st == NVFP4_OK && dh) st = check_matrix(dh, rows, cols, lddh, dt);
+    if (st == NVFP4_OK) st = check_matrix(dx, rows, cols, lddx, dt);
+    if (st != NVFP4_OK) return st;
+    if (cols > kMaxNormCols || rows > 0x7FFFFFFF) return NVFP4_ERR_UNSUPPORTED;
+    if (rows > 0) {
+        if (!ws || ws_bytes < nvfp4_rmsnorm_backward_workspace_size(rows, cols)) return NVFP4_ERR_WORKSPACE;
+        if (!aligned(ws, 16)) return NVFP4_ERR_ALIGN;
+    }
+    RmsNormBackward n = {dy, h, dh, rstd, weight, dt == NVFP4_BF16, w_dt == NVFP4_BF16, rows, cols, lddy, ldh, lddh,
+                         lddx, dx, dweight, static_cast<float*>(ws)};
+    return launch_rmsnorm_backward(n, static_cast<hipStream_t>(stream)) == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
+}
+
+// ---------------------------------------------------------------- routing
+size_t nvfp4_route_workspace_size(int64_t tokens, int64_t experts) {
+    if (tokens < 0 || experts < 1 || experts > kMaxExperts) return 0;
+    return (size_t)route_workspace_ints(tokens, (int)experts) * sizeof(int32_t);
+}
+
+nvfp4_status nvfp4_route(const void* logits, int32_t dt /* nvfp4_dtype */, int64_t tokens, int64_t experts, int64_t ld,
+                         const nvfp4_route_opts* opts, int32_t* ids, float* weights, int64_t* offsets, int32_t* order,
+                         int32_t* position, void* ws, size_t ws_bytes, void* stream) {
+    if (!opts) return NVFP4_ERR_NULL;
+    if (!valid_dtype(dt)) return NVFP4_ERR_ENUM;
+    if (opts->score != NVFP4_ROUTE_SOFTMAX && opts->score != NVFP4_ROUTE_SIGMOID) return NVFP4_ERR_ENUM;
+    if (opts->group_score != NVFP4_GROUP_MAX && opts->group_score != NVFP4_GROUP_TOP2) return NVFP4_ERR_ENUM;
+    const int64_t G = opts->groups, k = opts->top_k;
+    if (tokens < 0 || experts < 1 || G < 1 || experts % G || opts->top_groups < 1 || opts->top_groups > G || k < 1 ||
+        k > opts->top_groups * (experts / G))
+        return NVFP4_ERR_SHAPE;
+    nvfp4_status st = check_matrix(logits, tokens, experts, ld, dt);
+    if (st != NVFP4_OK) return st;
+    if (tokens > 0 && (!ids || !weights)) return NVFP4_ERR_NULL;
+    if ((order || position) && !offsets) return NVFP4_ERR_NULL;
+    if (offsets && tokens > 0 && (!order || !position)) return NVFP4_ERR_NULL;
+    if (!aligned(ids, 4) || !aligned(weights, 4) || !aligned(offsets, 8) || !aligned(order, 4) ||
+        !aligned(position, 4) || !aligned(opts->bias, 4))
+        return NVFP4_ERR_ALIGN;
+    if (experts > kMaxExperts || k > kMaxTopK || !route_shape_fits((int)experts, (int)G) || tokens * k > 0x7FFFFFFF)
+        return NVFP4_ERR_UNSUPPORTED;
+    const size_t need = offsets ? nvfp4_route_workspace_size(tokens, experts) : 0;
+    if (need) {
+        if (!ws || ws_bytes < need) return NVFP4_ERR_WORKSPACE;
+        if (!aligned(ws, 16)) return NVFP4_ERR_ALIGN;
+    }
+    RouteArgs a;
+    a.logits = logits;
+    a.bf16 = dt == NVFP4_BF16;
+    a.tokens = tokens;
+    a.ld = ld;
+    a.bias = opts->bias;
+    a.shape = RouteShape{(int)experts, (int)G, (int)(experts / G), opts->top_groups, opts->top_k, 0,
+                         opts->group_score == NVFP4_GROUP_TOP2};
+    a.sigmoid = opts->score == NVFP4_ROUTE_SIGMOID;
+    a.renorm = opts->renorm != 0;
+    a.ids = ids;
+    a.weights = weights;
+    a.offsets = offsets;
+    a.order = order;
+    a.position = position;
+    a.counts = static_cast<int*>(ws);
+    a.span = 0;
+    return launch_route(a, static_cast<hipStream_t>(stream)) == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
+}
+
+nvfp4_status nvfp4_route_backward(const float* dweights, const void* logits, int32_t dt /* nvfp4_dtype */,
+                                  int64_t tokens, int64_t experts, int64_t ld, const int32_t* ids, int32_t top_k,
+                                  int32_t score /* nvfp4_route_score */, int32_t renorm, const float* dscores,
+                                  int64_t ldds, void* dlogits, int64_t lddl, void* stream) {
+    if (!valid_dtype(dt)) return NVFP4_ERR_ENUM;
+    if (score != NVFP4_ROUTE_SOFTMAX && score != NVFP4_ROUTE_SIGMOID) return NVFP4_ERR_ENUM;
+    if (tokens < 0 || experts < 1 || top_k < 1 || top_k > experts) return NVFP4_ERR_SHAPE;
+    nvfp4_status st = check_matrix(logits, tokens, experts, ld, dt);
+    if (st == NVFP4_OK && dscores) st = check_matrix(dscores, tokens, experts, ldds, NVFP4_F32);
+    if (st == NVFP4_OK) st = check_matrix(dlogits, tokens, experts, lddl, dt);
+    if (st != NVFP4_OK) return st;
+    if (tokens > 0 && (!dweights || !ids)) return NVFP4_ERR_NULL;
+    if (!aligned(dweights, 4) || !aligned(ids, 4)) return NVFP4_ERR_ALIGN;
+    if (experts > kMaxExperts || top_k > kMaxTopK || tokens > 0x7FFFFFFF) return NVFP4_ERR_UNSUPPORTED;
+    const RouteBackward a = {dweights, logits, ids, dscores, dlogits, tokens, ld, ldds, lddl, (int)experts, top_k,
+                             score == NVFP4_ROUTE_SIGMOID, renorm != 0};
+    return launch_route_backward(a, dt == NVFP4_BF16, static_cast<hipStream_t>(stream)) == hipSuccess ? NVFP4_OK
+                                                                                                     : NVFP4_ERR_HIP;
+}
+
 const char* nvfp4_status_string(int32_t s /* nvfp4_status */) {
     switch (s) {
         case NVFP4_OK: return "ok";

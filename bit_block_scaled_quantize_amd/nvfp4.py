@@ -25,11 +25,15 @@ NVFP4_EPI_NONE, NVFP4_EPI_SWIGLU = 0, 1
 NVFP4_SCALE_1D, NVFP4_SCALE_2D = 0, 1
 NVFP4_MX_E4M3, NVFP4_MX_E2M1 = 0, 1
 NVFP4_MX_ACC_NATIVE, NVFP4_MX_ACC_EXACT = 0, 1
+NVFP4_ROUTE_SOFTMAX, NVFP4_ROUTE_SIGMOID = 0, 1
+NVFP4_GROUP_MAX, NVFP4_GROUP_TOP2 = 0, 1
 
 EXPORTED = ["nvfp4_quantize_workspace_size", "nvfp4_quantize", "nvfp4_quantize_noalloc", "nvfp4_requantize",
             "nvfp4_dequantize",
             "nvfp4_gemm", "nvfp4_gemm_workspace_size", "nvfp4_grouped_gemm", "nvfp4_mx_quantize", "nvfp4_mx_dequantize", "nvfp4_mx_gemm",
             "nvfp4_mx_gemm_workspace_size",
+            "nvfp4_rmsnorm", "nvfp4_rmsnorm_backward", "nvfp4_rmsnorm_backward_workspace_size",
+            "nvfp4_route", "nvfp4_route_workspace_size", "nvfp4_route_backward",
             "nvfp4_status_string", "nvfp4_version"]
 
 
@@ -48,6 +52,12 @@ class CQuantOpts(ctypes.Structure):
     _fields_ = [("layout", ctypes.c_int32), ("round", ctypes.c_int32), ("sr_seed", ctypes.c_uint64),
                 ("hadamard", ctypes.c_int32), ("hadamard_seed", ctypes.c_uint64),
                 ("amax_in", ctypes.c_void_p), ("amax_out", ctypes.c_void_p)]
+
+
+class CRouteOpts(ctypes.Structure):
+    _fields_ = [("top_k", ctypes.c_int32), ("score", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32), ("group_score", ctypes.c_int32), ("renorm", ctypes.c_int32),
+                ("bias", ctypes.c_void_p)]
 
 
 def _load():
@@ -85,6 +95,19 @@ def _load():
     L.nvfp4_mx_gemm.restype = i32
     L.nvfp4_mx_gemm_workspace_size.argtypes = [ctypes.POINTER(CMXTensor), ctypes.POINTER(CMXTensor), i32, i32]
     L.nvfp4_mx_gemm_workspace_size.restype = sz
+    L.nvfp4_rmsnorm.argtypes = [vp, i64, vp, i64, vp, i32, i32, i64, i64, ctypes.c_float, vp, i64, vp, i64,
+                                ctypes.POINTER(CMXTensor), vp, vp]
+    L.nvfp4_rmsnorm.restype = i32
+    L.nvfp4_rmsnorm_backward_workspace_size.argtypes = [i64, i64]
+    L.nvfp4_rmsnorm_backward_workspace_size.restype = sz
+    L.nvfp4_rmsnorm_backward.argtypes = [vp, i64, vp, i64, vp, vp, i32, vp, i64, i32, i64, i64, vp, i64, vp, vp, sz, vp]
+    L.nvfp4_rmsnorm_backward.restype = i32
+    L.nvfp4_route_workspace_size.argtypes = [i64, i64]
+    L.nvfp4_route_workspace_size.restype = sz
+    L.nvfp4_route.argtypes = [vp, i32, i64, i64, i64, ctypes.POINTER(CRouteOpts), vp, vp, vp, vp, vp, vp, sz, vp]
+    L.nvfp4_route.restype = i32
+    L.nvfp4_route_backward.argtypes = [vp, vp, i32, i64, i64, i64, vp, i32, i32, i32, vp, i64, vp, i64, vp]
+    L.nvfp4_route_backward.restype = i32
     L.nvfp4_status_string.argtypes = [i32]
     L.nvfp4_status_string.restype = ctypes.c_char_p
     L.nvfp4_version.argtypes = []
@@ -130,6 +153,8 @@ def _launches_on_stream(fn):
     stream, so that everything it allocates belongs to that stream."""
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
         with _on(stream):
             return fn(*args, stream=stream, **kw)
     return call
@@ -413,4 +438,211 @@ def nvfp4_mx_gemm(A, B, out_dtype=torch.float32, out=None, accum=NVFP4_MX_ACC_NA
     st = lib.nvfp4_mx_gemm(ctypes.byref(ca), ctypes.byref(cb), ctypes.c_void_p(out.data_ptr()),
                            _dtype_code(out.dtype), ldc, accum, _ptr(workspace), ws_bytes, _stream(stream))
     _check("nvfp4_mx_gemm", st)
+    return out
+
+
+# ---------------------------------------------------------------- MoE-block operators
+def _launch_stream(t, stream):
+    """Raw handle of the stream a call on the tensors of t's device runs on."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors must be on the current GPU, got {t.device}")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _matrix(name, t, rows=None, cols=None, dtype=None, like=None):
+    """Leading dimension of a 2-D tensor with unit column stride, checked."""
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError(f"{name} must be a matrix with unit column stride")
+    r, c = t.shape
+    if (rows is not None and r != rows) or (cols is not None and c != cols):
+        raise ValueError(f"{name} is {r} x {c}, expected {rows} x {cols}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if like is not None and t.get_device() != like.get_device():
+        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    return t.stride(0) if r > 1 else max(c, t.stride(0))
+
+
+def _flat(name, t, numel, dtype, like):
+    """Address of a contiguous tensor of numel elements, checked."""
+    if t.numel() != numel or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with {numel} elements")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.get_device() != like.get_device():
+        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    return t.data_ptr()
+
+
+@dataclass
+class RMSNormOutput:
+    """h (the sum with the residual; x itself without one), y, mx (MXTensor)
+    and rstd, each None when not asked for."""
+    h: torch.Tensor
+    y: torch.Tensor = None
+    mx: MXTensor = None
+    rstd: torch.Tensor = None
+
+
+@_launches_on_stream
+def nvfp4_rmsnorm(x, weight, residual=None, eps=1e-6, y=True, mx_elem=None, rstd=False, out=None, stream=None):
+    """RMS norm of h = x + residual (rows x cols, float32 or bfloat16): y =
+    h / sqrt(mean(h^2) + eps) * weight as a tensor of x's dtype (y=True), as
+    an MXTensor (mx_elem=NVFP4_MX_E4M3 or NVFP4_MX_E2M1), or both; rstd=True
+    returns 1 / sqrt(mean(h^2) + eps) per row for the backward pass.  out: an
+    RMSNormOutput of preallocated tensors for what is asked for (out.h may be
+    residual or x)."""
+    ldx = _matrix("x", x)
+    rows, cols = x.shape
+    dt = x.dtype
+    code = _dtype_code(dt)
+    w = _flat("weight", weight, cols, weight.dtype, x)
+    ldr = 0 if residual is None else _matrix("residual", residual, rows, cols, dt, x)
+    if out is None:
+        out = RMSNormOutput(x if residual is None else torch.empty((rows, cols), dtype=dt, device=x.device),
+                            torch.empty((rows, cols), dtype=dt, device=x.device) if y else None,
+                            None if mx_elem is None else MXTensor.empty(rows, cols, mx_elem, x.device),
+                            torch.empty((rows,), dtype=torch.float32, device=x.device) if rstd else None)
+    else:
+        out = RMSNormOutput(out.h if residual is not None else x, out.y if y else None,
+                            None if mx_elem is None else out.mx, out.rstd if rstd else None)
+    h = None if out.h is x and residual is None else out.h
+    ldh = 0 if h is None else _matrix("out.h", h, rows, cols, dt, x)
+    ldy = 0 if out.y is None else _matrix("out.y", out.y, rows, cols, dt, x)
+    mx = None
+    if out.mx is not None:
+        if out.mx.elem != mx_elem:
+            raise ValueError("out.mx has another element format than mx_elem")
+        _flat("out.mx.codes", out.mx.codes, rows * cols // (1 if mx_elem == NVFP4_MX_E4M3 else 2), torch.uint8, x)
+        _flat("out.mx.scales", out.mx.scales, rows * (cols // 32), torch.uint8, x)
+        mx = ctypes.byref(out.mx.c())
+    st = lib.nvfp4_rmsnorm(
+        x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr, w, _dtype_code(weight.dtype), code,
+        rows, cols, eps, None if h is None else h.data_ptr(), ldh, None if out.y is None else out.y.data_ptr(), ldy, mx,
+        None if out.rstd is None else _flat("out.rstd", out.rstd, rows, torch.float32, x), _launch_stream(x, stream))
+    _check("nvfp4_rmsnorm", st)
+    return out
+
+
+@_launches_on_stream
+def nvfp4_rmsnorm_backward(dy, h, rstd, weight, dh=None, dx=None, dweight=None, workspace=None, stream=None):
+    """(dx, dweight) of nvfp4_rmsnorm from the h and rstd it gave: dx (h's
+    dtype) is the gradient of x and of residual alike, dh (optional) the
+    gradient that reaches h by the residual stream, dweight float32.  dx,
+    dweight and workspace (nvfp4_rmsnorm_backward_workspace_size) may be
+    preallocated."""
+    ldh = _matrix("h", h)
+    rows, cols = h.shape
+    dt = h.dtype
+    code = _dtype_code(dt)
+    lddy = _matrix("dy", dy, rows, cols, dt, h)
+    r = _flat("rstd", rstd, rows, torch.float32, h)
+    w = _flat("weight", weight, cols, weight.dtype, h)
+    lddh = 0 if dh is None else _matrix("dh", dh, rows, cols, dt, h)
+    if dx is None:
+        dx = torch.empty((rows, cols), dtype=dt, device=h.device)
+    lddx = _matrix("dx", dx, rows, cols, dt, h)
+    if dweight is None:
+        dweight = torch.empty((cols,), dtype=torch.float32, device=h.device)
+    dwp = _flat("dweight", dweight, cols, torch.float32, h)
+    if workspace is None:
+        need = lib.nvfp4_rmsnorm_backward_workspace_size(rows, cols)
+        workspace = torch.empty(need // 4, dtype=torch.float32, device=h.device)
+    st = lib.nvfp4_rmsnorm_backward(
+        dy.data_ptr(), lddy, h.data_ptr(), ldh, r, w, _dtype_code(weight.dtype), None if dh is None else dh.data_ptr(),
+        lddh, code, rows, cols, dx.data_ptr(), lddx, dwp, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _launch_stream(h, stream))
+    _check("nvfp4_rmsnorm_backward", st)
+    return dx, dweight
+
+
+def nvfp4_rmsnorm_backward_workspace_size(rows, cols):
+    """Bytes of workspace of nvfp4_rmsnorm_backward."""
+    return int(lib.nvfp4_rmsnorm_backward_workspace_size(rows, cols))
+
+
+@dataclass
+class RouteOutput:
+    """ids int32 and weights float32 [tokens, top_k]; with the dispatch plan
+    offsets int64 [experts + 1], order and position int32 [tokens * top_k]."""
+    ids: torch.Tensor
+    weights: torch.Tensor
+    offsets: torch.Tensor = None
+    order: torch.Tensor = None
+    position: torch.Tensor = None
+
+
+def nvfp4_route_workspace_size(tokens, experts):
+    """Bytes of workspace of nvfp4_route with the dispatch plan."""
+    return int(lib.nvfp4_route_workspace_size(tokens, experts))
+
+
+@_launches_on_stream
+def nvfp4_route(logits, top_k, bias=None, score=NVFP4_ROUTE_SOFTMAX, groups=1, top_groups=1,
+                group_score=NVFP4_GROUP_TOP2, renorm=True, plan=True, out=None, workspace=None, stream=None):
+    """Route tokens to experts by their logits (tokens x experts, float32 or
+    bfloat16): the top_k experts of the largest score + bias (bias float32
+    [experts]) within the top_groups groups of the largest group score, and
+    their weights.  plan=True also sorts the tokens * top_k assignments by
+    expert (offsets feed nvfp4_grouped_gemm; order // top_k are the tokens to
+    gather).  out: a RouteOutput of preallocated tensors."""
+    ld = _matrix("logits", logits)
+    tokens, experts = logits.shape
+    code = _dtype_code(logits.dtype)
+    dev = logits.device
+    n = tokens * top_k
+    if out is None:
+        i32 = torch.int32
+        out = RouteOutput(torch.empty((tokens, top_k), dtype=i32, device=dev),
+                          torch.empty((tokens, top_k), dtype=torch.float32, device=dev))
+        if plan:
+            out.offsets = torch.empty((experts + 1,), dtype=torch.int64, device=dev)
+            out.order = torch.empty((n,), dtype=i32, device=dev)
+            out.position = torch.empty((n,), dtype=i32, device=dev)
+        pi, pw = out.ids.data_ptr(), out.weights.data_ptr()
+        pf, po, pp = (out.offsets.data_ptr(), out.order.data_ptr(), out.position.data_ptr()) if plan else (None,) * 3
+    else:
+        pi = _flat("out.ids", out.ids, n, torch.int32, logits)
+        pw = _flat("out.weights", out.weights, n, torch.float32, logits)
+        pf = po = pp = None
+        if plan:
+            pf = _flat("out.offsets", out.offsets, experts + 1, torch.int64, logits)
+            po = _flat("out.order", out.order, n, torch.int32, logits)
+            pp = _flat("out.position", out.position, n, torch.int32, logits)
+    b = None if bias is None else _flat("bias", bias, experts, torch.float32, logits)
+    if workspace is None and plan:
+        need = lib.nvfp4_route_workspace_size(tokens, experts)
+        workspace = torch.empty(need // 4, dtype=torch.int32, device=dev) if need else None
+    opts = CRouteOpts(top_k, score, groups, top_groups, group_score, 1 if renorm else 0, b)
+    st = lib.nvfp4_route(
+        logits.data_ptr(), code, tokens, experts, ld, ctypes.byref(opts), pi, pw, pf, po, pp,
+        None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _launch_stream(logits, stream))
+    _check("nvfp4_route", st)
+    return out
+
+
+@_launches_on_stream
+def nvfp4_route_backward(dweights, logits, ids, score=NVFP4_ROUTE_SOFTMAX, renorm=True, dscores=None, out=None,
+                         stream=None):
+    """Gradient of the logits from that of the chosen weights (float32
+    [tokens, top_k]) and, optionally, of all scores (dscores float32 [tokens,
+    experts], as of an auxiliary balance loss)."""
+    ld = _matrix("logits", logits)
+    tokens, experts = logits.shape
+    if ids.dim() != 2:
+        raise ValueError("ids must be tokens x top_k")
+    top_k = ids.shape[1]
+    code = _dtype_code(logits.dtype)
+    pi = _flat("ids", ids, tokens * top_k, torch.int32, logits)
+    pw = _flat("dweights", dweights, tokens * top_k, torch.float32, logits)
+    ldds = 0 if dscores is None else _matrix("dscores", dscores, tokens, experts, torch.float32, logits)
+    if out is None:
+        out = torch.empty((tokens, experts), dtype=logits.dtype, device=logits.device)
+    lddl = _matrix("out", out, tokens, experts, logits.dtype, logits)
+    st = lib.nvfp4_route_backward(
+        pw, logits.data_ptr(), code, tokens, experts, ld, pi, top_k, score, 1 if renorm else 0,
+        None if dscores is None else dscores.data_ptr(), ldds, out.data_ptr(), lddl, _launch_stream(logits, stream))
+    _check("nvfp4_route_backward", st)
     return out

@@ -365,6 +365,105 @@ nvfp4_status nvfp4_mx_gemm(const nvfp4_mx_tensor* A, const nvfp4_mx_tensor* B, v
 size_t nvfp4_mx_gemm_workspace_size(const nvfp4_mx_tensor* A, const nvfp4_mx_tensor* B, int32_t c_dt /* nvfp4_dtype */,
                                     int32_t accum);
 
+/* ------------------------------------------------------------------------
+ * Operators of a mixture-of-experts block around the quantized products: the
+ * norm that feeds them, the routing that plans them and the products of a few
+ * tokens.  Matrices of these operators (x, residual, h, y, logits and their
+ * gradients) need only their element's alignment and a leading dimension >=
+ * cols; sums are binary32 in a fixed order, so results repeat bit for bit.
+ * ---------------------------------------------------------------------- */
+
+/* RMS norm with the residual's addition.  Per row:
+ *   h = x + residual, rounded to dt (residual NULL: h = x);
+ *   rstd = 1 / sqrt(sum h^2 / cols + eps), binary32;
+ *   y = (h * rstd) * weight, binary32.
+ * Outputs, each optional (NULL) but one of y and mx: h (rows x cols, dt; may
+ * be x or residual itself, same leading dimension), y rounded to dt, mx the
+ * ROW_1D nearest-even MX quantization of the binary32 y (mx->elem selects the
+ * element), rstd (rows floats, what the backward pass reads).
+ * weight: cols elements of dtype w_dt.  Requirements: cols >= 1, for mx
+ * cols % 32 == 0, mx->rows/cols = rows/cols and codes 16-byte aligned;
+ * eps > 0, cols <= 32768 and rows < 2^31 (else UNSUPPORTED); the squares of a
+ * row must sum within binary32's range.  rows == 0 is a no-op. */
+nvfp4_status nvfp4_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight,
+                           int32_t w_dt /* nvfp4_dtype */, int32_t dt /* nvfp4_dtype */, int64_t rows, int64_t cols,
+                           float eps, void* h, int64_t ldh, void* y, int64_t ldy, nvfp4_mx_tensor* mx, float* rstd,
+                           void* stream);
+
+/* Bytes of workspace nvfp4_rmsnorm_backward needs (partial sums of dweight;
+ * 0 for no rows and for invalid sizes). */
+size_t nvfp4_rmsnorm_backward_workspace_size(int64_t rows, int64_t cols);
+
+/* Backward of nvfp4_rmsnorm from the h and rstd it gave: with g = dy * weight
+ * and xhat = h * rstd,
+ *   dx = rstd * (g - xhat * mean(g * xhat)) + dh   (rounded to dt; it is the
+ *        gradient of x and of residual alike; dh, the gradient that reaches h
+ *        by the residual stream, may be NULL),
+ *   dweight = sum over rows of dy * xhat           (cols floats).
+ * dy, h, dh and dx have dtype dt; dx may be dy, h or dh itself (same leading
+ * dimension).  rows == 0 writes zeros to dweight.  ws 16-byte aligned. */
+nvfp4_status nvfp4_rmsnorm_backward(const void* dy, int64_t lddy, const void* h, int64_t ldh, const float* rstd,
+                                    const void* weight, int32_t w_dt /* nvfp4_dtype */, const void* dh, int64_t lddh,
+                                    int32_t dt /* nvfp4_dtype */, int64_t rows, int64_t cols, void* dx, int64_t lddx,
+                                    float* dweight, void* ws, size_t ws_bytes, void* stream);
+
+typedef enum { NVFP4_ROUTE_SOFTMAX = 0, NVFP4_ROUTE_SIGMOID = 1 } nvfp4_route_score;
+typedef enum { NVFP4_GROUP_MAX = 0, NVFP4_GROUP_TOP2 = 1 } nvfp4_group_score;
+
+typedef struct {
+    int32_t top_k;       /* experts per token */
+    int32_t score;       /* nvfp4_route_score */
+    int32_t groups;      /* the experts, in order, form this many equal groups (1: none) */
+    int32_t top_groups;  /* groups that stay eligible */
+    int32_t group_score; /* nvfp4_group_score: a group's best selection score, or the sum of its best two */
+    int32_t renorm;      /* nonzero: divide the chosen scores by their sum */
+    const float* bias;   /* nullable DEVICE pointer: one float per expert, added for the choice only */
+} nvfp4_route_opts;
+
+/* Bytes of workspace nvfp4_route needs when it makes the dispatch plan (0 for
+ * few tokens and for invalid sizes). */
+size_t nvfp4_route_workspace_size(int64_t tokens, int64_t experts);
+
+/* Route tokens to experts.  Per row l of logits (tokens x experts, dtype dt,
+ * row stride ld): scores p (softmax of the row, or the sigmoid of each);
+ * selection scores s = p + bias; the top_groups groups of the largest group
+ * score stay, and the top_k experts of the largest s among them are chosen, in
+ * that order; ties of scores go to the lower index, and scores are compared as
+ * binary64 evaluation of these formulas orders them.
+ *   ids      tokens x top_k: the chosen experts;
+ *   weights  tokens x top_k floats: their p, divided by their sum with renorm.
+ * The dispatch plan (offsets, order and position all given, or all NULL),
+ * over the assignments i = token * top_k + place:
+ *   offsets  int64[experts + 1]: first sorted place of each expert (what
+ *            nvfp4_grouped_gemm takes);
+ *   order    int32[tokens * top_k]: the assignment at each sorted place, by
+ *            expert and, within one, in assignment order;
+ *   position int32[tokens * top_k]: the sorted place of each assignment.
+ * A logit of NaN or -inf counts as the lowest finite value (weight 0 beside
+ * any other) and +inf as the largest, so that a row that is masked throughout
+ * chooses its first experts with equal weights; a bias of NaN or -inf puts
+ * its expert last.
+ * Requirements: experts % groups == 0, 1 <= top_groups <= groups,
+ * 1 <= top_k <= top_groups * experts / groups (else SHAPE); experts <= 2048,
+ * top_k <= 16, groups <= 64, experts of a group at most 32 for each of the
+ * 64 / (groups rounded up to a power of two) lanes it gets,
+ * tokens * top_k < 2^31 (else UNSUPPORTED).  tokens == 0 writes zero offsets. */
+nvfp4_status nvfp4_route(const void* logits, int32_t dt /* nvfp4_dtype */, int64_t tokens, int64_t experts, int64_t ld,
+                         const nvfp4_route_opts* opts, int32_t* ids, float* weights, int64_t* offsets, int32_t* order,
+                         int32_t* position, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of the logits (tokens x experts, dtype dt) from those of the
+ * chosen weights (dweights, tokens x top_k floats; ids as nvfp4_route gave
+ * them: distinct within a row, an index out of range counts as none) and,
+ * with dscores (nullable, tokens x experts floats, row stride ldds), of all
+ * scores p, as an auxiliary balance loss has one.  The choice itself has no
+ * gradient.  dlogits may be logits itself (same leading dimension).
+ * Limits as for nvfp4_route.  tokens == 0 is a no-op. */
+nvfp4_status nvfp4_route_backward(const float* dweights, const void* logits, int32_t dt /* nvfp4_dtype */,
+                                  int64_t tokens, int64_t experts, int64_t ld, const int32_t* ids, int32_t top_k,
+                                  int32_t score /* nvfp4_route_score */, int32_t renorm, const float* dscores,
+                                  int64_t ldds, void* dlogits, int64_t lddl, void* stream);
+
 /* Static description of a status code. */
 const char* nvfp4_status_string(int32_t s /* nvfp4_status */);
 
