@@ -14,4 +14,5 @@ from .nvfp4 import (  # noqa: F401
     NVFP4_ROUTE_SOFTMAX, NVFP4_ROUTE_SIGMOID, NVFP4_GROUP_MAX, NVFP4_GROUP_TOP2,
     RMSNormOutput, nvfp4_rmsnorm, nvfp4_rmsnorm_backward, nvfp4_rmsnorm_backward_workspace_size,
     RouteOutput, nvfp4_route, nvfp4_route_workspace_size, nvfp4_route_backward,
+    nvfp4_gemv, nvfp4_mx_gemv, nvfp4_expert_gemv, nvfp4_expert_gemv_workspace_size,
 )

@@ -170,4 +170,28 @@ struct RouteBackward {
 };
 hipError_t launch_route_backward(const RouteBackward& a, bool bf16, hipStream_t s);
 
+// Products of a few rows with 4-bit weights (see nvfp4_gemv, nvfp4_mx_gemv and
+// nvfp4_expert_gemv).
+constexpr int64_t kMaxGemvRows = 1024;
+constexpr int kMaxGemvAssignments = 1024;
+struct GemvArgs {
+    const void* x;
+    int64_t m, ldx;
+    const uint8_t* codes;
+    const uint8_t* scales;
+    const float* ts;  // NULL: 1
+    int64_t N, K;     // one matrix
+    void* y;
+    int64_t ldy;
+    // the routed form (ids NULL: none): assignment i = token * top_k + place
+    const int* ids;
+    int assignments, top_k, experts;
+    bool x_per_assignment;
+    bool x_bf16, y_bf16, scale_2d, mx;
+};
+hipError_t launch_gemv(const GemvArgs& p, bool swiglu, hipStream_t s);
+// weights NULL: a row of y for each assignment; else their weighted sums, by
+// way of ws (assignments x output columns floats).
+hipError_t launch_expert_gemv(GemvArgs p, bool swiglu, const float* weights, float* ws, hipStream_t s);
+
 }  // namespace nvfp4

@@ -528,6 +528,98 @@ nvfp4_status nvfp4_route_backward(const float* dweights, const void* logits, int
                                                                                                      : NVFP4_ERR_HIP;
 }
 
+// ---------------------------------------------------------------- products of a few rows
+namespace {
+
+// Arguments that nvfp4_gemv and its MX and routed forms share: the output
+// columns of one matrix of N rows, x and y.
+nvfp4_status check_gemv(const void* x, int32_t dt, int64_t x_rows, int64_t ldx, int64_t N, int64_t K, const void* y,
+                        int32_t y_dt, int64_t y_rows, int64_t ldy, int32_t ep) {
+    const bool swiglu = ep == NVFP4_EPI_SWIGLU;
+    if (swiglu && (N % 2 || (N / 2) % 16)) return NVFP4_ERR_SHAPE;
+    if (x_rows < 0) return NVFP4_ERR_SHAPE;
+    const int64_t outs = swiglu ? N / 2 : N;
+    nvfp4_status st = check_matrix(x, K > 0 ? x_rows : 0, K, ldx, dt);
+    if (st == NVFP4_OK) st = check_matrix(y, outs > 0 ? y_rows : 0, outs, ldy, y_dt);
+    if (st != NVFP4_OK) return st;
+    if (cdiv(N, 16) > 0x7FFFFFFF) return NVFP4_ERR_UNSUPPORTED;
+    return NVFP4_OK;
+}
+
+}  // namespace
+
+nvfp4_status nvfp4_gemv(const void* x, int32_t dt /* nvfp4_dtype */, int64_t m, int64_t ldx, const nvfp4_tensor* W,
+                        void* y, int32_t y_dt /* nvfp4_dtype */, int64_t ldy, int32_t ep /* nvfp4_epilogue */,
+                        void* stream) {
+    if (!W) return NVFP4_ERR_NULL;
+    if (!valid_dtype(dt) || !valid_dtype(y_dt)) return NVFP4_ERR_ENUM;
+    if (ep != NVFP4_EPI_NONE && ep != NVFP4_EPI_SWIGLU) return NVFP4_ERR_ENUM;
+    nvfp4_status st = check_operand(W);
+    if (st == NVFP4_OK) st = check_gemv(x, dt, m, ldx, W->rows, W->cols, y, y_dt, m, ldy, ep);
+    if (st != NVFP4_OK) return st;
+    if (m > kMaxGemvRows) return NVFP4_ERR_UNSUPPORTED;
+    GemvArgs p = {x, m, ldx, W->codes, W->scales, W->tensor_scale, W->rows, W->cols, y, ldy, nullptr, 0, 1, 0, false,
+                  dt == NVFP4_BF16, y_dt == NVFP4_BF16, W->scale_mode == NVFP4_SCALE_2D, false};
+    const hipError_t e = launch_gemv(p, ep == NVFP4_EPI_SWIGLU, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
+}
+
+nvfp4_status nvfp4_mx_gemv(const void* x, int32_t dt /* nvfp4_dtype */, int64_t m, int64_t ldx,
+                           const nvfp4_mx_tensor* W, void* y, int32_t y_dt /* nvfp4_dtype */, int64_t ldy,
+                           void* stream) {
+    if (!W) return NVFP4_ERR_NULL;
+    if (!valid_dtype(dt) || !valid_dtype(y_dt)) return NVFP4_ERR_ENUM;
+    if (W->elem != NVFP4_MX_E4M3 && W->elem != NVFP4_MX_E2M1) return NVFP4_ERR_ENUM;
+    if (W->rows < 0 || W->cols < 0 || W->cols % 32) return NVFP4_ERR_SHAPE;
+    if (W->rows > 0 && W->cols > 0 && (!W->codes || !W->scales)) return NVFP4_ERR_NULL;
+    if (!aligned(W->codes, 16)) return NVFP4_ERR_ALIGN;
+    const nvfp4_status st = check_gemv(x, dt, m, ldx, W->rows, W->cols, y, y_dt, m, ldy, NVFP4_EPI_NONE);
+    if (st != NVFP4_OK) return st;
+    if (W->elem != NVFP4_MX_E2M1 || m > kMaxGemvRows) return NVFP4_ERR_UNSUPPORTED;
+    GemvArgs p = {x, m, ldx, W->codes, W->scales, nullptr, W->rows, W->cols, y, ldy, nullptr, 0, 1, 0, false,
+                  dt == NVFP4_BF16, y_dt == NVFP4_BF16, false, true};
+    const hipError_t e = launch_gemv(p, false, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
+}
+
+size_t nvfp4_expert_gemv_workspace_size(int64_t tokens, int32_t top_k, int64_t n) {
+    if (tokens < 0 || top_k < 1 || n < 0 || tokens > kMaxGemvAssignments / top_k) return 0;
+    if (n > (int64_t)1 << 40) return 0;
+    return (size_t)(tokens * top_k * n) * sizeof(float);
+}
+
+nvfp4_status nvfp4_expert_gemv(const void* x, int32_t dt /* nvfp4_dtype */, int64_t x_rows, int64_t ldx,
+                               const int32_t* ids, int64_t tokens, int32_t top_k, const nvfp4_tensor* W,
+                               int32_t experts, const float* weights, void* y, int32_t y_dt /* nvfp4_dtype */,
+                               int64_t ldy, int32_t ep /* nvfp4_epilogue */, void* ws, size_t ws_bytes, void* stream) {
+    if (!W) return NVFP4_ERR_NULL;
+    if (!valid_dtype(dt) || !valid_dtype(y_dt)) return NVFP4_ERR_ENUM;
+    if (ep != NVFP4_EPI_NONE && ep != NVFP4_EPI_SWIGLU) return NVFP4_ERR_ENUM;
+    if (experts < 1 || tokens < 0 || top_k < 1) return NVFP4_ERR_SHAPE;
+    nvfp4_status st = check_operand(W);
+    if (st != NVFP4_OK) return st;
+    if (W->rows % experts) return NVFP4_ERR_SHAPE;
+    const int64_t N = W->rows / experts;
+    if (W->scale_mode == NVFP4_SCALE_2D && N % 16) return NVFP4_ERR_SHAPE;
+    if (tokens > kMaxGemvAssignments / top_k) return NVFP4_ERR_UNSUPPORTED;
+    const int64_t assignments = tokens * top_k;
+    if (x_rows != tokens && x_rows != assignments) return NVFP4_ERR_SHAPE;
+    st = check_gemv(x, dt, x_rows, ldx, N, W->cols, y, y_dt, weights ? tokens : assignments, ldy, ep);
+    if (st != NVFP4_OK) return st;
+    if (tokens > 0 && !ids) return NVFP4_ERR_NULL;
+    if (!aligned(ids, 4) || !aligned(weights, 4)) return NVFP4_ERR_ALIGN;
+    const size_t need = weights ? nvfp4_expert_gemv_workspace_size(tokens, top_k, ep == NVFP4_EPI_SWIGLU ? N / 2 : N) : 0;
+    if (need) {
+        if (!ws || ws_bytes < need) return NVFP4_ERR_WORKSPACE;
+        if (!aligned(ws, 16)) return NVFP4_ERR_ALIGN;
+    }
+    GemvArgs p = {x, x_rows, ldx, W->codes, W->scales, W->tensor_scale, N, W->cols, y, ldy, ids, (int)assignments, top_k,
+                  experts, x_rows != tokens, dt == NVFP4_BF16, y_dt == NVFP4_BF16, W->scale_mode == NVFP4_SCALE_2D, false};
+    const hipError_t e = launch_expert_gemv(p, ep == NVFP4_EPI_SWIGLU, weights, static_cast<float*>(ws),
+                                            static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
+}
+
 const char* nvfp4_status_string(int32_t s /* nvfp4_status */) {
     switch (s) {
         case NVFP4_OK: return "ok";

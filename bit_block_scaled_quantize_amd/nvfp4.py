@@ -34,6 +34,7 @@ EXPORTED = ["nvfp4_quantize_workspace_size", "nvfp4_quantize", "nvfp4_quantize_n
             "nvfp4_mx_gemm_workspace_size",
             "nvfp4_rmsnorm", "nvfp4_rmsnorm_backward", "nvfp4_rmsnorm_backward_workspace_size",
             "nvfp4_route", "nvfp4_route_workspace_size", "nvfp4_route_backward",
+            "nvfp4_gemv", "nvfp4_mx_gemv", "nvfp4_expert_gemv", "nvfp4_expert_gemv_workspace_size",
             "nvfp4_status_string", "nvfp4_version"]
 
 
@@ -108,6 +109,15 @@ def _load():
     L.nvfp4_route.restype = i32
     L.nvfp4_route_backward.argtypes = [vp, vp, i32, i64, i64, i64, vp, i32, i32, i32, vp, i64, vp, i64, vp]
     L.nvfp4_route_backward.restype = i32
+    L.nvfp4_gemv.argtypes = [vp, i32, i64, i64, ctypes.POINTER(CTensor), vp, i32, i64, i32, vp]
+    L.nvfp4_gemv.restype = i32
+    L.nvfp4_mx_gemv.argtypes = [vp, i32, i64, i64, ctypes.POINTER(CMXTensor), vp, i32, i64, vp]
+    L.nvfp4_mx_gemv.restype = i32
+    L.nvfp4_expert_gemv_workspace_size.argtypes = [i64, i32, i64]
+    L.nvfp4_expert_gemv_workspace_size.restype = sz
+    L.nvfp4_expert_gemv.argtypes = [vp, i32, i64, i64, vp, i64, i32, ctypes.POINTER(CTensor), i32, vp, vp, i32, i64, i32,
+                                    vp, sz, vp]
+    L.nvfp4_expert_gemv.restype = i32
     L.nvfp4_status_string.argtypes = [i32]
     L.nvfp4_status_string.restype = ctypes.c_char_p
     L.nvfp4_version.argtypes = []
@@ -645,4 +655,91 @@ def nvfp4_route_backward(dweights, logits, ids, score=NVFP4_ROUTE_SOFTMAX, renor
         pw, logits.data_ptr(), code, tokens, experts, ld, pi, top_k, score, 1 if renorm else 0,
         None if dscores is None else dscores.data_ptr(), ldds, out.data_ptr(), lddl, _launch_stream(logits, stream))
     _check("nvfp4_route_backward", st)
+    return out
+
+
+def _weight(w, like, n_scales=1):
+    """C form of a 4-bit weight (NVFP4Tensor or MXTensor), its arrays checked."""
+    rows, cols = w.rows, w.cols
+    if isinstance(w, MXTensor):
+        if w.elem != NVFP4_MX_E2M1:
+            raise ValueError("the weight must have E2M1 elements")
+        ns = rows * (cols // 32)
+    else:
+        ns = (rows // 16 if w.scale_mode == NVFP4_SCALE_2D else rows) * (cols // 16)
+        _flat("tensor_scale", w.tensor_scale, n_scales, torch.float32, like)
+    _flat("codes", w.codes, rows * (cols // 2), torch.uint8, like)
+    _flat("scales", w.scales, ns, torch.uint8, like)
+    return w.c()
+
+
+def _gemv_out(out, rows, cols, dtype, x):
+    if out is None:
+        return torch.empty((rows, cols), dtype=x.dtype if dtype is None else dtype, device=x.device)
+    _matrix("out", out, rows, cols, None, x)
+    return out
+
+
+@_launches_on_stream
+def nvfp4_gemv(x, w, epilogue=NVFP4_EPI_NONE, out_dtype=None, out=None, stream=None):
+    """x W^T of a few rows x (m x K, bfloat16 or float32, not quantized) and an
+    NVFP4Tensor w (N x K): m x N in out_dtype (x's unless given); with
+    NVFP4_EPI_SWIGLU (N = 2F) gate * sigmoid(gate) * up, m x F."""
+    ldx = _matrix("x", x, x.shape[0], w.cols)
+    m = x.shape[0]
+    c = _weight(w, x)
+    out = _gemv_out(out, m, w.rows // 2 if epilogue == NVFP4_EPI_SWIGLU else w.rows, out_dtype, x)
+    st = lib.nvfp4_gemv(x.data_ptr(), _dtype_code(x.dtype), m, ldx, ctypes.byref(c), out.data_ptr(),
+                        _dtype_code(out.dtype), _matrix("out", out), epilogue, _launch_stream(x, stream))
+    _check("nvfp4_gemv", st)
+    return out
+
+
+@_launches_on_stream
+def nvfp4_mx_gemv(x, w, out_dtype=None, out=None, stream=None):
+    """nvfp4_gemv for an MXFP4 weight (MXTensor with E2M1 elements)."""
+    ldx = _matrix("x", x, x.shape[0], w.cols)
+    m = x.shape[0]
+    c = _weight(w, x)
+    out = _gemv_out(out, m, w.rows, out_dtype, x)
+    st = lib.nvfp4_mx_gemv(x.data_ptr(), _dtype_code(x.dtype), m, ldx, ctypes.byref(c), out.data_ptr(),
+                           _dtype_code(out.dtype), _matrix("out", out), _launch_stream(x, stream))
+    _check("nvfp4_mx_gemv", st)
+    return out
+
+
+def nvfp4_expert_gemv_workspace_size(tokens, top_k, n):
+    """Bytes of workspace of nvfp4_expert_gemv with weights (n output columns)."""
+    return int(lib.nvfp4_expert_gemv_workspace_size(tokens, top_k, n))
+
+
+@_launches_on_stream
+def nvfp4_expert_gemv(x, ids, w, experts, weights=None, epilogue=NVFP4_EPI_NONE, out_dtype=None, out=None,
+                      workspace=None, stream=None):
+    """Routed nvfp4_gemv: ids (int32 [tokens, top_k]) names the expert of each
+    assignment, w stacks `experts` matrices (tensor_scale [experts]).  x has a
+    row for each token or for each assignment (tokens * top_k).  Without
+    weights: a row of the result for each assignment; with weights (float32
+    [tokens, top_k]): each token's weighted sum of its products."""
+    if ids.dim() != 2:
+        raise ValueError("ids must be tokens x top_k")
+    tokens, top_k = ids.shape
+    n = tokens * top_k
+    if x.dim() != 2 or x.shape[0] not in (tokens, n):
+        raise ValueError("x must have a row for each token or for each assignment")
+    ldx = _matrix("x", x, x.shape[0], w.cols)
+    c = _weight(w, x, experts)
+    cols = w.rows // experts // (2 if epilogue == NVFP4_EPI_SWIGLU else 1)
+    pi = _flat("ids", ids, n, torch.int32, x)
+    pw = None if weights is None else _flat("weights", weights, n, torch.float32, x)
+    out = _gemv_out(out, n if weights is None else tokens, cols, out_dtype, x)
+    if workspace is None and weights is not None:
+        need = lib.nvfp4_expert_gemv_workspace_size(tokens, top_k, cols)
+        workspace = torch.empty(need // 4, dtype=torch.float32, device=x.device)
+    st = lib.nvfp4_expert_gemv(
+        x.data_ptr(), _dtype_code(x.dtype), x.shape[0], ldx, pi, tokens, top_k, ctypes.byref(c), experts, pw,
+        out.data_ptr(), _dtype_code(out.dtype), _matrix("out", out), epilogue,
+        None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _launch_stream(x, stream))
+    _check("nvfp4_expert_gemv", st)
     return out

@@ -464,6 +464,51 @@ nvfp4_status nvfp4_route_backward(const float* dweights, const void* logits, int
                                   int32_t score /* nvfp4_route_score */, int32_t renorm, const float* dscores,
                                   int64_t ldds, void* dlogits, int64_t lddl, void* stream);
 
+/* y = x * W^T for a few rows x (m x K, dtype dt, row stride ldx, not
+ * quantized) and an NVFP4 weight W (N x K, SCALE_1D or SCALE_2D):
+ *   y[i][n] = s_W * sum_k x[i][k] (v_W sb_W)[n][k], exact products of BF16 x
+ *   (of binary32 x: of its three BF16 parts) summed in binary32, rounded once
+ *   to y_dt; m x N, row stride ldy.
+ * EPI_SWIGLU: N = 2F, F % 16 == 0; y (m x F) = gate * sigmoid(gate) * up as
+ * for nvfp4_gemm, in either dtype.
+ * This is the product of a decode step: it reads the weight once for every 16
+ * rows.  Requirements: K % 16 == 0 (SCALE_2D: N % 16 == 0), codes 16-byte
+ * aligned; m <= 1024 (else UNSUPPORTED).  m == 0 or N == 0 is a no-op; K == 0
+ * writes zeros. */
+nvfp4_status nvfp4_gemv(const void* x, int32_t dt /* nvfp4_dtype */, int64_t m, int64_t ldx, const nvfp4_tensor* W,
+                        void* y, int32_t y_dt /* nvfp4_dtype */, int64_t ldy, int32_t ep /* nvfp4_epilogue */,
+                        void* stream);
+
+/* nvfp4_gemv for an MXFP4 weight (W->elem == NVFP4_MX_E2M1, else UNSUPPORTED;
+ * K % 32 == 0).  Weights of magnitude below 2^-126 may count as zero. */
+nvfp4_status nvfp4_mx_gemv(const void* x, int32_t dt /* nvfp4_dtype */, int64_t m, int64_t ldx,
+                           const nvfp4_mx_tensor* W, void* y, int32_t y_dt /* nvfp4_dtype */, int64_t ldy,
+                           void* stream);
+
+/* Bytes of workspace nvfp4_expert_gemv needs for a weighted sum of n output
+ * columns (0 for invalid sizes). */
+size_t nvfp4_expert_gemv_workspace_size(int64_t tokens, int32_t top_k, int64_t n);
+
+/* Routed nvfp4_gemv: W stacks `experts` matrices of N = W->rows / experts rows
+ * (W->tensor_scale: one float each); assignment i = token * top_k + place
+ * multiplies by the matrix of expert ids[i] (DEVICE int32, tokens x top_k; an
+ * index out of range is no expert: its product is zero).
+ *   x_rows == tokens: the assignments of a token share its row of x;
+ *   x_rows == tokens * top_k: each has its own (as the first form's y gives).
+ *   weights NULL: y has a row for each assignment (tokens * top_k rows);
+ *   weights (tokens x top_k floats): y[t] = sum over the places j, in order,
+ *   of weights[t][j] * product, in binary32 (tokens rows; assignments
+ *   without an expert add nothing); ws_bytes >=
+ *   nvfp4_expert_gemv_workspace_size(tokens, top_k, output columns).
+ * An expert's matrix is read once for every 16 of its assignments.
+ * Requirements as for nvfp4_gemv; W->rows % experts == 0 (SCALE_2D: N % 16 ==
+ * 0); top_k >= 1; tokens * top_k <= 1024 (else UNSUPPORTED; nvfp4_grouped_gemm
+ * is the path of many tokens).  tokens == 0 is a no-op. */
+nvfp4_status nvfp4_expert_gemv(const void* x, int32_t dt /* nvfp4_dtype */, int64_t x_rows, int64_t ldx,
+                               const int32_t* ids, int64_t tokens, int32_t top_k, const nvfp4_tensor* W,
+                               int32_t experts, const float* weights, void* y, int32_t y_dt /* nvfp4_dtype */,
+                               int64_t ldy, int32_t ep /* nvfp4_epilogue */, void* ws, size_t ws_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* nvfp4_status_string(int32_t s /* nvfp4_status */);
 

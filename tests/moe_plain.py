@@ -106,3 +106,43 @@ def route_backward(dw, l, ids, sigmoid, renorm, ds):
     if sigmoid:
         return (1.0 - p) * (p * ds + chosen)
     return p * (ds - (p * ds).sum(axis=1, keepdims=True) - common) + chosen
+
+
+# ---------------------------------------------------------------- products with 4-bit weights
+E2M1 = np.array([0, .5, 1, 1.5, 2, 3, 4, 6, 0, -.5, -1, -1.5, -2, -3, -4, -6])
+
+
+def e2m1(codes):
+    """Values of packed E2M1 codes (rows x cols/2 bytes, low nibble first)."""
+    c = codes.cpu().numpy()
+    return np.stack((E2M1[c & 15], E2M1[c >> 4]), axis=2).reshape(c.shape[0], -1)
+
+
+def e4m3(b):
+    b = b.cpu().numpy().astype(np.int64)
+    e, m = b >> 3, b & 7
+    return np.where(e > 0, (8 + m) * 2.0 ** (e - 10.0), m * 2.0 ** -9)
+
+
+def nvfp4_weight(w, experts=1):
+    """The values of an NVFP4Tensor (a stack of `experts` matrices)."""
+    s = e4m3(w.scales)
+    s = np.repeat(s, 16, axis=1)
+    s = np.repeat(s, 16, axis=0) if w.scale_mode == 1 else s
+    ts = host(w.tensor_scale)
+    return e2m1(w.codes) * s * np.repeat(ts, w.rows // experts)[:, None]
+
+
+def mx_weight(w):
+    s = 2.0 ** (w.scales.cpu().numpy().astype(np.int64) - 127.0)
+    return e2m1(w.codes) * np.repeat(s, 32, axis=1)
+
+
+def swiglu(z, wabs):
+    """gate sigmoid(gate) up of z = [gate, up], and how far it moves when each
+    of z does by `wabs`."""
+    f = z.shape[1] // 2
+    g, u, dg, du = z[:, :f], z[:, f:], wabs[:, :f], wabs[:, f:]
+    with np.errstate(over="ignore"):
+        s = 1.0 / (1.0 + np.exp(-g))
+    return g * s * u, np.abs(s * (1.0 + g * (1.0 - s)) * u) * dg + np.abs(g * s) * du
