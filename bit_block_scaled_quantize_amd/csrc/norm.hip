@@ -4,7 +4,7 @@
 // Forward, per row of n elements:
 //   h = round(x + residual)            (the row type: the residual stream as stored)
 //   rstd = 1 / sqrt(sum h^2 / n + eps)
-//   y = (h * rstd) * weight
+//   y = (h * weight) * rstd     (BF16 h and weight: the product is exact)
 // y is written in the row type, as MX codes and scales of the binary32 y, or
 // both.  Backward, with g = dy * weight and xhat = h * rstd:
 //   dx = rstd * (g - xhat * mean(g * xhat)) + dh
@@ -53,6 +53,24 @@ __device__ __forceinline__ void load_weight(const void* w, bool bf16, int64_t c,
 
 constexpr int block_of(int tpr) { return tpr > 256 ? tpr : 256; }
 
+// 1 / sqrt(x), the correctly rounded root's reciprocal taken one Newton step
+// further: with t = x r, r (1 + (1 - t r) / 2), t's own rounding error put back.
+// An MX code that lies between two grid values goes by y's last bits.
+__device__ __forceinline__ float rsqrt32(float x) {
+    const float r = 1.0f / __builtin_sqrtf(x);
+    const float t = x * r, te = __builtin_fmaf(x, r, -t);
+    const float e = __builtin_fmaf(-te, r, __builtin_fmaf(-t, r, 1.0f));
+    return __builtin_fmaf(0.5f * e, r, r);
+}
+
+// The sum of 8 squares, by halves.
+__device__ __forceinline__ float squares8(const float v[8]) {
+    float q[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) q[j] = __builtin_fmaf(v[2 * j + 1], v[2 * j + 1], v[2 * j] * v[2 * j]);
+    return (q[0] + q[1]) + (q[2] + q[3]);
+}
+
 template <typename T, int TPR, int NC>
 __global__ void __launch_bounds__(block_of(TPR)) k_rmsnorm(const NormFwd<T> a) {
     __shared__ float red[TPR > 64 ? TPR / 64 : 1];
@@ -90,11 +108,10 @@ __global__ void __launch_bounds__(block_of(TPR)) k_rmsnorm(const NormFwd<T> a) {
     for (int i = 0; i < NC; ++i) {
         const int64_t c = 8 * ((int64_t)i * TPR + t), n = a.cols - c;
         if (a.h && live && n > 0) store_upto8(a.h + r * a.ldh + c, n, v[i]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) ss = __builtin_fmaf(v[i][j], v[i][j], ss);
+        ss += squares8(v[i]);
     }
     ss = row_sum<TPR>(ss, red);
-    const float rstd = 1.0f / __builtin_sqrtf(ss / (float)a.cols + a.eps);
+    const float rstd = rsqrt32(ss / (float)a.cols + a.eps);
     if (a.rstd && live && t == 0) a.rstd[r] = rstd;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
@@ -103,7 +120,7 @@ __global__ void __launch_bounds__(block_of(TPR)) k_rmsnorm(const NormFwd<T> a) {
         float w[8], y[8];
         load_weight(a.weight, a.w_bf16, c, n, w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = (v[i][j] * rstd) * w[j];
+        for (int j = 0; j < 8; ++j) y[j] = (v[i][j] * w[j]) * rstd;
         if (a.y && live) store_upto8(a.y + r * a.ldy + c, n, y);
         if (a.codes) {  // cols % 32 == 0: the four lanes of a block agree on n > 0
             uint32_t cw[2];
@@ -132,11 +149,74 @@ struct NormBwd {
     bool w_bf16;
 };
 
+// 8 elements as they lie in memory.
+template <typename T>
+struct Raw {
+    uint32_t q[2 * sizeof(T)];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int j = 0; j < (int)(2 * sizeof(T)); ++j) q[j] = 0;
+    }
+    // p[0 .. min(n, 8) - 1], zero beyond (n >= 1)
+    __device__ __forceinline__ void load(const T* p, int64_t n) {
+        constexpr int W = 2 * sizeof(T);
+        if (n >= 8) {
+#pragma unroll
+            for (int k = 0; k < W / 4; ++k) {
+                const u4_align2 u = *reinterpret_cast<const u4_align2*>(p + 16 / sizeof(T) * k);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) q[4 * k + j] = u[j];
+            }
+        } else if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                q[j] = (2 * j < n ? (uint32_t)p[2 * j] : 0u) | (2 * j + 1 < n ? (uint32_t)p[2 * j + 1] << 16 : 0u);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) q[j] = j < n ? __float_as_uint(p[j]) : 0u;
+        }
+    }
+    __device__ __forceinline__ float value(int j) const {
+        if constexpr (sizeof(T) == 2) return __uint_as_float((j & 1) ? q[j >> 1] & 0xFFFF0000u : q[j >> 1] << 16);
+        else return __uint_as_float(q[j]);
+    }
+};
+
+// What a row's thread reads: its elements of dy, h and dh, and the row's rstd.
+template <typename T, int NC>
+struct BwdRow {
+    Raw<T> dy[NC], h[NC], dh[NC];
+    float rstd;
+};
+
+template <typename T, int TPR, int NC>
+__device__ __forceinline__ void load_row(const NormBwd<T>& a, int64_t r, int t, BwdRow<T, NC>& b) {
+    b.rstd = a.rstd[r];
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        const int64_t c = 8 * ((int64_t)i * TPR + t), n = a.cols - c;
+        b.dy[i].clear();
+        b.h[i].clear();
+        b.dh[i].clear();
+        if (n > 0) {
+            b.dy[i].load(a.dy + r * a.lddy + c, n);
+            b.h[i].load(a.h + r * a.ldh + c, n);
+            if (a.dh) b.dh[i].load(a.dh + r * a.lddh + c, n);
+        }
+    }
+}
+
+// Whether the next row's elements fit in registers beside the current row's
+// (a workgroup of 1024 threads has 128 registers a thread).
+template <typename T>
+constexpr bool reads_ahead(int tpr, int nc) { return tpr < 1024 || nc * sizeof(T) <= 4; }
+
 // Row group g takes rows g, g + groups, ... and leaves its sum of dy * xhat in
-// parts[g]; the next row's elements are loaded before the current row's sum is
-// waited for.
+// parts[g].  The next row's elements are under way while the current row's sum
+// goes round, so that the loads never wait for a reduction.
 template <typename T, int TPR, int NC>
 __global__ void __launch_bounds__(block_of(TPR)) k_rmsnorm_backward(const NormBwd<T> a) {
+    constexpr bool AHEAD = reads_ahead<T>(TPR, NC);
     __shared__ float red[2][TPR > 64 ? TPR / 64 : 1];
     const int t = threadIdx.x % TPR;
     const int64_t g = (int64_t)blockIdx.x * (block_of(TPR) / TPR) + threadIdx.x / TPR;
@@ -150,35 +230,36 @@ __global__ void __launch_bounds__(block_of(TPR)) k_rmsnorm_backward(const NormBw
     }
     // every group of a workgroup makes the same number of turns (row_sum needs
     // all lanes); turns past the last row read it again and add nothing
-    const int64_t turns = (a.rows + a.groups - 1) / a.groups;
+    const int64_t turns = (a.rows + a.groups - 1) / a.groups, last = a.rows - 1;
     const float inv_n = 1.0f / (float)a.cols;
     int buf = 0;
+    BwdRow<T, NC> cur, next;
+    if constexpr (AHEAD) load_row<T, TPR, NC>(a, min(g, last), t, cur);
     for (int64_t k = 0; k < turns; ++k) {
         const int64_t row = g + k * a.groups;
-        const bool live = row < a.rows;
-        const int64_t r = live ? row : a.rows - 1;
-        float dy[NC][8], h[NC][8];
-        const float rstd = a.rstd[r];
+        if constexpr (AHEAD) {
+            if (k + 1 < turns) load_row<T, TPR, NC>(a, min(row + a.groups, last), t, next);
+        } else {
+            load_row<T, TPR, NC>(a, min(row, last), t, cur);
+        }
+        const bool live = row <= last;
+        if (!live) {
+            cur.rstd = 0.0f;
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            const int64_t c = 8 * ((int64_t)i * TPR + t), n = a.cols - c;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) dy[i][j] = h[i][j] = 0.0f;
-            if (n > 0) {
-                load_upto8(a.dy + r * a.lddy + c, n, dy[i]);
-                load_upto8(a.h + r * a.ldh + c, n, h[i]);
+            for (int i = 0; i < NC; ++i) {
+                cur.dy[i].clear();
+                cur.h[i].clear();
             }
         }
+        const float rstd = cur.rstd;
         float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < NC; ++i)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float xh = h[i][j] * rstd;
-                if (live) dw[i][j] = __builtin_fmaf(dy[i][j], xh, dw[i][j]);
-                dy[i][j] = dy[i][j] * w[i][j];
-                h[i][j] = xh;
-                s = __builtin_fmaf(dy[i][j], xh, s);
+                const float dy = cur.dy[i].value(j), xh = cur.h[i].value(j) * rstd;
+                dw[i][j] = __builtin_fmaf(dy, xh, dw[i][j]);
+                s = __builtin_fmaf(dy * w[i][j], xh, s);
             }
         s = row_sum<TPR>(s, red[buf]) * inv_n;
         buf ^= 1;
@@ -187,14 +268,14 @@ __global__ void __launch_bounds__(block_of(TPR)) k_rmsnorm_backward(const NormBw
             const int64_t c = 8 * ((int64_t)i * TPR + t), n = a.cols - c;
             if (n <= 0 || !live) continue;
             float q[8];
-            if (a.dh) load_upto8(a.dh + r * a.lddh + c, n, q);
-            else
 #pragma unroll
-                for (int j = 0; j < 8; ++j) q[j] = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) q[j] = __builtin_fmaf(rstd, __builtin_fmaf(-h[i][j], s, dy[i][j]), q[j]);
-            store_upto8(a.dx + r * a.lddx + c, n, q);
+            for (int j = 0; j < 8; ++j) {
+                const float gx = __builtin_fmaf(-(cur.h[i].value(j) * rstd), s, cur.dy[i].value(j) * w[i][j]);
+                q[j] = __builtin_fmaf(rstd, gx, cur.dh[i].value(j));
+            }
+            store_upto8(a.dx + row * a.lddx + c, n, q);
         }
+        if constexpr (AHEAD) cur = next;
     }
     if (g < a.groups)
 #pragma unroll
@@ -227,14 +308,15 @@ __global__ void __launch_bounds__(256) k_sum_parts(const float* __restrict__ par
 
 inline int64_t n_cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Threads per row: the fewest whose kMaxNC chunks hold the row; more where
-// there are too few rows to give every SIMD a wave (the row's latency then
-// counts).
-int threads_per_row(int64_t rows, int64_t cols) {
+// Threads per row: the fewest that hold the row in `most` chunks each; more
+// where there are too few rows to give every SIMD a wave (the row's latency
+// then counts).
+int threads_per_row(int64_t rows, int64_t cols, int most) {
     const int64_t chunks = n_cdiv(cols, 8);
+    const auto more = [](int tpr) { return tpr == 256 || tpr == 512 ? 2 * tpr : 4 * tpr; };
     int tpr = 16;
-    while (chunks > (int64_t)tpr * kMaxNC) tpr *= 4;
-    while (tpr < 1024 && tpr < chunks && rows * tpr < 64 * 1024) tpr *= 4;
+    while (tpr < 1024 && chunks > (int64_t)tpr * most) tpr = more(tpr);
+    while (tpr < 1024 && tpr < chunks && rows * tpr < 64 * 1024) tpr = more(tpr);
     return tpr;
 }
 
@@ -248,7 +330,7 @@ struct BwdPlan {
 // row of binary32 partial sums, written and read again).
 BwdPlan bwd_plan(int64_t rows, int64_t cols) {
     BwdPlan p;
-    p.tpr = threads_per_row(rows, cols);
+    p.tpr = threads_per_row(rows, cols, 2);
     const int64_t per = block_of(p.tpr) / p.tpr;
     p.blocks = std::min<int64_t>(512, n_cdiv(n_cdiv(rows, 4), per));
     p.groups = std::min(rows, p.blocks * per);
@@ -265,12 +347,13 @@ BwdPlan bwd_plan(int64_t rows, int64_t cols) {
 
 template <typename T>
 hipError_t norm_typed(const NormFwd<T>& a, hipStream_t s) {
-    const int tpr = threads_per_row(a.rows, a.cols);
+    const int tpr = threads_per_row(a.rows, a.cols, kMaxNC);
     const dim3 g((unsigned)n_cdiv(a.rows, block_of(tpr) / tpr)), b(block_of(tpr));
     switch (tpr) {
         case 16: NVFP4_NORM_NC(k_rmsnorm, T, 16, g, b, 0, s); break;
         case 64: NVFP4_NORM_NC(k_rmsnorm, T, 64, g, b, 0, s); break;
         case 256: NVFP4_NORM_NC(k_rmsnorm, T, 256, g, b, 0, s); break;
+        case 512: NVFP4_NORM_NC(k_rmsnorm, T, 512, g, b, 0, s); break;
         default: NVFP4_NORM_NC(k_rmsnorm, T, 1024, g, b, 0, s);
     }
     return hipGetLastError();
@@ -285,6 +368,7 @@ hipError_t norm_bwd_typed(NormBwd<T> a, float* dweight, hipStream_t s) {
         case 16: NVFP4_NORM_NC(k_rmsnorm_backward, T, 16, g, b, 0, s); break;
         case 64: NVFP4_NORM_NC(k_rmsnorm_backward, T, 64, g, b, 0, s); break;
         case 256: NVFP4_NORM_NC(k_rmsnorm_backward, T, 256, g, b, 0, s); break;
+        case 512: NVFP4_NORM_NC(k_rmsnorm_backward, T, 512, g, b, 0, s); break;
         default: NVFP4_NORM_NC(k_rmsnorm_backward, T, 1024, g, b, 0, s);
     }
     hipError_t e = hipGetLastError();

@@ -111,6 +111,10 @@ struct MaxOp {
     __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
 };
 
+// A barrier of the workgroup for what lies in LDS alone: loads from memory
+// that are under way stay so.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
 // Sum over the TPR threads (16, 64, or whole workgroup of TPR threads) that
 // share a row, in a fixed order, the result in every thread.  lds: TPR / 64
 // floats that no other use of the current phase touches (TPR > 64); a second
@@ -121,7 +125,7 @@ __device__ __forceinline__ float row_sum(float x, float* lds) {
     x = reduce64(x, AddOp());
     if constexpr (TPR > 64) {
         if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
-        __syncthreads();
+        lds_barrier();
         x = 0.0f;
 #pragma unroll
         for (int w = 0; w < TPR / 64; ++w) x += lds[w];

@@ -376,7 +376,7 @@ size_t nvfp4_mx_gemm_workspace_size(const nvfp4_mx_tensor* A, const nvfp4_mx_ten
 /* RMS norm with the residual's addition.  Per row:
  *   h = x + residual, rounded to dt (residual NULL: h = x);
  *   rstd = 1 / sqrt(sum h^2 / cols + eps), binary32;
- *   y = (h * rstd) * weight, binary32.
+ *   y = (h * weight) * rstd, binary32.
  * Outputs, each optional (NULL) but one of y and mx: h (rows x cols, dt; may
  * be x or residual itself, same leading dimension), y rounded to dt, mx the
  * ROW_1D nearest-even MX quantization of the binary32 y (mx->elem selects the
