@@ -13,9 +13,12 @@
 //
 // Both are HBM-bound streams.  A row's elements stay in registers between the
 // sum and the outputs, so every array is read or written once: TPR threads
-// share a row (16, 64, 256 or 1024), each holding NC chunks of 8 consecutive
+// share a row (16, 64, 256, 512 or 1024), each holding NC chunks of 8 consecutive
 // elements (chunk i of thread t starts at 8 (i TPR + t)), so a wave's 16-byte
 // accesses are contiguous and four lanes hold one 32-element MX block.
+// Measured, BF16: forward with h, y and MXFP8 codes, 8192 x 5120, 76.9 us or
+// 4.92 TB/s; backward with dh, 16384 x 7168, 185 us or 5.07 TB/s (a large copy
+// reaches 5.07).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -29,7 +32,9 @@ namespace nvfp4 {
 
 namespace {
 
-constexpr int kMaxNC = 4;
+// Chunks a thread: at most kNC (8192 x 5120 forward with 4: 81.5 us, with 2:
+// 76.9) but in the widest rows, which 1024 threads hold in kMaxNC.
+constexpr int kNC = 2, kMaxNC = 4;
 
 template <typename T>
 struct NormFwd {
@@ -41,7 +46,7 @@ struct NormFwd {
     uint8_t* codes;     // nullable
     uint8_t* scales;
     float* rstd;        // nullable
-    int64_t rows, cols, ldx, ldr, ldh, ldy;
+    int64_t rows, cols, ldx, ldr, ldh, ldy, groups, turns;
     float eps;
     bool w_bf16, mx_e2m1;
 };
@@ -50,104 +55,6 @@ __device__ __forceinline__ void load_weight(const void* w, bool bf16, int64_t c,
     if (bf16) load_upto8(static_cast<const uint16_t*>(w) + c, n, v);
     else load_upto8(static_cast<const float*>(w) + c, n, v);
 }
-
-constexpr int block_of(int tpr) { return tpr > 256 ? tpr : 256; }
-
-// 1 / sqrt(x), the correctly rounded root's reciprocal taken one Newton step
-// further: with t = x r, r (1 + (1 - t r) / 2), t's own rounding error put back.
-// An MX code that lies between two grid values goes by y's last bits.
-__device__ __forceinline__ float rsqrt32(float x) {
-    const float r = 1.0f / __builtin_sqrtf(x);
-    const float t = x * r, te = __builtin_fmaf(x, r, -t);
-    const float e = __builtin_fmaf(-te, r, __builtin_fmaf(-t, r, 1.0f));
-    return __builtin_fmaf(0.5f * e, r, r);
-}
-
-// The sum of 8 squares, by halves.
-__device__ __forceinline__ float squares8(const float v[8]) {
-    float q[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) q[j] = __builtin_fmaf(v[2 * j + 1], v[2 * j + 1], v[2 * j] * v[2 * j]);
-    return (q[0] + q[1]) + (q[2] + q[3]);
-}
-
-template <typename T, int TPR, int NC>
-__global__ void __launch_bounds__(block_of(TPR)) k_rmsnorm(const NormFwd<T> a) {
-    __shared__ float red[TPR > 64 ? TPR / 64 : 1];
-    const int t = threadIdx.x % TPR;
-    const int64_t row = (int64_t)blockIdx.x * (block_of(TPR) / TPR) + threadIdx.x / TPR;
-    // groups past the last row repeat it and store nothing
-    const bool live = row < a.rows;
-    const int64_t r = live ? row : a.rows - 1;
-    float v[NC][8];
-    float ss = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NC; ++i) {
-        const int64_t c = 8 * ((int64_t)i * TPR + t), n = a.cols - c;
-        if (n > 0) load_upto8(a.x + r * a.ldx + c, n, v[i]);
-        else
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
-    }
-    if (a.residual) {
-        float q[NC][8];
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            const int64_t c = 8 * ((int64_t)i * TPR + t), n = a.cols - c;
-            if (n > 0) load_upto8(a.residual + r * a.ldr + c, n, q[i]);
-            else
-#pragma unroll
-                for (int j = 0; j < 8; ++j) q[i][j] = 0.0f;
-        }
-#pragma unroll
-        for (int i = 0; i < NC; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = rounded_to<T>(v[i][j] + q[i][j]);
-    }
-#pragma unroll
-    for (int i = 0; i < NC; ++i) {
-        const int64_t c = 8 * ((int64_t)i * TPR + t), n = a.cols - c;
-        if (a.h && live && n > 0) store_upto8(a.h + r * a.ldh + c, n, v[i]);
-        ss += squares8(v[i]);
-    }
-    ss = row_sum<TPR>(ss, red);
-    const float rstd = rsqrt32(ss / (float)a.cols + a.eps);
-    if (a.rstd && live && t == 0) a.rstd[r] = rstd;
-#pragma unroll
-    for (int i = 0; i < NC; ++i) {
-        const int64_t c = 8 * ((int64_t)i * TPR + t), n = a.cols - c;
-        if (n <= 0) continue;
-        float w[8], y[8];
-        load_weight(a.weight, a.w_bf16, c, n, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = (v[i][j] * w[j]) * rstd;
-        if (a.y && live) store_upto8(a.y + r * a.ldy + c, n, y);
-        if (a.codes) {  // cols % 32 == 0: the four lanes of a block agree on n > 0
-            uint32_t cw[2];
-            const uint32_t sb = a.mx_e2m1 ? mx_block_rne8<kMxE2M1>(y, cw) : mx_block_rne8<kMxE4M3>(y, cw);
-            if (live) {
-                if (a.mx_e2m1)
-                    *reinterpret_cast<uint32_t*>(a.codes + r * (a.cols / 2) + c / 2) = cw[0];
-                else
-                    *reinterpret_cast<uint2*>(a.codes + r * a.cols + c) = make_uint2(cw[0], cw[1]);
-                if ((t & 3) == 0) a.scales[r * (a.cols / 32) + c / 32] = (uint8_t)sb;
-            }
-        }
-    }
-}
-
-template <typename T>
-struct NormBwd {
-    const T* dy;
-    const T* h;
-    const T* dh;  // nullable
-    const float* rstd;
-    const void* weight;
-    T* dx;
-    float* parts;  // groups x cols
-    int64_t rows, cols, lddy, ldh, lddh, lddx, groups;
-    bool w_bf16;
-};
 
 // 8 elements as they lie in memory.
 template <typename T>
@@ -180,6 +87,120 @@ struct Raw {
         if constexpr (sizeof(T) == 2) return __uint_as_float((j & 1) ? q[j >> 1] & 0xFFFF0000u : q[j >> 1] << 16);
         else return __uint_as_float(q[j]);
     }
+};
+
+constexpr int block_of(int tpr) { return tpr > 256 ? tpr : 256; }
+
+// 1 / sqrt(x), the correctly rounded root's reciprocal taken one Newton step
+// further: with t = x r, r (1 + (1 - t r) / 2), t's own rounding error put back.
+// An MX code that lies between two grid values goes by y's last bits.
+__device__ __forceinline__ float rsqrt32(float x) {
+    const float r = 1.0f / __builtin_sqrtf(x);
+    const float t = x * r, te = __builtin_fmaf(x, r, -t);
+    const float e = __builtin_fmaf(-te, r, __builtin_fmaf(-t, r, 1.0f));
+    return __builtin_fmaf(0.5f * e, r, r);
+}
+
+// The sum of 8 squares, by halves.
+__device__ __forceinline__ float squares8(const float v[8]) {
+    float q[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) q[j] = __builtin_fmaf(v[2 * j + 1], v[2 * j + 1], v[2 * j] * v[2 * j]);
+    return (q[0] + q[1]) + (q[2] + q[3]);
+}
+
+template <typename T, int NC>
+struct FwdRow {
+    Raw<T> x[NC], residual[NC];
+};
+
+template <typename T, int TPR, int NC>
+__device__ __forceinline__ void load_row(const NormFwd<T>& a, int64_t r, int t, FwdRow<T, NC>& b) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        const int64_t c = 8 * ((int64_t)i * TPR + t), n = a.cols - c;
+        b.x[i].clear();
+        b.residual[i].clear();
+        if (n > 0) {
+            b.x[i].load(a.x + r * a.ldx + c, n);
+            if (a.residual) b.residual[i].load(a.residual + r * a.ldr + c, n);
+        }
+    }
+}
+
+// Row group g takes rows g, g + groups, ...; with AHEAD the next row's elements
+// are under way while the current row's sum goes round and its outputs leave.
+template <typename T, int TPR, int NC, bool AHEAD>
+__global__ void __launch_bounds__(block_of(TPR)) k_rmsnorm(const NormFwd<T> a) {
+    __shared__ float red[2][TPR > 64 ? TPR / 64 : 1];
+    const int t = threadIdx.x % TPR;
+    const int64_t g = (int64_t)blockIdx.x * (block_of(TPR) / TPR) + threadIdx.x / TPR;
+    const int64_t last = a.rows - 1;
+    const float cols = (float)a.cols;
+    int buf = 0;
+    FwdRow<T, NC> cur, next;
+    load_row<T, TPR, NC>(a, min(g, last), t, cur);
+    // every group of a workgroup makes the same number of turns; those past
+    // the last row repeat it and store nothing
+    for (int64_t k = 0; k < a.turns; ++k) {
+        const int64_t row = g + k * a.groups, r = min(row, last);
+        if constexpr (AHEAD) {
+            if (k + 1 < a.turns) load_row<T, TPR, NC>(a, min(row + a.groups, last), t, next);
+        }
+        const bool live = row <= last;
+        float v[NC][8];
+        float ss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int64_t c = 8 * ((int64_t)i * TPR + t), n = a.cols - c;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[i][j] = cur.x[i].value(j);
+                if (a.residual) v[i][j] = rounded_to<T>(v[i][j] + cur.residual[i].value(j));
+            }
+            if (a.h && live && n > 0) store_upto8(a.h + r * a.ldh + c, n, v[i]);
+            ss += squares8(v[i]);
+        }
+        ss = row_sum<TPR>(ss, red[buf]);
+        buf ^= 1;
+        const float rstd = rsqrt32(ss / cols + a.eps);
+        if (a.rstd && live && t == 0) a.rstd[r] = rstd;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int64_t c = 8 * ((int64_t)i * TPR + t), n = a.cols - c;
+            if (n <= 0) continue;
+            float w[8], y[8];
+            load_weight(a.weight, a.w_bf16, c, n, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = (v[i][j] * w[j]) * rstd;
+            if (a.y && live) store_upto8(a.y + r * a.ldy + c, n, y);
+            if (a.codes) {  // cols % 32 == 0: the four lanes of a block agree on n > 0
+                uint32_t cw[2];
+                const uint32_t sb = a.mx_e2m1 ? mx_block_rne8<kMxE2M1>(y, cw) : mx_block_rne8<kMxE4M3>(y, cw);
+                if (live) {
+                    if (a.mx_e2m1)
+                        *reinterpret_cast<uint32_t*>(a.codes + r * (a.cols / 2) + c / 2) = cw[0];
+                    else
+                        *reinterpret_cast<uint2*>(a.codes + r * a.cols + c) = make_uint2(cw[0], cw[1]);
+                    if ((t & 3) == 0) a.scales[r * (a.cols / 32) + c / 32] = (uint8_t)sb;
+                }
+            }
+        }
+        if constexpr (AHEAD) cur = next;
+    }
+}
+
+template <typename T>
+struct NormBwd {
+    const T* dy;
+    const T* h;
+    const T* dh;  // nullable
+    const float* rstd;
+    const void* weight;
+    T* dx;
+    float* parts;  // groups x cols
+    int64_t rows, cols, lddy, ldh, lddh, lddx, groups;
+    bool w_bf16;
 };
 
 // What a row's thread reads: its elements of dy, h and dh, and the row's rstd.
@@ -308,14 +329,14 @@ __global__ void __launch_bounds__(256) k_sum_parts(const float* __restrict__ par
 
 inline int64_t n_cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Threads per row: the fewest that hold the row in `most` chunks each; more
+// Threads per row: the fewest that hold the row in kNC chunks each; more
 // where there are too few rows to give every SIMD a wave (the row's latency
 // then counts).
-int threads_per_row(int64_t rows, int64_t cols, int most) {
+int threads_per_row(int64_t rows, int64_t cols) {
     const int64_t chunks = n_cdiv(cols, 8);
     const auto more = [](int tpr) { return tpr == 256 || tpr == 512 ? 2 * tpr : 4 * tpr; };
     int tpr = 16;
-    while (tpr < 1024 && chunks > (int64_t)tpr * most) tpr = more(tpr);
+    while (tpr < 1024 && chunks > (int64_t)tpr * kNC) tpr = more(tpr);
     while (tpr < 1024 && tpr < chunks && rows * tpr < 64 * 1024) tpr = more(tpr);
     return tpr;
 }
@@ -330,7 +351,7 @@ struct BwdPlan {
 // row of binary32 partial sums, written and read again).
 BwdPlan bwd_plan(int64_t rows, int64_t cols) {
     BwdPlan p;
-    p.tpr = threads_per_row(rows, cols, 2);
+    p.tpr = threads_per_row(rows, cols);
     const int64_t per = block_of(p.tpr) / p.tpr;
     p.blocks = std::min<int64_t>(512, n_cdiv(n_cdiv(rows, 4), per));
     p.groups = std::min(rows, p.blocks * per);
@@ -345,17 +366,44 @@ BwdPlan bwd_plan(int64_t rows, int64_t cols) {
         else hipLaunchKernelGGL((K<T, TPR, kMaxNC>), __VA_ARGS__, a);                                       \
     } while (0)
 
+// More rows than fill the chip with 1024 threads a compute unit: that many
+// workgroups take the rows in turn, reading ahead (8192 x 5120: one workgroup
+// a row 82.8 us, reading ahead 76.9 with 1024 threads a unit and 78.0 with
+// 2048).
+template <typename T, int TPR, int NC>
+void norm_launch(NormFwd<T> a, hipStream_t s) {
+    constexpr int per = block_of(TPR) / TPR;
+    constexpr bool ahead = TPR < 1024;
+    int64_t blocks = n_cdiv(a.rows, per);
+    const int64_t most = 256 * (1024 / block_of(TPR));
+    if (ahead && blocks > most) {
+        blocks = most;
+        a.groups = blocks * per;
+        a.turns = n_cdiv(a.rows, a.groups);
+        hipLaunchKernelGGL((k_rmsnorm<T, TPR, NC, ahead>), dim3((unsigned)blocks), dim3(block_of(TPR)), 0, s, a);
+    } else {
+        a.groups = blocks * per;
+        a.turns = 1;
+        hipLaunchKernelGGL((k_rmsnorm<T, TPR, NC, false>), dim3((unsigned)blocks), dim3(block_of(TPR)), 0, s, a);
+    }
+}
+
 template <typename T>
 hipError_t norm_typed(const NormFwd<T>& a, hipStream_t s) {
-    const int tpr = threads_per_row(a.rows, a.cols, kMaxNC);
-    const dim3 g((unsigned)n_cdiv(a.rows, block_of(tpr) / tpr)), b(block_of(tpr));
+    const int tpr = threads_per_row(a.rows, a.cols);
+    const int64_t nc = n_cdiv(n_cdiv(a.cols, 8), tpr);
+#define NVFP4_NORM_FWD(TPR)                                       \
+    if (nc <= 1) norm_launch<T, TPR, 1>(a, s);                    \
+    else if (nc <= 2) norm_launch<T, TPR, 2>(a, s);               \
+    else norm_launch<T, TPR, kMaxNC>(a, s)
     switch (tpr) {
-        case 16: NVFP4_NORM_NC(k_rmsnorm, T, 16, g, b, 0, s); break;
-        case 64: NVFP4_NORM_NC(k_rmsnorm, T, 64, g, b, 0, s); break;
-        case 256: NVFP4_NORM_NC(k_rmsnorm, T, 256, g, b, 0, s); break;
-        case 512: NVFP4_NORM_NC(k_rmsnorm, T, 512, g, b, 0, s); break;
-        default: NVFP4_NORM_NC(k_rmsnorm, T, 1024, g, b, 0, s);
+        case 16: NVFP4_NORM_FWD(16); break;
+        case 64: NVFP4_NORM_FWD(64); break;
+        case 256: NVFP4_NORM_FWD(256); break;
+        case 512: NVFP4_NORM_FWD(512); break;
+        default: NVFP4_NORM_FWD(1024);
     }
+#undef NVFP4_NORM_FWD
     return hipGetLastError();
 }
 
