@@ -151,11 +151,12 @@ struct RouteArgs {
     int64_t* offsets;  // NULL: no dispatch plan (order and position unused)
     int* order;
     int* position;
-    int* counts;   // route_workspace_ints
-    int64_t span;  // set by the launcher
+    uint8_t* counts;  // route_workspace_bytes
+    int64_t span;      // tokens of a workgroup; set by the launcher, as group is
+    int group;         // spans of a workgroup of the second step
 };
 bool route_shape_fits(int experts, int groups);
-int64_t route_workspace_ints(int64_t tokens, int experts);
+size_t route_workspace_bytes(int64_t tokens, int experts);
 hipError_t launch_route(RouteArgs a, hipStream_t s);
 
 struct RouteBackward {

@@ -459,7 +459,7 @@ nvfp4_status nvfp4_rmsnorm_backward(const void* dy, int64_t lddy, const void* h,
 // ---------------------------------------------------------------- routing
 size_t nvfp4_route_workspace_size(int64_t tokens, int64_t experts) {
     if (tokens < 0 || experts < 1 || experts > kMaxExperts) return 0;
-    return (size_t)route_workspace_ints(tokens, (int)experts) * sizeof(int32_t);
+    return route_workspace_bytes(tokens, (int)experts);
 }
 
 nvfp4_status nvfp4_route(const void* logits, int32_t dt /* nvfp4_dtype */, int64_t tokens, int64_t experts, int64_t ld,
@@ -503,8 +503,9 @@ nvfp4_status nvfp4_route(const void* logits, int32_t dt /* nvfp4_dtype */, int64
     a.offsets = offsets;
     a.order = order;
     a.position = position;
-    a.counts = static_cast<int*>(ws);
+    a.counts = static_cast<uint8_t*>(ws);
     a.span = 0;
+    a.group = 0;
     return launch_route(a, static_cast<hipStream_t>(stream)) == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
 }
 

@@ -42,6 +42,13 @@ __device__ __forceinline__ float load1(const void* p, bool bf16, int64_t i) {
 
 __device__ __forceinline__ float sigmoid32(float l) { return 1.0f / (1.0f + expf(-l)); }
 
+// Scores for the choice alone, by the hardware's exponential and reciprocal.
+// An exponential e^-x is off by at most (x + 2) U (U = 2^-24) of itself, which
+// is under 3 U of 1 for every x >= 0: the sigmoid, whose slope in log e is
+// p (1 - p), by under 2^-21 (its reciprocal's step included).
+__device__ __forceinline__ float quick_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
+__device__ __forceinline__ float quick_sigmoid(float l) { return __builtin_amdgcn_rcpf(1.0f + quick_exp(-l)); }
+
 // exp(l - m) with the rounding error of the difference put back (the error of
 // a binary32 difference is itself a binary32 value): a few ulp for any l <= m.
 __device__ __forceinline__ float exp_diff(float l, float m) {
@@ -58,18 +65,6 @@ __device__ __forceinline__ float lanes_reduce(float x, Op op) {
 }
 template <int LPT>
 __device__ __forceinline__ float lanes_max(float x) { return lanes_reduce<LPT>(x, MaxOp()); }
-template <int LPT>
-__device__ __forceinline__ double lanes_max(double x) {
-#pragma unroll
-    for (int d = 1; d < LPT; d <<= 1) x = fmax(x, __shfl_xor(x, d));
-    return x;
-}
-template <int LPT>
-__device__ __forceinline__ double lanes_sum(double x) {
-#pragma unroll
-    for (int d = 1; d < LPT; d <<= 1) x += __shfl_xor(x, d);
-    return x;
-}
 
 // The bits of a ballot that belong to the caller's token, from bit 0.
 template <int LPT>
@@ -78,74 +73,33 @@ __device__ __forceinline__ uint64_t own_bits(uint64_t mask) {
     else return (mask >> (threadIdx.x & 48)) & 0xFFFFull;
 }
 
-// Which groups stay: `kept` tells whether the caller's lane belongs to one of
-// the top_groups groups of the largest group score (ties to the lower index).
-// s: the selection scores, V a lane, -inf where there is none.  Returns false
-// where two group scores are nearer than tol(x) of a score of size x, twice
-// what they may be off by (negative: exact).
-template <typename F, int LPT, int V, typename Tol>
-__device__ __forceinline__ bool keep_groups(const F s[V], const RouteShape& g, Tol tol, bool& kept) {
-    const F none = -(F)__builtin_inf();
-    const int lane = threadIdx.x & (LPT - 1), mine = lane / g.lanes_per_group;
-    // the group's best two scores
-    F a = none, b = none;
+// Elements p[0 .. min(n, V) - 1] as binary32 (what lies beyond stays as it was).
+template <int V>
+__device__ __forceinline__ void load_values(const void* p, bool bf16, int n, float v[V]) {
+    if constexpr (V >= 8) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        b = fmax(b, fmin(a, s[j]));
-        a = fmax(a, s[j]);
-    }
-    for (int d = 1; d < g.lanes_per_group; d <<= 1) {
-        const F a2 = __shfl_xor(a, d), b2 = __shfl_xor(b, d);
-        b = fmax(fmin(a, a2), fmax(b, b2));
-        a = fmax(a, a2);
-    }
-    const F gs = (g.group_top2 && b > none) ? a + b : a;
-    int ahead = 0;  // groups before the own one
-    bool certain = true;
-    for (int o = 0; o < g.groups; ++o) {
-        const F q = __shfl(gs, (threadIdx.x & 63 & ~(LPT - 1)) + o * g.lanes_per_group);
-        ahead += (q > gs || (q == gs && o < mine)) ? 1 : 0;
-        if (mine < g.groups && o != mine && fabs(q - gs) <= tol(fmax(fabs(q), fabs(gs)))) certain = false;
-    }
-    kept = mine < g.groups && ahead < g.top_groups;
-    return certain;
-}
-
-// The top_k largest of the keys s (V a lane, -inf where there is none; used
-// up), ties to the lower index: lane j < top_k gets the j-th one's expert in
-// id.  Returns as keep_groups does.
-template <typename F, int LPT, int V, typename Tol>
-__device__ __forceinline__ bool choose(F s[V], const RouteShape& g, int base, Tol tol, int& id) {
-    const F none = -(F)__builtin_inf();
-    const int lane = threadIdx.x & (LPT - 1);
-    bool certain = true;
-    F last = 0;
-    id = 0;
-    for (int it = 0; it <= g.top_k; ++it) {
-        F m = s[0];
+        for (int c = 0; c < V; c += 8)
+            if (c < n) {
+                if (bf16) load_upto8(static_cast<const uint16_t*>(p) + c, n - c, v + c);
+                else load_upto8(static_cast<const float*>(p) + c, n - c, v + c);
+            }
+    } else {
+        typedef float fv_t __attribute__((ext_vector_type(V), aligned(4)));
+        typedef uint16_t hv_t __attribute__((ext_vector_type(V), aligned(2)));
+        if (n >= V && bf16) {
+            const hv_t q = *static_cast<const hv_t*>(p);
 #pragma unroll
-        for (int j = 1; j < V; ++j) m = fmax(m, s[j]);
-        const F M = lanes_max<LPT>(m);
-        if (it > 0 && M > none && last - M <= tol(fmax(fabs(last), fabs(M)))) certain = false;
-        if (it == g.top_k) break;
-        last = M;
-        const uint64_t has = own_bits<LPT>(__ballot(m == M));
-        const int win = __ffsll((unsigned long long)has) - 1;
-        int at = 0;
-        if (lane == win) {
-            bool done = false;
+            for (int j = 0; j < V; ++j) v[j] = bf16_to_f32(q[j]);
+        } else if (n >= V) {
+            const fv_t q = *static_cast<const fv_t*>(p);
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[j] = q[j];
+        } else {
 #pragma unroll
             for (int j = 0; j < V; ++j)
-                if (!done && s[j] == M) {
-                    done = true;
-                    at = base + j;
-                    s[j] = none;
-                }
+                if (j < n) v[j] = load1(p, bf16, j);
         }
-        at = __shfl(at, (threadIdx.x & 63 & ~(LPT - 1)) + win);
-        if (lane == it) id = at;
     }
-    return certain;
 }
 
 // A selection score that compares: NaN and infinities as `logit` takes them.
@@ -154,162 +108,292 @@ __device__ __forceinline__ F comparable(F s) {
     return fmin(fmax(s, (F)kLowest), (F)-kLowest);
 }
 
-// One wave's tokens (64 / LPT of them from t0): lane group u's token is t0 + u;
-// tokens past the end repeat the last one.  Returns lane j < top_k's chosen
-// expert and weight.
+// How far binary32 scores are off, counted twice (two are compared): a score
+// of size x by tol(x).  Sigmoid: 4 U = 2^-22.  Softmax, p <= 1 / total: 3 U of
+// that and the sum's relative error, 38 U of its additions and (2 x + 2) U of
+// its terms, x = m - l, whose mean under p is at most log E < 8.  Both: U of
+// the sum with the bias.
+struct Tolerance {
+    float absolute;
+    __device__ __forceinline__ float operator()(float x) const { return absolute + 0x1p-20f * x; }
+};
+
+// Which groups stay, from a and b, the best and second best key of the
+// caller's lane (-inf where there is none): `kept` tells whether the lane
+// belongs to one of the top_groups groups of the largest group score (ties to
+// the lower index).  score(a, b): the group score of a group's best two.
+// Returns false where a group that stays and one that does not are nearer than
+// twice the tolerance and not alike (`exact`: equal keys are equal scores).
+template <int LPT, typename Score, typename Tol>
+__device__ __forceinline__ bool keep_groups(float a, float b, const RouteShape& g, Score score, bool exact, Tol tol,
+                                            bool& kept) {
+    const int lane = threadIdx.x & (LPT - 1), mine = lane / g.lanes_per_group;
+    const int first = threadIdx.x & 63 & ~(LPT - 1);  // the token's first lane of the wave
+    for (int d = 1; d < g.lanes_per_group; d <<= 1) {
+        const float a2 = __shfl_xor(a, d), b2 = __shfl_xor(b, d);
+        b = fmaxf(fminf(a, a2), fmaxf(b, b2));
+        a = fmaxf(a, a2);
+    }
+    const float gs = score(a, b);
+    const bool is = mine < g.groups;
+    int ahead = 0;  // groups before the own one
+    for (int o = 0; o < g.groups; ++o) {
+        const float q = __shfl(gs, first + o * g.lanes_per_group);
+        ahead += (q > gs || (q == gs && o < mine)) ? 1 : 0;
+    }
+    kept = is && ahead < g.top_groups;
+    const float none = -__builtin_inff();
+    const float least = -lanes_max<LPT>(kept ? -gs : none), most = lanes_max<LPT>(is && !kept ? gs : none);
+    const bool near = least - most <= 2.0f * tol(fmaxf(fabsf(least), fabsf(most)));
+    if (!__any(near)) return true;
+    bool certain = true;
+    for (int o = 0; o < g.groups; ++o) {
+        const int at = first + o * g.lanes_per_group;
+        const float q = __shfl(gs, at), qa = __shfl(a, at), qb = __shfl(b, at);
+        const bool other = __shfl((int)kept, at) != (int)kept;
+        if (is && other && fabsf(q - gs) <= 2.0f * tol(fmaxf(fabsf(q), fabsf(gs))) && !(exact && qa == a && qb == b))
+            certain = false;
+    }
+    return certain;
+}
+
+// The n largest of the keys s (V a lane, -inf where there is none; used up),
+// ties to the lower index: lane j < n gets the j-th one's expert and key.
+// out: a row of LDS for the token.
 template <int LPT, int V>
-__device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int& id, float& weight) {
+__device__ __forceinline__ void choose(float s[V], int n, int base, int* out, int& id, float& key) {
+    const float none = -__builtin_inff();
+    const int lane = threadIdx.x & (LPT - 1);
+    const uint64_t lower = (1ull << lane) - 1;
+    key = none;
+    for (int it = 0; it < n; ++it) {
+        float m = s[0];
+#pragma unroll
+        for (int j = 1; j < V; ++j) m = fmaxf(m, s[j]);
+        const float M = lanes_max<LPT>(m);
+        const bool win = m == M && (own_bits<LPT>(__ballot(m == M)) & lower) == 0;
+        if (lane == it) key = M;
+        bool done = !win;
+        int at = 0;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const bool hit = !done && s[j] == M;
+            s[j] = hit ? none : s[j];
+            at = hit ? j : at;
+            done |= hit;
+        }
+        if (win) out[it] = base + at;
+    }
+    __builtin_amdgcn_wave_barrier();
+    id = lane < n ? out[lane] : 0;
+}
+
+// The choice of one token by binary64 scores, by a whole wave: lane
+// `to` + j gets the j-th chosen expert.  score: a row of LDS (experts doubles).
+__device__ __forceinline__ void choose_exactly(const RouteArgs& a, int64_t t, double* score, int to, int& id) {
+    const RouteShape& g = a.shape;
+    const int lane = threadIdx.x & 63, E = g.experts;
+    const double none = -__builtin_inf();
+    const int64_t row = t * a.ld;
+    float m = kLowest;
+    double total = 1.0;
+    if (!a.sigmoid) {
+        for (int e = lane; e < E; e += 64) m = fmaxf(m, logit(load1(a.logits, a.bf16, row + e)));
+        m = lanes_max<64>(m);
+        total = 0.0;
+    }
+#pragma unroll 1
+    for (int e = lane; e < E; e += 64) {
+        const double x = (double)logit(load1(a.logits, a.bf16, row + e));
+        const double v = exp(a.sigmoid ? -x : x - (double)m);
+        score[e] = a.sigmoid ? 1.0 / (1.0 + v) : v;
+        if (!a.sigmoid) total += v;
+    }
+    if (!a.sigmoid) {
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d);
+    }
+    for (int e = lane; e < E; e += 64) {
+        const double p = score[e] / total;
+        score[e] = a.bias ? comparable(p + (double)a.bias[e]) : p;
+    }
+    __builtin_amdgcn_wave_barrier();
+    if (g.top_groups < g.groups) {
+        double best = none, second = none;
+        if (lane < g.groups)
+            for (int e = lane * g.group_size; e < (lane + 1) * g.group_size; ++e) {
+                second = fmax(second, fmin(best, score[e]));
+                best = fmax(best, score[e]);
+            }
+        const double gs = g.group_top2 && second > none ? best + second : best;
+        int ahead = 0;
+        for (int o = 0; o < g.groups; ++o) {
+            const double q = __shfl(gs, o);
+            ahead += (q > gs || (q == gs && o < lane)) ? 1 : 0;
+        }
+        const uint64_t kept = __ballot(lane < g.groups && ahead < g.top_groups);
+        __builtin_amdgcn_wave_barrier();
+        for (int e = lane; e < E; e += 64)
+            if (!(kept >> (e / g.group_size) & 1)) score[e] = none;
+    }
+    // without a bias, the kept experts by their logits (their scores may
+    // underflow to ties)
+    if (!a.bias)
+        for (int e = lane; e < E; e += 64)
+            if (score[e] > none) score[e] = (double)logit(load1(a.logits, a.bf16, row + e));
+    for (int it = 0; it < g.top_k; ++it) {
+        double best = none;
+        int at = E;
+        for (int e = lane; e < E; e += 64)
+            if (score[e] > best) {
+                best = score[e];
+                at = e;
+            }
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const double o = __shfl_xor(best, d);
+            const int oat = __shfl_xor(at, d);
+            if (o > best || (o == best && oat < at)) {
+                best = o;
+                at = oat;
+            }
+        }
+        if (lane == to + it) id = at;
+        if ((at & 63) == lane) score[at] = none;
+    }
+    __builtin_amdgcn_wave_barrier();
+}
+
+// One wave's tokens, 64 / LPT of them: the caller's lane group has token t.
+// Returns lane j < top_k's chosen expert and weight.  out: a row of LDS for
+// the token; exact: one for the wave.
+template <int LPT, int V>
+__device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int* out, double* exact, int& id,
+                                            float& weight) {
     const RouteShape& g = a.shape;
     const int lane = threadIdx.x & (LPT - 1);
     const int grp = lane / g.lanes_per_group, li = lane % g.lanes_per_group;
     const int base = grp * g.group_size + li * V;
     const int have = grp < g.groups ? max(0, min(V, g.group_size - li * V)) : 0;
     const int64_t row = t * a.ld;
-    float l[V];
-    if constexpr (V >= 8) {
-#pragma unroll
-        for (int c = 0; c < V / 8; ++c) {
-            const int64_t at = row + base + 8 * c;
-            if (8 * c >= have)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) l[8 * c + j] = 0.0f;
-            else if (a.bf16) load_upto8(static_cast<const uint16_t*>(a.logits) + at, have - 8 * c, l + 8 * c);
-            else load_upto8(static_cast<const float*>(a.logits) + at, have - 8 * c, l + 8 * c);
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j) l[j] = j < have ? load1(a.logits, a.bf16, row + base + j) : 0.0f;
-    }
+    const float none = -__builtin_inff();
+    float s[V];
+    load_values<V>(static_cast<const char*>(a.logits) + (row + base) * (a.bf16 ? 2 : 4), a.bf16, have, s);
     float m = kLowest;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        l[j] = j < have ? logit(l[j]) : -__builtin_inff();
-        m = fmaxf(m, l[j]);
+        s[j] = j < have ? logit(s[j]) : none;
+        m = fmaxf(m, s[j]);
     }
-    const bool softmax = !a.sigmoid;
+    const bool softmax = !a.sigmoid, by_group = g.top_groups < g.groups;
     float total = 1.0f;
     if (softmax) {
         m = lanes_max<LPT>(m);
         if (a.bias || !a.renorm) {
             total = 0.0f;
+            // (not renormalised: the sum is part of the weights)
 #pragma unroll
-            for (int j = 0; j < V; ++j) total += exp_diff(l[j], m);
+            for (int j = 0; j < V; ++j) total += a.renorm ? quick_exp(s[j] - m) : exp_diff(s[j], m);
             total = lanes_reduce<LPT>(total, AddOp());
         }
     }
-    // Without a bias the scores grow with the logits, so single experts (and
-    // groups judged by their best one) are compared by the logits themselves,
-    // exactly.  Elsewhere binary32 scores decide wherever they are further
-    // apart than twice their error, and a wave with a nearer pair takes them
-    // in binary64 (16384 tokens of 256 experts with a bias: a few waves).
-    const bool by_group = g.top_groups < g.groups;
-    const bool need_scores = a.bias || (by_group && g.group_top2);
-    const float none = -__builtin_inff();
-    bool kept = true, certain = true;
-    float s[V];
+    // Without a bias the scores grow with the logits: those are the keys, and
+    // decide exactly.  With one, binary32 scores do wherever they are further
+    // apart than their error, and a token with a nearer pair is chosen in
+    // binary64 (16384 tokens of 256 experts: some tens), unless the pair has
+    // equal logits and biases.
+    const float inv_total = 1.0f / total;
+    const Tolerance tol = {softmax ? 0x1p-17f * (a.bias ? inv_total : 1.0f) : 0x1p-20f};
+    if (a.bias) {
+        float b[V];
+        load_values<V>(a.bias + base, false, have, b);
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        s[j] = l[j];
-        if (need_scores && j < have) {
-            const float p = softmax ? exp_diff(l[j], m) / total : sigmoid32(l[j]);
-            s[j] = a.bias ? comparable(p + a.bias[base + j]) : p;
+        for (int j = 0; j < V; ++j) {
+            const float p = softmax ? quick_exp(s[j] - m) * inv_total : quick_sigmoid(s[j]);
+            s[j] = j < have ? comparable(p + b[j]) : none;
         }
     }
-    // sigmoid: p <= 1 within 2^-22; softmax: p = e / total, the sum's relative
-    // error (at most 2^-19) common to all p <= 1 / total
-    const float abs_tol = softmax ? 0x1p-18f / total : 0x1p-20f;
-    const auto tol = [=](float x) { return need_scores ? abs_tol + 0x1p-20f * x : -1.0f; };
+    bool certain = true;
     if (by_group) {
-        certain = keep_groups<float, LPT, V>(s, g, [=](float x) { return 2.0f * tol(x); }, kept);
-#pragma unroll
-        for (int j = 0; j < V; ++j) s[j] = !kept ? none : a.bias ? s[j] : l[j];
-    }
-    if (a.bias) certain &= choose<float, LPT, V>(s, g, base, tol, id);
-    if (__any(!certain)) {
-        const double nothing = -__builtin_inf();
-        double sd[V];
-        double tot = 0.0;
+        float best = none, second = none;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const double x = (double)l[j];
-            sd[j] = j >= have ? 0.0 : softmax ? exp(x - (double)m) : 1.0 / (1.0 + exp(-x));
-            tot += sd[j];
+            second = fmaxf(second, fminf(best, s[j]));
+            best = fmaxf(best, s[j]);
         }
-        tot = lanes_sum<LPT>(tot);
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const double p = softmax ? sd[j] / tot : sd[j];
-            sd[j] = j >= have ? nothing : a.bias ? comparable(p + (double)a.bias[base + j]) : p;
-        }
-        const auto exact = [](double) { return -1.0; };
-        if (by_group) keep_groups<double, LPT, V>(sd, g, exact, kept);
-        if (a.bias) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) sd[j] = kept ? sd[j] : nothing;
-            choose<double, LPT, V>(sd, g, base, exact, id);
+        bool kept;
+        if (!g.group_top2 && !a.bias) {
+            keep_groups<LPT>(best, second, g, [](float x, float) { return x; }, true, [](float) { return -1.0f; }, kept);
+        } else if (a.bias) {
+            const bool two = g.group_top2;
+            certain = keep_groups<LPT>(best, second, g, [=](float x, float y) { return two && y > none ? x + y : x; }, false,
+                                       tol, kept);
         } else {
+            const auto p = [=](float l) { return softmax ? quick_exp(l - m) : quick_sigmoid(l); };
+            certain = keep_groups<LPT>(best, second, g, [=](float x, float y) { return y > none ? p(x) + p(y) : p(x); }, true,
+                                       tol, kept);
+        }
 #pragma unroll
-            for (int j = 0; j < V; ++j) s[j] = kept ? l[j] : none;
+        for (int j = 0; j < V; ++j) s[j] = kept ? s[j] : none;
+    }
+    // (with a bias one more, to see how far the next one is behind)
+    float key;
+    choose<LPT, V>(s, a.bias ? g.top_k + 1 : g.top_k, base, out, id, key);
+    if (a.bias) {
+        const float ahead = __shfl_up(key, 1, LPT);
+        const int before = __shfl_up(id, 1, LPT);
+        bool near = lane > 0 && lane <= g.top_k && key > none && ahead - key <= tol(fmaxf(fabsf(ahead), fabsf(key)));
+        if (__any(near)) {
+            if (near)
+                near = !(load1(a.logits, a.bf16, row + id) == load1(a.logits, a.bf16, row + before) &&
+                         a.bias[id] == a.bias[before]);
+            certain &= own_bits<LPT>(__ballot(near)) == 0;
         }
     }
-    if (!a.bias) choose<float, LPT, V>(s, g, base, [](float) { return -1.0f; }, id);
+    // a token whose lanes are not all certain
+    uint64_t open = __ballot(!certain);
+    while (open) {
+        const int u = (__ffsll((unsigned long long)open) - 1) & ~(LPT - 1);  // its first lane
+        choose_exactly(a, __shfl(t, u), exact, u, id);
+        open = LPT == 64 ? 0 : open & ~(0xFFFFull << u);
+    }
     // the chosen scores from their logits
     const bool mine = lane < g.top_k;
-    const float lc = mine ? logit(load1(a.logits, a.bf16, row + id)) : -__builtin_inff();
-    float p;
+    const float lc = mine ? logit(load1(a.logits, a.bf16, row + id)) : none;
     if (a.renorm) {
         const float mc = lanes_max<LPT>(lc);
         // sigmoids so small that their logits' exponentials are the same to
         // 2^-64 are normalised as those (binary32 would underflow)
         const bool by_exp = softmax || mc < -64.0f;
-        p = !mine ? 0.0f : by_exp ? exp_diff(lc, mc) : sigmoid32(lc);
-        p = p / lanes_reduce<LPT>(p, AddOp());
+        const float p = !mine ? 0.0f : by_exp ? exp_diff(lc, mc) : sigmoid32(lc);
+        weight = p / lanes_reduce<LPT>(p, AddOp());
     } else {
-        p = !mine ? 0.0f : softmax ? exp_diff(lc, m) / total : sigmoid32(lc);
-    }
-    weight = p;
-}
-
-// Chosen experts and weights of tokens [t0, t1) by one workgroup of 256
-// threads, counted by expert into count[] (LDS, cleared here) when given.
-template <int LPT, int V>
-__device__ __forceinline__ void route_span(const RouteArgs& a, int64_t t0, int64_t t1, int* count) {
-    constexpr int TPB = 256 / LPT;
-    const RouteShape& g = a.shape;
-    if (count) {
-        for (int e = threadIdx.x; e < g.experts; e += 256) count[e] = 0;
-        __syncthreads();
-    }
-    const int lane = threadIdx.x & (LPT - 1);
-    for (int64_t t = t0 + threadIdx.x / LPT; t - threadIdx.x / LPT < t1; t += TPB) {
-        int id;
-        float w;
-        route_token<LPT, V>(a, t < t1 ? t : t1 - 1, id, w);
-        if (t < t1 && lane < g.top_k) {
-            a.ids[t * g.top_k + lane] = id;
-            a.weights[t * g.top_k + lane] = w;
-            if (count) atomicAdd(count + id, 1);  // (integer: the order does not matter)
-        }
+        weight = !mine ? 0.0f : softmax ? exp_diff(lc, m) / total : sigmoid32(lc);
     }
 }
 
-// Exclusive prefix sum of v[0 .. n) in LDS by 256 threads, in place; returns
-// the total.  tmp: 256 ints.
+// Exclusive prefix sum of v[0 .. n) in LDS by the workgroup, in place; returns
+// the total.  tmp: an int for each wave.
 __device__ __forceinline__ int exclusive_scan(int* v, int n, int* tmp) {
-    const int per = (n + 255) / 256, b = threadIdx.x * per;
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    const int per = (n + blockDim.x - 1) / blockDim.x, b = threadIdx.x * per;
     int sum = 0;
     for (int j = 0; j < per; ++j)
         if (b + j < n) sum += v[b + j];
-    tmp[threadIdx.x] = sum;
-    __syncthreads();
-    for (int d = 1; d < 256; d <<= 1) {
-        const int x = threadIdx.x >= d ? tmp[threadIdx.x - d] : 0;
-        __syncthreads();
-        tmp[threadIdx.x] += x;
-        __syncthreads();
+    int upto = sum;  // over the wave's lanes up to the own one
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int x = __shfl_up(upto, d);
+        if (lane >= d) upto += x;
     }
-    int run = tmp[threadIdx.x] - sum;
-    const int total = tmp[255];
+    if (lane == 63) tmp[wv] = upto;
+    __syncthreads();
+    int run = upto - sum, total = 0;
+    for (int w = 0; w < waves; ++w) {
+        const int x = tmp[w];
+        if (w < wv) run += x;
+        total += x;
+    }
     for (int j = 0; j < per; ++j)
         if (b + j < n) {
             const int x = v[b + j];
@@ -320,98 +404,159 @@ __device__ __forceinline__ int exclusive_scan(int* v, int n, int* tmp) {
     return total;
 }
 
-// Sorted places of assignments [a0, a1), next[e] (LDS) the place of the next
-// assignment of expert e.  Each wave finds, for its 64 assignments, the lanes
-// of the same expert by one ballot per bit of the expert's index; a table of
-// the four waves' counts puts the waves in order.  wave_count: 4 * experts
-// ints, zero.
-__device__ __forceinline__ void place_span(const RouteArgs& a, int64_t a0, int64_t a1, int* next, int* wave_count) {
-    const int E = a.shape.experts, lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-    for (int64_t c = a0; c < a1; c += 256) {
-        const int64_t i = c + threadIdx.x;
-        const bool in = i < a1;
-        const int id = in ? a.ids[i] : 0;
-        uint64_t same = __ballot(in);
-        for (int b = 1; b < E; b <<= 1) {
-            const uint64_t m = __ballot((id & b) != 0);
-            same &= (id & b) ? m : ~m;
-        }
-        const int rank = __popcll(same & ((1ull << lane) - 1)), n = __popcll(same);
-        const bool leader = in && rank == 0;
-        if (leader) wave_count[wv * E + id] = n;
+// Experts of a row of counts (bytes), rounded up so that rows are 16-byte aligned.
+__host__ __device__ __forceinline__ int count_row(int experts) { return (experts + 15) / 16 * 16; }
+
+// LDS of k_route, in 4-byte words: a row of choices for each token, a row of
+// binary64 scores for each wave; with the plan a count and a mask of 64 tokens
+// for each expert and a word for each wave.
+__host__ __device__ __forceinline__ int route_lds_words(int experts, int waves, int lpt, bool plan) {
+    return waves * (64 / lpt * (kMaxTopK + 1) + 2 * (experts + 1)) + (plan ? 3 * experts + waves : 0);
+}
+
+extern __shared__ __attribute__((aligned(16))) int route_lds[];
+
+// The choice over the tokens of span blockIdx.x, 64 / LPT for each wave at a
+// time.  With the plan, position gets the rank of each assignment among those
+// of its expert in the span (the experts of a token are distinct: the bits of
+// the tokens before it in the expert's mask, and the count of earlier rounds),
+// and counts[span][expert] their number; a lone workgroup (few tokens: a
+// second launch would cost more than its work) goes on to the sorted places.
+template <int LPT, int V>
+__global__ void __launch_bounds__(1024) k_route(const RouteArgs a) {
+    const int E = a.shape.experts, k = a.shape.top_k;
+    const int wave = threadIdx.x >> 6, waves = blockDim.x >> 6, lane = threadIdx.x & (LPT - 1);
+    const int u = threadIdx.x / LPT, round = blockDim.x / LPT;
+    double* exact = reinterpret_cast<double*>(route_lds) + wave * (E + 1);
+    int* out = route_lds + 2 * waves * (E + 1) + u * (kMaxTopK + 1);
+    int* count = route_lds + 2 * waves * (E + 1) + round * (kMaxTopK + 1);
+    uint32_t* mask = reinterpret_cast<uint32_t*>(count + E);  // low and high words
+    int* tmp = count + 3 * E;
+    const bool plan = a.offsets != nullptr;
+    const int64_t t0 = (int64_t)blockIdx.x * a.span, t1 = min(t0 + a.span, a.tokens);
+    if (plan) {
+        for (int e = threadIdx.x; e < 3 * E; e += blockDim.x) count[e] = 0;
         __syncthreads();
-        if (in) {
-            int p = next[id] + rank;
-            for (int w = 0; w < wv; ++w) p += wave_count[w * E + id];
-            a.position[i] = p;
-            a.order[p] = (int)i;
+    }
+    for (int64_t r = t0; r < t1; r += round) {
+        const int64_t t = r + u;
+        int id = 0;
+        float w;
+        // (tokens past the end repeat the last one)
+        route_token<LPT, V>(a, min(t, t1 - 1), out, exact, id, w);
+        const bool mine = t < t1 && lane < k;
+        if (mine) {
+            a.ids[t * k + lane] = id;
+            a.weights[t * k + lane] = w;
+            if (plan) atomicOr(mask + 2 * id + (u >> 5), 1u << (u & 31));  // (the order does not matter)
+        }
+        if (!plan) continue;
+        __syncthreads();
+        if (mine) {
+            const uint32_t lo = mask[2 * id], hi = mask[2 * id + 1], below = (1u << (u & 31)) - 1;
+            a.position[t * k + lane] =
+                count[id] + (u < 32 ? __popc(lo & below) : __popc(lo) + __popc(hi & below));
         }
         __syncthreads();
-        if (leader) {
-            atomicAdd(next + id, n);
-            wave_count[wv * E + id] = 0;
+        for (int e = threadIdx.x; e < E; e += blockDim.x) {
+            count[e] += __popc(mask[2 * e]) + __popc(mask[2 * e + 1]);
+            mask[2 * e] = mask[2 * e + 1] = 0;
         }
         __syncthreads();
     }
-}
-
-extern __shared__ int route_lds[];
-
-// Choice over the tokens of span blockIdx.x, and counts[span][expert] for the
-// plan.  A lone workgroup (few tokens: a second launch would cost more than
-// its work) goes on to the sorted places itself.
-template <int LPT, int V>
-__global__ void __launch_bounds__(256) k_route(const RouteArgs a) {
-    const int E = a.shape.experts;
-    const int64_t t0 = (int64_t)blockIdx.x * a.span, t1 = min(t0 + a.span, a.tokens);
-    int* count = a.offsets ? route_lds : nullptr;
-    route_span<LPT, V>(a, t0, t1, count);
-    if (!count) return;
-    __syncthreads();  // (and the chosen ids, written by this workgroup, are read back below)
+    if (!plan) return;
     if (gridDim.x > 1) {
-        for (int e = threadIdx.x; e < E; e += 256) a.counts[(int64_t)blockIdx.x * E + e] = count[e];
+        const int row = count_row(E);
+        uint8_t* counts = a.counts + (int64_t)blockIdx.x * row;
+        for (int e = threadIdx.x; e < row; e += blockDim.x) counts[e] = e < E ? (uint8_t)count[e] : (uint8_t)0;
         return;
     }
-    int* waves = count + E;
-    int* tmp = waves + 4 * E;
-    for (int e = threadIdx.x; e < 4 * E; e += 256) waves[e] = 0;
     const int sum = exclusive_scan(count, E, tmp);
-    for (int e = threadIdx.x; e < E; e += 256) a.offsets[e] = count[e];
+    for (int e = threadIdx.x; e < E; e += blockDim.x) a.offsets[e] = count[e];
     if (threadIdx.x == 0) a.offsets[E] = sum;
-    place_span(a, 0, a.tokens * a.shape.top_k, count, waves);
+    for (int i = threadIdx.x; i < a.tokens * k; i += blockDim.x) {  // (ids and ranks of this workgroup's own)
+        const int p = count[a.ids[i]] + a.position[i];
+        a.position[i] = p;
+        a.order[p] = i;
+    }
 }
 
-// Sorted places of span blockIdx.x's assignments: every workgroup sums the
-// spans' counts itself (all of them for the experts' offsets, those before it
-// for its own places) instead of waiting for a scan in a launch between.
-__global__ void __launch_bounds__(256) k_route_places(const RouteArgs a, int spans) {
-    const int E = a.shape.experts;
-    int* total = route_lds;       // E: assignments of each expert, then its first place
-    int* before = total + E;      // E: those of earlier spans, then the next place
-    int* waves = before + E;      // 4 E
-    int* tmp = waves + 4 * E;     // 256
-    for (int e = threadIdx.x; e < E; e += 256) {
-        int all = 0, pre = 0;
+// Parts of the spans that k_route_places sums side by side.
+__host__ __device__ __forceinline__ int route_parts(int row) { return min(1024 / (row / 4), 32); }
+
+// Sorted places of the assignments of spans [blockIdx.x * a.group, + a.group):
+// every workgroup sums the spans' counts itself (all of them for the experts'
+// offsets, those before its own for its places) instead of waiting for a scan
+// in a launch between.  A thread sums 4 experts (a word of bytes, as two pairs
+// of 16 bits) over one part of the spans; the parts are added through LDS.
+__global__ void __launch_bounds__(1024) k_route_places(const RouteArgs a, int spans) {
+    const int E = a.shape.experts, k = a.shape.top_k, row = count_row(E), words = row / 4, parts = route_parts(row);
+    int* total = route_lds;     // assignments of each expert, then its first place
+    int* before = total + row;  // those of earlier spans, then the next place
+    int* tmp = before + row;    // 16
+    int* all_of = tmp + 16;     // parts x row
+    int* pre_of = all_of + parts * row;
+    const int first = blockIdx.x * a.group, c = threadIdx.x % words, part = threadIdx.x / words;
+    if (part < parts) {
+        const uint32_t* counts = reinterpret_cast<const uint32_t*>(a.counts) + c;
+        const int per = (spans + parts - 1) / parts, b0 = part * per, b1 = min(b0 + per, spans);
+        int sum[4] = {}, pre[4] = {};
+        const auto add = [&](int b, int end) {
+            while (b < end) {
+                uint32_t even = 0, odd = 0;
+                const int stop = min(end, b + 256);
 #pragma unroll 8
-        for (int b = 0; b < spans; ++b) {
-            const int n = a.counts[(int64_t)b * E + e];
-            all += n;
-            pre += b < (int)blockIdx.x ? n : 0;
+                for (; b < stop; ++b) {
+                    const uint32_t w = counts[(int64_t)b * words];
+                    even += w & 0x00FF00FFu;
+                    odd += (w >> 8) & 0x00FF00FFu;
+                }
+                sum[0] += even & 0xFFFFu;
+                sum[1] += odd & 0xFFFFu;
+                sum[2] += even >> 16;
+                sum[3] += odd >> 16;
+            }
+        };
+        const int mid = max(b0, min(b1, first));
+        add(b0, mid);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) pre[j] = sum[j];
+        add(mid, b1);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            all_of[part * row + 4 * c + j] = sum[j];
+            pre_of[part * row + 4 * c + j] = pre[j];
         }
-        total[e] = all;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < row; e += blockDim.x) {
+        int sum = 0, pre = 0;
+#pragma unroll 8
+        for (int q = 0; q < parts; ++q) {
+            sum += all_of[q * row + e];
+            pre += pre_of[q * row + e];
+        }
+        total[e] = sum;
         before[e] = pre;
     }
-    for (int e = threadIdx.x; e < 4 * E; e += 256) waves[e] = 0;
     __syncthreads();
     const int sum = exclusive_scan(total, E, tmp);
-    for (int e = threadIdx.x; e < E; e += 256) {
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
         before[e] += total[e];
         if (blockIdx.x == 0) a.offsets[e] = total[e];
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) a.offsets[E] = sum;
-    __syncthreads();
-    const int64_t t0 = (int64_t)blockIdx.x * a.span, t1 = min(t0 + a.span, a.tokens);
-    place_span(a, t0 * a.shape.top_k, t1 * a.shape.top_k, before, waves);
+    for (int b = first; b < min(first + a.group, spans); ++b) {
+        __syncthreads();
+        const int64_t i1 = min((b + 1) * a.span, a.tokens) * k;
+        for (int64_t i = b * a.span * k + threadIdx.x; i < i1; i += blockDim.x) {
+            const int p = before[a.ids[i]] + a.position[i];
+            a.position[i] = p;
+            a.order[p] = (int)i;
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < E; e += blockDim.x) before[e] += a.counts[(int64_t)b * row + e];
+    }
 }
 
 // ---------------------------------------------------------------- backward
@@ -518,36 +663,50 @@ inline int64_t r_cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // Lanes per token and values per lane for a routing shape; {0, 0} when the
 // groups do not fit.  A group's experts lie on LPT / (groups rounded up to a
 // power of two) lanes, in index order, so that the lowest lane and the lowest
-// value among equal ones is the lowest expert.
+// value among equal ones is the lowest expert.  16 lanes do less work a token,
+// 64 come to its end sooner: those where the tokens are few.
 struct LaneShape {
     int lpt, v, per_group;
 };
-LaneShape lane_shape(int experts, int groups) {
+LaneShape lane_shape(int experts, int groups, int top_k, int64_t tokens) {
     int slots = 1;
     while (slots < groups) slots *= 2;
     for (int lpt : {16, 64}) {
-        if (slots > lpt) continue;
+        if (slots > lpt || (lpt == 16 && (top_k >= 16 || tokens <= 256))) continue;
         const int per = lpt / slots, need = (int)r_cdiv(experts / groups, per);
-        for (int v : {2, 4, 8, 16, 32})
-            if (need <= v) return {lpt, lpt == 64 ? std::max(v, 8) : v, per};
+        for (int v : {2, 4, 8, 16, 32}) {
+            if (lpt == 16 ? v > 16 : v < 4) continue;
+            if (need <= v) return {lpt, v, per};
+        }
     }
     return {0, 0, 0};
 }
 
-// Tokens of one workgroup's span: a multiple of 16, at most 256 spans.
-int64_t route_span_tokens(int64_t tokens) { return r_cdiv(r_cdiv(tokens, 256), 16) * 16; }
+// Threads of a workgroup: as many as have their waves' rows of binary64 scores
+// in 32 KiB of LDS.
+int route_threads(int experts) { return experts <= 256 ? 1024 : experts <= 512 ? 512 : experts <= 1024 ? 256 : 128; }
 
-constexpr int64_t kSmallTokens = 32;  // one workgroup takes both steps up to here
+// Tokens of a span: a round of its workgroup, or as many rounds as leave at
+// most 256 spans, but no more than a byte counts.
+int64_t route_span_tokens(int64_t tokens, int round) {
+    return std::min<int64_t>(r_cdiv(r_cdiv(tokens, 256), round) * round, 192);
+}
 
 template <int LPT, int V>
 hipError_t route_shaped(RouteArgs a, hipStream_t s) {
-    const size_t E = (size_t)a.shape.experts;
-    a.span = a.tokens <= kSmallTokens ? a.tokens : route_span_tokens(a.tokens);
+    const int E = a.shape.experts;
+    int threads = route_threads(E);
+    if (a.tokens * LPT < threads) threads = std::max<int>((int)r_cdiv(a.tokens * LPT, 64) * 64, std::min(threads, 256));
+    const int round = threads / LPT;
+    a.span = route_span_tokens(a.tokens, round);
     const int spans = (int)r_cdiv(a.tokens, a.span);
-    hipLaunchKernelGGL((k_route<LPT, V>), dim3((unsigned)spans), dim3(256), (5 * E + 256) * sizeof(int), s, a);
+    hipLaunchKernelGGL((k_route<LPT, V>), dim3((unsigned)spans), dim3(threads),
+                       route_lds_words(E, threads / 64, LPT, a.offsets != nullptr) * sizeof(int), s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.offsets || spans == 1) return e;
-    hipLaunchKernelGGL(k_route_places, dim3((unsigned)spans), dim3(256), (6 * E + 256) * sizeof(int), s, a, spans);
+    a.group = (int)r_cdiv(spans, 256);
+    hipLaunchKernelGGL(k_route_places, dim3((unsigned)r_cdiv(spans, a.group)), dim3(1024),
+                       (2 * count_row(E) * (1 + route_parts(count_row(E))) + 16) * sizeof(int), s, a, spans);
     return hipGetLastError();
 }
 
@@ -557,11 +716,11 @@ hipError_t route_lanes(const RouteArgs& a, LaneShape ls, hipStream_t s) {
             case 2: return route_shaped<16, 2>(a, s);
             case 4: return route_shaped<16, 4>(a, s);
             case 8: return route_shaped<16, 8>(a, s);
-            case 16: return route_shaped<16, 16>(a, s);
-            default: return route_shaped<16, 32>(a, s);
+            default: return route_shaped<16, 16>(a, s);
         }
     }
     switch (ls.v) {
+        case 4: return route_shaped<64, 4>(a, s);
         case 8: return route_shaped<64, 8>(a, s);
         case 16: return route_shaped<64, 16>(a, s);
         default: return route_shaped<64, 32>(a, s);
@@ -589,11 +748,12 @@ __global__ void k_zero_offsets(int64_t* offsets, int n) {
 
 }  // namespace
 
-bool route_shape_fits(int experts, int groups) { return lane_shape(experts, groups).lpt != 0; }
+bool route_shape_fits(int experts, int groups) { return lane_shape(experts, groups, kMaxTopK, 1).lpt != 0; }
 
-int64_t route_workspace_ints(int64_t tokens, int experts) {
-    if (tokens <= kSmallTokens) return 0;
-    return r_cdiv(tokens, route_span_tokens(tokens)) * experts;
+size_t route_workspace_bytes(int64_t tokens, int experts) {
+    // (a workgroup's round is least with 64 lanes a token)
+    const int round = route_threads(experts) / 64;
+    return tokens <= round ? 0 : (size_t)(r_cdiv(tokens, route_span_tokens(tokens, round)) * count_row(experts));
 }
 
 hipError_t launch_route(RouteArgs a, hipStream_t s) {
@@ -602,7 +762,7 @@ hipError_t launch_route(RouteArgs a, hipStream_t s) {
         hipLaunchKernelGGL(k_zero_offsets, dim3(1), dim3(64), 0, s, a.offsets, a.shape.experts + 1);
         return hipGetLastError();
     }
-    const LaneShape ls = lane_shape(a.shape.experts, a.shape.groups);
+    const LaneShape ls = lane_shape(a.shape.experts, a.shape.groups, a.shape.top_k, a.tokens);
     a.shape.lanes_per_group = ls.per_group;
     return route_lanes(a, ls, s);
 }

@@ -623,7 +623,7 @@ def nvfp4_route(logits, top_k, bias=None, score=NVFP4_ROUTE_SOFTMAX, groups=1, t
     b = None if bias is None else _flat("bias", bias, experts, torch.float32, logits)
     if workspace is None and plan:
         need = lib.nvfp4_route_workspace_size(tokens, experts)
-        workspace = torch.empty(need // 4, dtype=torch.int32, device=dev) if need else None
+        workspace = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
     opts = CRouteOpts(top_k, score, groups, top_groups, group_score, 1 if renorm else 0, b)
     st = lib.nvfp4_route(
         logits.data_ptr(), code, tokens, experts, ld, ctypes.byref(opts), pi, pw, pf, po, pp,
