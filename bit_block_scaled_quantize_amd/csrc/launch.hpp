@@ -189,6 +189,7 @@ struct GemvArgs {
     int assignments, top_k, experts;
     bool x_per_assignment;
     bool x_bf16, y_bf16, scale_2d, mx;
+    int rows;  // of x at a time; set by the launcher
 };
 hipError_t launch_gemv(const GemvArgs& p, bool swiglu, hipStream_t s);
 // weights NULL: a row of y for each assignment; else their weighted sums, by

@@ -560,7 +560,7 @@ nvfp4_status nvfp4_gemv(const void* x, int32_t dt /* nvfp4_dtype */, int64_t m, 
     if (st != NVFP4_OK) return st;
     if (m > kMaxGemvRows) return NVFP4_ERR_UNSUPPORTED;
     GemvArgs p = {x, m, ldx, W->codes, W->scales, W->tensor_scale, W->rows, W->cols, y, ldy, nullptr, 0, 1, 0, false,
-                  dt == NVFP4_BF16, y_dt == NVFP4_BF16, W->scale_mode == NVFP4_SCALE_2D, false};
+                  dt == NVFP4_BF16, y_dt == NVFP4_BF16, W->scale_mode == NVFP4_SCALE_2D, false, 0};
     const hipError_t e = launch_gemv(p, ep == NVFP4_EPI_SWIGLU, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
 }
@@ -578,7 +578,7 @@ nvfp4_status nvfp4_mx_gemv(const void* x, int32_t dt /* nvfp4_dtype */, int64_t 
     if (st != NVFP4_OK) return st;
     if (W->elem != NVFP4_MX_E2M1 || m > kMaxGemvRows) return NVFP4_ERR_UNSUPPORTED;
     GemvArgs p = {x, m, ldx, W->codes, W->scales, nullptr, W->rows, W->cols, y, ldy, nullptr, 0, 1, 0, false,
-                  dt == NVFP4_BF16, y_dt == NVFP4_BF16, false, true};
+                  dt == NVFP4_BF16, y_dt == NVFP4_BF16, false, true, 0};
     const hipError_t e = launch_gemv(p, false, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
 }
@@ -615,7 +615,7 @@ nvfp4_status nvfp4_expert_gemv(const void* x, int32_t dt /* nvfp4_dtype */, int6
         if (!aligned(ws, 16)) return NVFP4_ERR_ALIGN;
     }
     GemvArgs p = {x, x_rows, ldx, W->codes, W->scales, W->tensor_scale, N, W->cols, y, ldy, ids, (int)assignments, top_k,
-                  experts, x_rows != tokens, dt == NVFP4_BF16, y_dt == NVFP4_BF16, W->scale_mode == NVFP4_SCALE_2D, false};
+                  experts, x_rows != tokens, dt == NVFP4_BF16, y_dt == NVFP4_BF16, W->scale_mode == NVFP4_SCALE_2D, false, 0};
     const hipError_t e = launch_expert_gemv(p, ep == NVFP4_EPI_SWIGLU, weights, static_cast<float*>(ws),
                                             static_cast<hipStream_t>(stream));
     return e == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
