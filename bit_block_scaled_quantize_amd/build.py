@@ -1,4 +1,6 @@
-"""Build libnvfp4.so (the HIP kernels + C ABI) in-tree for gfx950 with hipcc.
+"""Build libnvfp4.so (the HIP kernels + C ABI) in-tree for gfx950 with hipcc,
+and _native.so, the Python binding of the MoE-block operators, against it with
+the host compiler.
 
 Flags that matter for correctness:
   -ffp-contract=off            every a*b+c rounds twice, as the format's
@@ -12,16 +14,19 @@ Flags that matter for correctness:
                                no packed FP32 instructions are generated.
 """
 import concurrent.futures
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libnvfp4.so")
+BINDING = os.path.join(HERE, "_native.so")
 BUILD = os.path.join(HERE, "_build")
 SOURCES = ["quantize.hip", "gemm.hip", "mx.hip", "mx_gemm.hip", "norm.hip", "route.hip", "gemv.hip", "nvfp4_api.hip"]
 ARCH = os.environ.get("NVFP4_OFFLOAD_ARCH", "gfx950")
@@ -55,17 +60,47 @@ def _compile(src):
     return obj
 
 
+def _compile_binding():
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        raise RuntimeError("no host C++ compiler found; the Python binding cannot be built")
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    inc = os.path.join(torch_dir, "include")
+    obj = os.path.join(BUILD, "binding.o")
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall", "-Wno-unused-function", "-I", INCLUDE,
+           "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cxx} failed for binding.cpp:\n{r.stdout}\n{r.stderr}")
+    return cxx, obj, os.path.join(torch_dir, "lib")
+
+
+def _link_binding(cxx, obj, torch_lib):
+    # torch is loaded before the module is imported; libnvfp4.so lies beside it
+    tmp = BINDING + ".tmp"
+    cmd = [cxx, "-shared", "-o", tmp, obj, "-L", HERE, "-l:libnvfp4.so", "-L", torch_lib, "-ltorch_python", "-ltorch_cpu",
+           "-lc10", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + torch_lib]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of the binding failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(verbose=False):
-    """Compile every source and link libnvfp4.so (always rebuilds)."""
+    """Compile every source and link libnvfp4.so and _native.so (always rebuilds)."""
     os.makedirs(BUILD, exist_ok=True)
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(_compile, SOURCES))
+        binding = binding.result()
     tmp = LIB + ".tmp"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(*binding)
     if verbose:
         print(LIB)
     return LIB

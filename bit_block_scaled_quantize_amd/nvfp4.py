@@ -1,4 +1,5 @@
-"""Thin ctypes binding of libnvfp4.so (include/nvfp4.h).
+"""Thin binding of libnvfp4.so (include/nvfp4.h): ctypes, and for the operators
+of a mixture-of-experts block the compiled module _native.
 
 Argument marshalling only: every step of quantize / dequantize / GEMM runs in
 the HIP kernels behind the C ABI.  PyTorch supplies device memory (output
@@ -126,6 +127,10 @@ def _load():
 
 
 lib = _load()
+try:
+    from . import _native  # (linked against the library just loaded)
+except ImportError as e:
+    raise ImportError("the Python binding _native.so is not built; run bit_block_scaled_quantize_amd/build.py") from e
 
 
 class NVFP4Error(RuntimeError):
@@ -452,37 +457,12 @@ def nvfp4_mx_gemm(A, B, out_dtype=torch.float32, out=None, accum=NVFP4_MX_ACC_NA
 
 
 # ---------------------------------------------------------------- MoE-block operators
-def _launch_stream(t, stream):
-    """Raw handle of the stream a call on the tensors of t's device runs on."""
-    dev = t.get_device()
-    if dev < 0 or dev != torch._C._cuda_getDevice():
-        raise ValueError(f"the tensors must be on the current GPU, got {t.device}")
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+# (checks, allocation and the calls themselves in csrc/binding.cpp)
+_native.setup(NVFP4Error, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
 
 
-def _matrix(name, t, rows=None, cols=None, dtype=None, like=None):
-    """Leading dimension of a 2-D tensor with unit column stride, checked."""
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
-        raise ValueError(f"{name} must be a matrix with unit column stride")
-    r, c = t.shape
-    if (rows is not None and r != rows) or (cols is not None and c != cols):
-        raise ValueError(f"{name} is {r} x {c}, expected {rows} x {cols}")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if like is not None and t.get_device() != like.get_device():
-        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
-    return t.stride(0) if r > 1 else max(c, t.stride(0))
-
-
-def _flat(name, t, numel, dtype, like):
-    """Address of a contiguous tensor of numel elements, checked."""
-    if t.numel() != numel or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous with {numel} elements")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.get_device() != like.get_device():
-        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
-    return t.data_ptr()
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 @dataclass
@@ -503,36 +483,17 @@ def nvfp4_rmsnorm(x, weight, residual=None, eps=1e-6, y=True, mx_elem=None, rstd
     returns 1 / sqrt(mean(h^2) + eps) per row for the backward pass.  out: an
     RMSNormOutput of preallocated tensors for what is asked for (out.h may be
     residual or x)."""
-    ldx = _matrix("x", x)
-    rows, cols = x.shape
-    dt = x.dtype
-    code = _dtype_code(dt)
-    w = _flat("weight", weight, cols, weight.dtype, x)
-    ldr = 0 if residual is None else _matrix("residual", residual, rows, cols, dt, x)
-    if out is None:
-        out = RMSNormOutput(x if residual is None else torch.empty((rows, cols), dtype=dt, device=x.device),
-                            torch.empty((rows, cols), dtype=dt, device=x.device) if y else None,
-                            None if mx_elem is None else MXTensor.empty(rows, cols, mx_elem, x.device),
-                            torch.empty((rows,), dtype=torch.float32, device=x.device) if rstd else None)
-    else:
-        out = RMSNormOutput(out.h if residual is not None else x, out.y if y else None,
-                            None if mx_elem is None else out.mx, out.rstd if rstd else None)
-    h = None if out.h is x and residual is None else out.h
-    ldh = 0 if h is None else _matrix("out.h", h, rows, cols, dt, x)
-    ldy = 0 if out.y is None else _matrix("out.y", out.y, rows, cols, dt, x)
-    mx = None
-    if out.mx is not None:
-        if out.mx.elem != mx_elem:
-            raise ValueError("out.mx has another element format than mx_elem")
-        _flat("out.mx.codes", out.mx.codes, rows * cols // (1 if mx_elem == NVFP4_MX_E4M3 else 2), torch.uint8, x)
-        _flat("out.mx.scales", out.mx.scales, rows * (cols // 32), torch.uint8, x)
-        mx = ctypes.byref(out.mx.c())
-    st = lib.nvfp4_rmsnorm(
-        x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr, w, _dtype_code(weight.dtype), code,
-        rows, cols, eps, None if h is None else h.data_ptr(), ldh, None if out.y is None else out.y.data_ptr(), ldy, mx,
-        None if out.rstd is None else _flat("out.rstd", out.rstd, rows, torch.float32, x), _launch_stream(x, stream))
-    _check("nvfp4_rmsnorm", st)
-    return out
+    oh = oy = codes = scales = orstd = None
+    if out is not None:
+        oh, oy, orstd = out.h, out.y, out.rstd
+        if mx_elem is not None and out.mx is not None:
+            if out.mx.elem != mx_elem:
+                raise ValueError("out.mx has another element format than mx_elem")
+            codes, scales = out.mx.codes, out.mx.scales
+    h, oy, codes, scales, orstd = _native.rmsnorm(x, weight, residual, eps, y, -1 if mx_elem is None else mx_elem, rstd,
+                                                  oh, oy, codes, scales, orstd, _handle(stream))
+    mx = None if codes is None else MXTensor(codes, scales, x.shape[0], x.shape[1], mx_elem)
+    return RMSNormOutput(x if residual is None else h, oy, mx, orstd)
 
 
 @_launches_on_stream
@@ -542,29 +503,7 @@ def nvfp4_rmsnorm_backward(dy, h, rstd, weight, dh=None, dx=None, dweight=None, 
     gradient that reaches h by the residual stream, dweight float32.  dx,
     dweight and workspace (nvfp4_rmsnorm_backward_workspace_size) may be
     preallocated."""
-    ldh = _matrix("h", h)
-    rows, cols = h.shape
-    dt = h.dtype
-    code = _dtype_code(dt)
-    lddy = _matrix("dy", dy, rows, cols, dt, h)
-    r = _flat("rstd", rstd, rows, torch.float32, h)
-    w = _flat("weight", weight, cols, weight.dtype, h)
-    lddh = 0 if dh is None else _matrix("dh", dh, rows, cols, dt, h)
-    if dx is None:
-        dx = torch.empty((rows, cols), dtype=dt, device=h.device)
-    lddx = _matrix("dx", dx, rows, cols, dt, h)
-    if dweight is None:
-        dweight = torch.empty((cols,), dtype=torch.float32, device=h.device)
-    dwp = _flat("dweight", dweight, cols, torch.float32, h)
-    if workspace is None:
-        need = lib.nvfp4_rmsnorm_backward_workspace_size(rows, cols)
-        workspace = torch.empty(need // 4, dtype=torch.float32, device=h.device)
-    st = lib.nvfp4_rmsnorm_backward(
-        dy.data_ptr(), lddy, h.data_ptr(), ldh, r, w, _dtype_code(weight.dtype), None if dh is None else dh.data_ptr(),
-        lddh, code, rows, cols, dx.data_ptr(), lddx, dwp, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _launch_stream(h, stream))
-    _check("nvfp4_rmsnorm_backward", st)
-    return dx, dweight
+    return _native.rmsnorm_backward(dy, h, rstd, weight, dh, dx, dweight, workspace, _handle(stream))
 
 
 def nvfp4_rmsnorm_backward_workspace_size(rows, cols):
@@ -597,40 +536,10 @@ def nvfp4_route(logits, top_k, bias=None, score=NVFP4_ROUTE_SOFTMAX, groups=1, t
     their weights.  plan=True also sorts the tokens * top_k assignments by
     expert (offsets feed nvfp4_grouped_gemm; order // top_k are the tokens to
     gather).  out: a RouteOutput of preallocated tensors."""
-    ld = _matrix("logits", logits)
-    tokens, experts = logits.shape
-    code = _dtype_code(logits.dtype)
-    dev = logits.device
-    n = tokens * top_k
-    if out is None:
-        i32 = torch.int32
-        out = RouteOutput(torch.empty((tokens, top_k), dtype=i32, device=dev),
-                          torch.empty((tokens, top_k), dtype=torch.float32, device=dev))
-        if plan:
-            out.offsets = torch.empty((experts + 1,), dtype=torch.int64, device=dev)
-            out.order = torch.empty((n,), dtype=i32, device=dev)
-            out.position = torch.empty((n,), dtype=i32, device=dev)
-        pi, pw = out.ids.data_ptr(), out.weights.data_ptr()
-        pf, po, pp = (out.offsets.data_ptr(), out.order.data_ptr(), out.position.data_ptr()) if plan else (None,) * 3
-    else:
-        pi = _flat("out.ids", out.ids, n, torch.int32, logits)
-        pw = _flat("out.weights", out.weights, n, torch.float32, logits)
-        pf = po = pp = None
-        if plan:
-            pf = _flat("out.offsets", out.offsets, experts + 1, torch.int64, logits)
-            po = _flat("out.order", out.order, n, torch.int32, logits)
-            pp = _flat("out.position", out.position, n, torch.int32, logits)
-    b = None if bias is None else _flat("bias", bias, experts, torch.float32, logits)
-    if workspace is None and plan:
-        need = lib.nvfp4_route_workspace_size(tokens, experts)
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
-    opts = CRouteOpts(top_k, score, groups, top_groups, group_score, 1 if renorm else 0, b)
-    st = lib.nvfp4_route(
-        logits.data_ptr(), code, tokens, experts, ld, ctypes.byref(opts), pi, pw, pf, po, pp,
-        None if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _launch_stream(logits, stream))
-    _check("nvfp4_route", st)
-    return out
+    o = (None,) * 5 if out is None else (out.ids, out.weights, out.offsets, out.order, out.position)
+    r = _native.route(logits, top_k, bias, score, groups, top_groups, group_score, renorm, plan, *o, workspace,
+                      _handle(stream))
+    return RouteOutput(*r) if out is None else out
 
 
 @_launches_on_stream
@@ -639,45 +548,11 @@ def nvfp4_route_backward(dweights, logits, ids, score=NVFP4_ROUTE_SOFTMAX, renor
     """Gradient of the logits from that of the chosen weights (float32
     [tokens, top_k]) and, optionally, of all scores (dscores float32 [tokens,
     experts], as of an auxiliary balance loss)."""
-    ld = _matrix("logits", logits)
-    tokens, experts = logits.shape
-    if ids.dim() != 2:
-        raise ValueError("ids must be tokens x top_k")
-    top_k = ids.shape[1]
-    code = _dtype_code(logits.dtype)
-    pi = _flat("ids", ids, tokens * top_k, torch.int32, logits)
-    pw = _flat("dweights", dweights, tokens * top_k, torch.float32, logits)
-    ldds = 0 if dscores is None else _matrix("dscores", dscores, tokens, experts, torch.float32, logits)
-    if out is None:
-        out = torch.empty((tokens, experts), dtype=logits.dtype, device=logits.device)
-    lddl = _matrix("out", out, tokens, experts, logits.dtype, logits)
-    st = lib.nvfp4_route_backward(
-        pw, logits.data_ptr(), code, tokens, experts, ld, pi, top_k, score, 1 if renorm else 0,
-        None if dscores is None else dscores.data_ptr(), ldds, out.data_ptr(), lddl, _launch_stream(logits, stream))
-    _check("nvfp4_route_backward", st)
-    return out
+    return _native.route_backward(dweights, logits, ids, score, renorm, dscores, out, _handle(stream))
 
 
-def _weight(w, like, n_scales=1):
-    """C form of a 4-bit weight (NVFP4Tensor or MXTensor), its arrays checked."""
-    rows, cols = w.rows, w.cols
-    if isinstance(w, MXTensor):
-        if w.elem != NVFP4_MX_E2M1:
-            raise ValueError("the weight must have E2M1 elements")
-        ns = rows * (cols // 32)
-    else:
-        ns = (rows // 16 if w.scale_mode == NVFP4_SCALE_2D else rows) * (cols // 16)
-        _flat("tensor_scale", w.tensor_scale, n_scales, torch.float32, like)
-    _flat("codes", w.codes, rows * (cols // 2), torch.uint8, like)
-    _flat("scales", w.scales, ns, torch.uint8, like)
-    return w.c()
-
-
-def _gemv_out(out, rows, cols, dtype, x):
-    if out is None:
-        return torch.empty((rows, cols), dtype=x.dtype if dtype is None else dtype, device=x.device)
-    _matrix("out", out, rows, cols, None, x)
-    return out
+def _code(dtype):
+    return -1 if dtype is None else _dtype_code(dtype)
 
 
 @_launches_on_stream
@@ -685,27 +560,14 @@ def nvfp4_gemv(x, w, epilogue=NVFP4_EPI_NONE, out_dtype=None, out=None, stream=N
     """x W^T of a few rows x (m x K, bfloat16 or float32, not quantized) and an
     NVFP4Tensor w (N x K): m x N in out_dtype (x's unless given); with
     NVFP4_EPI_SWIGLU (N = 2F) gate * sigmoid(gate) * up, m x F."""
-    ldx = _matrix("x", x, x.shape[0], w.cols)
-    m = x.shape[0]
-    c = _weight(w, x)
-    out = _gemv_out(out, m, w.rows // 2 if epilogue == NVFP4_EPI_SWIGLU else w.rows, out_dtype, x)
-    st = lib.nvfp4_gemv(x.data_ptr(), _dtype_code(x.dtype), m, ldx, ctypes.byref(c), out.data_ptr(),
-                        _dtype_code(out.dtype), _matrix("out", out), epilogue, _launch_stream(x, stream))
-    _check("nvfp4_gemv", st)
-    return out
+    return _native.gemv(x, w.codes, w.scales, w.tensor_scale, w.rows, w.cols, w.scale_mode, epilogue, _code(out_dtype),
+                        out, _handle(stream))
 
 
 @_launches_on_stream
 def nvfp4_mx_gemv(x, w, out_dtype=None, out=None, stream=None):
     """nvfp4_gemv for an MXFP4 weight (MXTensor with E2M1 elements)."""
-    ldx = _matrix("x", x, x.shape[0], w.cols)
-    m = x.shape[0]
-    c = _weight(w, x)
-    out = _gemv_out(out, m, w.rows, out_dtype, x)
-    st = lib.nvfp4_mx_gemv(x.data_ptr(), _dtype_code(x.dtype), m, ldx, ctypes.byref(c), out.data_ptr(),
-                           _dtype_code(out.dtype), _matrix("out", out), _launch_stream(x, stream))
-    _check("nvfp4_mx_gemv", st)
-    return out
+    return _native.mx_gemv(x, w.codes, w.scales, w.rows, w.cols, w.elem, _code(out_dtype), out, _handle(stream))
 
 
 def nvfp4_expert_gemv_workspace_size(tokens, top_k, n):
@@ -721,25 +583,5 @@ def nvfp4_expert_gemv(x, ids, w, experts, weights=None, epilogue=NVFP4_EPI_NONE,
     row for each token or for each assignment (tokens * top_k).  Without
     weights: a row of the result for each assignment; with weights (float32
     [tokens, top_k]): each token's weighted sum of its products."""
-    if ids.dim() != 2:
-        raise ValueError("ids must be tokens x top_k")
-    tokens, top_k = ids.shape
-    n = tokens * top_k
-    if x.dim() != 2 or x.shape[0] not in (tokens, n):
-        raise ValueError("x must have a row for each token or for each assignment")
-    ldx = _matrix("x", x, x.shape[0], w.cols)
-    c = _weight(w, x, experts)
-    cols = w.rows // experts // (2 if epilogue == NVFP4_EPI_SWIGLU else 1)
-    pi = _flat("ids", ids, n, torch.int32, x)
-    pw = None if weights is None else _flat("weights", weights, n, torch.float32, x)
-    out = _gemv_out(out, n if weights is None else tokens, cols, out_dtype, x)
-    if workspace is None and weights is not None:
-        need = lib.nvfp4_expert_gemv_workspace_size(tokens, top_k, cols)
-        workspace = torch.empty(need // 4, dtype=torch.float32, device=x.device)
-    st = lib.nvfp4_expert_gemv(
-        x.data_ptr(), _dtype_code(x.dtype), x.shape[0], ldx, pi, tokens, top_k, ctypes.byref(c), experts, pw,
-        out.data_ptr(), _dtype_code(out.dtype), _matrix("out", out), epilogue,
-        None if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _launch_stream(x, stream))
-    _check("nvfp4_expert_gemv", st)
-    return out
+    return _native.expert_gemv(x, ids, w.codes, w.scales, w.tensor_scale, w.rows, w.cols, w.scale_mode, experts, weights,
+                               epilogue, _code(out_dtype), out, workspace, _handle(stream))
