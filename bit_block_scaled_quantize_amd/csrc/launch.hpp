@@ -136,7 +136,7 @@ hipError_t launch_rmsnorm_backward(const RmsNormBackward& n, hipStream_t s);
 constexpr int kMaxExperts = 2048, kMaxTopK = 16, kMaxRouteGroups = 64;
 struct RouteShape {
     int experts, groups, group_size, top_groups, top_k;
-    int lanes_per_group;  // set by the launcher
+    int lane_shift;  // a group lies on 2^lane_shift lanes; set by the launcher
     bool group_top2;
 };
 struct RouteArgs {

@@ -307,24 +307,24 @@ __global__ void __launch_bounds__(block_of(TPR)) k_rmsnorm_backward(const NormBw
 }
 
 // dweight[c] = sum over g of parts[g][c] in a fixed order: 32 columns a
-// workgroup, 8 threads a column.
-__global__ void __launch_bounds__(256) k_sum_parts(const float* __restrict__ parts, int64_t groups, int64_t cols,
-                                                   float* __restrict__ out) {
-    __shared__ float s[8][32];
+// workgroup, 32 threads a column (few groups: all their loads at once).
+__global__ void __launch_bounds__(1024) k_sum_parts(const float* __restrict__ parts, int64_t groups, int64_t cols,
+                                                    float* __restrict__ out) {
+    __shared__ float s[32][33];
     const int cx = threadIdx.x & 31, gy = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + cx;
     float v = 0.0f;
     if (c < cols) {
 #pragma unroll 8
-        for (int64_t g = gy; g < groups; g += 8) v += parts[g * cols + c];
+        for (int64_t g = gy; g < groups; g += 32) v += parts[g * cols + c];
     }
     s[gy][cx] = v;
     __syncthreads();
-    if (gy == 0 && c < cols) {
-#pragma unroll
-        for (int k = 1; k < 8; ++k) v += s[k][cx];
-        out[c] = v;
-    }
+    // column gy of the 32, its parts over the lanes of a half wave
+    v = s[cx][gy];
+    float a, b;
+    row_pair(reduce16(v, AddOp()), a, b);
+    if (cx == 0 && (int64_t)blockIdx.x * 32 + gy < cols) out[(int64_t)blockIdx.x * 32 + gy] = a + b;
 }
 
 inline int64_t n_cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -347,13 +347,13 @@ struct BwdPlan {
 };
 
 // Row groups of the backward pass: two workgroups a compute unit at most, and
-// at least four rows a group where there are that many (each group costs a
+// at least two rows a group where there are that many (each group costs a
 // row of binary32 partial sums, written and read again).
 BwdPlan bwd_plan(int64_t rows, int64_t cols) {
     BwdPlan p;
     p.tpr = threads_per_row(rows, cols);
     const int64_t per = block_of(p.tpr) / p.tpr;
-    p.blocks = std::min<int64_t>(512, n_cdiv(n_cdiv(rows, 4), per));
+    p.blocks = std::min<int64_t>(512, n_cdiv(n_cdiv(rows, 2), per));
     p.groups = std::min(rows, p.blocks * per);
     return p;
 }
@@ -421,7 +421,7 @@ hipError_t norm_bwd_typed(NormBwd<T> a, float* dweight, hipStream_t s) {
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(k_sum_parts, dim3((unsigned)n_cdiv(a.cols, 32)), dim3(256), 0, s, a.parts, p.groups, a.cols,
+    hipLaunchKernelGGL(k_sum_parts, dim3((unsigned)n_cdiv(a.cols, 32)), dim3(1024), 0, s, a.parts, p.groups, a.cols,
                        dweight);
     return hipGetLastError();
 }
@@ -484,7 +484,7 @@ hipError_t launch_rmsnorm(const RmsNorm& n, hipStream_t s) {
 hipError_t launch_rmsnorm_backward(const RmsNormBackward& n, hipStream_t s) {
     if (n.rows == 0) {
         // no rows: the weight's gradient is zero (the sum over no parts)
-        hipLaunchKernelGGL(k_sum_parts, dim3((unsigned)n_cdiv(n.cols, 32)), dim3(256), 0, s, n.ws, (int64_t)0,
+        hipLaunchKernelGGL(k_sum_parts, dim3((unsigned)n_cdiv(n.cols, 32)), dim3(1024), 0, s, n.ws, (int64_t)0,
                            n.cols, n.dweight);
         return hipGetLastError();
     }

@@ -65,6 +65,20 @@ __device__ __forceinline__ float lanes_reduce(float x, Op op) {
 }
 template <int LPT>
 __device__ __forceinline__ float lanes_max(float x) { return lanes_reduce<LPT>(x, MaxOp()); }
+template <int LPT>
+__device__ __forceinline__ int lanes_max(int x) {
+    x = max(x, (int)lane_xor1((uint32_t)x));
+    x = max(x, (int)lane_xor2((uint32_t)x));
+    x = max(x, (int)quad_perm<0x141>((uint32_t)x));  // (mirrors, as reduce16)
+    x = max(x, (int)quad_perm<0x140>((uint32_t)x));
+    if constexpr (LPT == 64) {
+        const auto a = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+        x = max((int)a[0], (int)a[1]);
+        const auto b = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+        x = max((int)b[0], (int)b[1]);
+    }
+    return x;
+}
 
 // The bits of a ballot that belong to the caller's token, from bit 0.
 template <int LPT>
@@ -114,8 +128,8 @@ __device__ __forceinline__ F comparable(F s) {
 // its terms, x = m - l, whose mean under p is at most log E < 8.  Both: U of
 // the sum with the bias.
 struct Tolerance {
-    float absolute;
-    __device__ __forceinline__ float operator()(float x) const { return absolute + 0x1p-20f * x; }
+    float absolute, relative;
+    __device__ __forceinline__ float operator()(float x) const { return absolute + relative * x; }
 };
 
 // Which groups stay, from a and b, the best and second best key of the
@@ -127,9 +141,9 @@ struct Tolerance {
 template <int LPT, typename Score, typename Tol>
 __device__ __forceinline__ bool keep_groups(float a, float b, const RouteShape& g, Score score, bool exact, Tol tol,
                                             bool& kept) {
-    const int lane = threadIdx.x & (LPT - 1), mine = lane / g.lanes_per_group;
+    const int lane = threadIdx.x & (LPT - 1), mine = lane >> g.lane_shift;
     const int first = threadIdx.x & 63 & ~(LPT - 1);  // the token's first lane of the wave
-    for (int d = 1; d < g.lanes_per_group; d <<= 1) {
+    for (int d = 1; d < 1 << g.lane_shift; d <<= 1) {
         const float a2 = __shfl_xor(a, d), b2 = __shfl_xor(b, d);
         b = fmaxf(fminf(a, a2), fmaxf(b, b2));
         a = fmaxf(a, a2);
@@ -138,7 +152,7 @@ __device__ __forceinline__ bool keep_groups(float a, float b, const RouteShape& 
     const bool is = mine < g.groups;
     int ahead = 0;  // groups before the own one
     for (int o = 0; o < g.groups; ++o) {
-        const float q = __shfl(gs, first + o * g.lanes_per_group);
+        const float q = __shfl(gs, first + (o << g.lane_shift));
         ahead += (q > gs || (q == gs && o < mine)) ? 1 : 0;
     }
     kept = is && ahead < g.top_groups;
@@ -148,7 +162,7 @@ __device__ __forceinline__ bool keep_groups(float a, float b, const RouteShape& 
     if (!__any(near)) return true;
     bool certain = true;
     for (int o = 0; o < g.groups; ++o) {
-        const int at = first + o * g.lanes_per_group;
+        const int at = first + (o << g.lane_shift);
         const float q = __shfl(gs, at), qa = __shfl(a, at), qb = __shfl(b, at);
         const bool other = __shfl((int)kept, at) != (int)kept;
         if (is && other && fabsf(q - gs) <= 2.0f * tol(fmaxf(fabsf(q), fabsf(gs))) && !(exact && qa == a && qb == b))
@@ -157,40 +171,91 @@ __device__ __forceinline__ bool keep_groups(float a, float b, const RouteShape& 
     return certain;
 }
 
-// The n largest of the keys s (V a lane, -inf where there is none; used up),
-// ties to the lower index: lane j < n gets the j-th one's expert and key.
-// out: a row of LDS for the token.
-template <int LPT, int V>
-__device__ __forceinline__ void choose(float s[V], int n, int base, int* out, int& id, float& key) {
-    const float none = -__builtin_inff();
-    const int lane = threadIdx.x & (LPT - 1);
-    const uint64_t lower = (1ull << lane) - 1;
-    key = none;
-    for (int it = 0; it < n; ++it) {
-        float m = s[0];
-#pragma unroll
-        for (int j = 1; j < V; ++j) m = fmaxf(m, s[j]);
-        const float M = lanes_max<LPT>(m);
-        const bool win = m == M && (own_bits<LPT>(__ballot(m == M)) & lower) == 0;
-        if (lane == it) key = M;
-        bool done = !win;
-        int at = 0;
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const bool hit = !done && s[j] == M;
-            s[j] = hit ? none : s[j];
-            at = hit ? j : at;
-            done |= hit;
-        }
-        if (win) out[it] = base + at;
+// Integers in the order of binary32 values, and back (to the value of a key
+// whose low bits are cleared).
+__device__ __forceinline__ int ordered(float s) {
+    const int b = (int)__float_as_uint(s + 0.0f);  // (-0 as 0)
+    return b ^ ((b >> 31) & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float value_of(int key) { return __uint_as_float((uint32_t)(key ^ ((key >> 31) & 0x7FFFFFFF))); }
+
+constexpr int kNone = (int)0x80000000;  // below every key
+
+constexpr int low_bits(int v) { return v <= 2 ? 1 : v <= 4 ? 2 : v <= 8 ? 3 : v <= 16 ? 4 : 5; }
+
+// Exchanges of Batcher's odd-even merge sort of V values.
+template <int V>
+struct Exchanges {
+    int n = 0;
+    uint8_t lo[V * 8] = {}, hi[V * 8] = {};
+    constexpr Exchanges() {
+        for (int p = 1; p < V; p *= 2)
+            for (int q = p; q >= 1; q /= 2)
+                for (int j = q % p; j + q < V; j += 2 * q)
+                    for (int i = 0; i < q && i + j + q < V; ++i)
+                        if ((i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+                            lo[n] = (uint8_t)(i + j);
+                            hi[n++] = (uint8_t)(i + j + q);
+                        }
     }
-    __builtin_amdgcn_wave_barrier();
-    id = lane < n ? out[lane] : 0;
+};
+
+// The lane's keys, largest first.
+template <int V>
+__device__ __forceinline__ void sort_keys(int key[V]) {
+    constexpr Exchanges<V> net;
+#pragma unroll
+    for (int c = 0; c < net.n; ++c) {
+        const int a = key[net.lo[c]], b = key[net.hi[c]];
+        key[net.lo[c]] = max(a, b);
+        key[net.hi[c]] = min(a, b);
+    }
+}
+
+// The next largest of the keys (sorted in each lane; it is taken out): goes to
+// lane `it`, its expert to out[it].  WHOLE: a key's low 16 bits are the
+// expert's index, from the end; else its low bits are the value's place in the
+// lane, from the end, and of lanes with the same key the first is taken.
+template <int LPT, int V, bool WHOLE>
+__device__ __forceinline__ void take(int key[V], int it, int base, int* out, int& mine) {
+    const int lane = threadIdx.x & (LPT - 1);
+    const int M = lanes_max<LPT>(key[0]);
+    if (lane == it) mine = M;
+    bool win = key[0] == M;
+    if constexpr (!WHOLE) {
+        win = win && (own_bits<LPT>(__ballot(win)) & ((1ull << lane) - 1)) == 0;
+        if (win) out[it] = base + V - 1 - (M & ((1 << low_bits(V)) - 1));
+    }
+    // (by bits: a choice between neighbours is compiled to indexing)
+    const int up = win ? -1 : 0;
+#pragma unroll
+    for (int j = 0; j + 1 < V; ++j) key[j] = (key[j + 1] & up) | (key[j] & ~up);
+    key[V - 1] = win ? kNone : key[V - 1];
+}
+
+// The selection score of expert c in binary64 (without a bias its logit, which
+// orders alike): row, m, base and have as route_token has them.
+template <int LPT>
+__device__ __forceinline__ double exact_score(const RouteArgs& a, int64_t row, float m, int base, int have, int c) {
+    const double x = (double)logit(load1(a.logits, a.bf16, row + c));
+    if (!a.bias) return x;
+    double sum = 1.0;
+    if (!a.sigmoid) {
+        sum = 0.0;
+#pragma unroll 1
+        for (int j = 0; j < have; ++j)
+            sum += exp((double)logit(load1(a.logits, a.bf16, row + base + j)) - (double)m);
+#pragma unroll
+        for (int d = 1; d < LPT; d <<= 1) sum += __shfl_xor(sum, d);
+    }
+    const double e = exp(a.sigmoid ? -x : x - (double)m);
+    return comparable((a.sigmoid ? 1.0 / (1.0 + e) : e / sum) + (double)a.bias[c]);
 }
 
 // The choice of one token by binary64 scores, by a whole wave: lane
-// `to` + j gets the j-th chosen expert.  score: a row of LDS (experts doubles).
-__device__ __forceinline__ void choose_exactly(const RouteArgs& a, int64_t t, double* score, int to, int& id) {
+// `to` + j gets the j-th chosen expert in place of id.  score: a row of LDS
+// (experts doubles).
+__device__ __forceinline__ int choose_exactly(const RouteArgs& a, int64_t t, double* score, int to, int id) {
     const RouteShape& g = a.shape;
     const int lane = threadIdx.x & 63, E = g.experts;
     const double none = -__builtin_inf();
@@ -262,6 +327,7 @@ __device__ __forceinline__ void choose_exactly(const RouteArgs& a, int64_t t, do
         if ((at & 63) == lane) score[at] = none;
     }
     __builtin_amdgcn_wave_barrier();
+    return id;
 }
 
 // One wave's tokens, 64 / LPT of them: the caller's lane group has token t.
@@ -272,13 +338,19 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int* 
                                             float& weight) {
     const RouteShape& g = a.shape;
     const int lane = threadIdx.x & (LPT - 1);
-    const int grp = lane / g.lanes_per_group, li = lane % g.lanes_per_group;
+    const int grp = lane >> g.lane_shift, li = lane & ((1 << g.lane_shift) - 1);
     const int base = grp * g.group_size + li * V;
-    const int have = grp < g.groups ? max(0, min(V, g.group_size - li * V)) : 0;
+    int have = grp < g.groups ? max(0, min(V, g.group_size - li * V)) : 0;
+    // (opaque, or V comparisons of it are kept in scalar registers throughout)
+    asm volatile("" : "+v"(have));
     const int64_t row = t * a.ld;
     const float none = -__builtin_inff();
     float s[V];
     load_values<V>(static_cast<const char*>(a.logits) + (row + base) * (a.bf16 ? 2 : 4), a.bf16, have, s);
+    float b[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) b[j] = 0.0f;
+    if (a.bias) load_values<V>(a.bias + base, false, have, b);
     float m = kLowest;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -289,29 +361,35 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int* 
     float total = 1.0f;
     if (softmax) {
         m = lanes_max<LPT>(m);
-        if (a.bias || !a.renorm) {
+        if (!a.renorm) {  // the sum is part of the weights
             total = 0.0f;
-            // (not renormalised: the sum is part of the weights)
 #pragma unroll
-            for (int j = 0; j < V; ++j) total += a.renorm ? quick_exp(s[j] - m) : exp_diff(s[j], m);
+            for (int j = 0; j < V; ++j) total += exp_diff(s[j], m);
+            total = lanes_reduce<LPT>(total, AddOp());
+        } else if (a.bias) {
+            total = 0.0f;
+#pragma unroll
+            for (int j = 0; j < V; ++j) total += quick_exp(s[j] - m);
             total = lanes_reduce<LPT>(total, AddOp());
         }
     }
-    // Without a bias the scores grow with the logits: those are the keys, and
-    // decide exactly.  With one, binary32 scores do wherever they are further
-    // apart than their error, and a token with a nearer pair is chosen in
-    // binary64 (16384 tokens of 256 experts: some tens), unless the pair has
-    // equal logits and biases.
+    // Without a bias the scores grow with the logits, which are compared
+    // instead.  With one, binary32 scores decide wherever they are further
+    // apart than their error; nearer ones are settled in binary64 (16384
+    // tokens of 256 experts: some tens).
     const float inv_total = 1.0f / total;
-    const Tolerance tol = {softmax ? 0x1p-17f * (a.bias ? inv_total : 1.0f) : 0x1p-20f};
+    const Tolerance tol = {softmax ? 0x1p-17f * (a.bias ? inv_total : 1.0f) : 0x1p-20f, 0x1p-20f};
     if (a.bias) {
-        float b[V];
-        load_values<V>(a.bias + base, false, have, b);
+        if (softmax) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const float p = softmax ? quick_exp(s[j] - m) * inv_total : quick_sigmoid(s[j]);
-            s[j] = j < have ? comparable(p + b[j]) : none;
+            for (int j = 0; j < V; ++j) s[j] = quick_exp(s[j] - m) * inv_total;
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) s[j] = quick_sigmoid(s[j]);
         }
+        asm volatile("" : "+v"(have));
+#pragma unroll
+        for (int j = 0; j < V; ++j) s[j] = j < have ? comparable(s[j] + b[j]) : none;
     }
     bool certain = true;
     if (by_group) {
@@ -336,25 +414,66 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int* 
 #pragma unroll
         for (int j = 0; j < V; ++j) s[j] = kept ? s[j] : none;
     }
-    // (with a bias one more, to see how far the next one is behind)
-    float key;
-    choose<LPT, V>(s, a.bias ? g.top_k + 1 : g.top_k, base, out, id, key);
-    if (a.bias) {
-        const float ahead = __shfl_up(key, 1, LPT);
-        const int before = __shfl_up(id, 1, LPT);
-        bool near = lane > 0 && lane <= g.top_k && key > none && ahead - key <= tol(fmaxf(fabsf(ahead), fabsf(key)));
+    // The keys: without a bias of BF16 logits, the logit's 16 bits over the
+    // expert's index, exact and distinct (less 1, which keeps the binary32 limits
+    // that stand for infinities apart from BF16's largest); else the upper bits of the binary32
+    // score over its place in the lane, 2^-19 of the score with 16 a lane.
+    const int k = g.top_k;
+    int key[V], last = kNone;
+    if (a.bf16 && !a.bias) {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            key[j] = s[j] == none ? kNone : ((ordered(s[j]) - 1) & ~0xFFFF) | (0xFFFF - (base + j));
+        sort_keys<V>(key);
+        for (int it = 0; it < k; ++it) take<LPT, V, true>(key, it, base, out, last);
+        id = lane < k ? 0xFFFF - (last & 0xFFFF) : 0;
+    } else {
+        constexpr int low = (1 << low_bits(V)) - 1;
+#pragma unroll
+        for (int j = 0; j < V; ++j) key[j] = s[j] == none ? kNone : (ordered(s[j]) & ~low) | (V - 1 - j);
+        sort_keys<V>(key);
+        // one more than top_k, to see how far the next one is behind
+        for (int it = 0; it <= k; ++it) take<LPT, V, false>(key, it, base, out, last);
+        // the steps of the keys, and the scores' own error where they are not exact
+        const Tolerance step = {a.bias ? tol.absolute + 0x1p-120f : 0x1p-120f, 0x1p-20f + (float)(low + 1) * 0x1p-22f};
+        const float at = value_of(last & ~low);
+        const float before = __shfl_up(at, 1, LPT);
+        const bool near = lane > 0 && lane <= k && last != kNone && before - at <= step(fmaxf(fabsf(before), fabsf(at)));
+        __builtin_amdgcn_wave_barrier();
         if (__any(near)) {
-            if (near)
-                near = !(load1(a.logits, a.bf16, row + id) == load1(a.logits, a.bf16, row + before) &&
-                         a.bias[id] == a.bias[before]);
-            certain &= own_bits<LPT>(__ballot(near)) == 0;
+            // near ones change places by their scores in binary64; candidates
+            // are added until the next one is out of the k-th's reach
+            int n = k + 1;
+            const float kth = __shfl(at, k - 1, LPT);
+            bool open = own_bits<LPT>(__ballot(near && lane == k)) != 0;
+            while (n < min(LPT, kMaxTopK + 1) && __any(open)) {
+                take<LPT, V, false>(key, n, base, out, last);
+                const float next = value_of(__shfl(last, n, LPT) & ~low);
+                open = open && __shfl(last, n, LPT) != kNone && kth - next <= step(fmaxf(fabsf(kth), fabsf(next)));
+                ++n;
+            }
+            certain &= !open;
+            __builtin_amdgcn_wave_barrier();
+            const bool in = lane < n && last != kNone;
+            const int c = in ? out[lane] : 0;
+            const double score = exact_score<LPT>(a, row, m, base, have, c);
+            int ahead = 0;
+            for (int i = 0; i < n; ++i) {
+                const double o = __shfl(score, i, LPT);
+                const int oc = __shfl(c, i, LPT), there = __shfl((int)in, i, LPT);
+                ahead += (there && (o > score || (o == score && oc < c))) ? 1 : 0;
+            }
+            __builtin_amdgcn_wave_barrier();
+            if (in && ahead <= k) out[ahead] = c;
+            __builtin_amdgcn_wave_barrier();
         }
+        id = lane < k ? out[lane] : 0;
     }
     // a token whose lanes are not all certain
     uint64_t open = __ballot(!certain);
     while (open) {
         const int u = (__ffsll((unsigned long long)open) - 1) & ~(LPT - 1);  // its first lane
-        choose_exactly(a, __shfl(t, u), exact, u, id);
+        id = choose_exactly(a, __shfl(t, u), exact, u, id);
         open = LPT == 64 ? 0 : open & ~(0xFFFFull << u);
     }
     // the chosen scores from their logits
@@ -362,10 +481,12 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int* 
     const float lc = mine ? logit(load1(a.logits, a.bf16, row + id)) : none;
     if (a.renorm) {
         const float mc = lanes_max<LPT>(lc);
+        float p = 0.0f;
+        if (!softmax && mine) p = sigmoid32(lc);
         // sigmoids so small that their logits' exponentials are the same to
         // 2^-64 are normalised as those (binary32 would underflow)
         const bool by_exp = softmax || mc < -64.0f;
-        const float p = !mine ? 0.0f : by_exp ? exp_diff(lc, mc) : sigmoid32(lc);
+        if (__any(by_exp) && mine && by_exp) p = exp_diff(lc, mc);
         weight = p / lanes_reduce<LPT>(p, AddOp());
     } else {
         weight = !mine ? 0.0f : softmax ? exp_diff(lc, m) / total : sigmoid32(lc);
@@ -420,7 +541,7 @@ extern __shared__ __attribute__((aligned(16))) int route_lds[];
 // time.  With the plan, position gets the rank of each assignment among those
 // of its expert in the span (the experts of a token are distinct: the bits of
 // the tokens before it in the expert's mask, and the count of earlier rounds),
-// and counts[span][expert] their number; a lone workgroup (few tokens: a
+// and counts[span][expert] their number; a lone workgroup (a round of tokens: a
 // second launch would cost more than its work) goes on to the sorted places.
 template <int LPT, int V>
 __global__ void __launch_bounds__(1024) k_route(const RouteArgs a) {
@@ -452,10 +573,11 @@ __global__ void __launch_bounds__(1024) k_route(const RouteArgs a) {
         }
         if (!plan) continue;
         __syncthreads();
+        int rank = 0;
         if (mine) {
             const uint32_t lo = mask[2 * id], hi = mask[2 * id + 1], below = (1u << (u & 31)) - 1;
-            a.position[t * k + lane] =
-                count[id] + (u < 32 ? __popc(lo & below) : __popc(lo) + __popc(hi & below));
+            rank = count[id] + (u < 32 ? __popc(lo & below) : __popc(lo) + __popc(hi & below));
+            if (gridDim.x > 1) a.position[t * k + lane] = rank;
         }
         __syncthreads();
         for (int e = threadIdx.x; e < E; e += blockDim.x) {
@@ -463,22 +585,21 @@ __global__ void __launch_bounds__(1024) k_route(const RouteArgs a) {
             mask[2 * e] = mask[2 * e + 1] = 0;
         }
         __syncthreads();
+        if (gridDim.x == 1) {  // (one round: all assignments are ranked)
+            const int sum = exclusive_scan(count, E, tmp);
+            if (mine) {
+                const int i = (int)t * k + lane, p = count[id] + rank;
+                a.position[i] = p;
+                a.order[p] = i;
+            }
+            for (int e = threadIdx.x; e < E; e += blockDim.x) a.offsets[e] = count[e];
+            if (threadIdx.x == 0) a.offsets[E] = sum;
+        }
     }
-    if (!plan) return;
-    if (gridDim.x > 1) {
-        const int row = count_row(E);
-        uint8_t* counts = a.counts + (int64_t)blockIdx.x * row;
-        for (int e = threadIdx.x; e < row; e += blockDim.x) counts[e] = e < E ? (uint8_t)count[e] : (uint8_t)0;
-        return;
-    }
-    const int sum = exclusive_scan(count, E, tmp);
-    for (int e = threadIdx.x; e < E; e += blockDim.x) a.offsets[e] = count[e];
-    if (threadIdx.x == 0) a.offsets[E] = sum;
-    for (int i = threadIdx.x; i < a.tokens * k; i += blockDim.x) {  // (ids and ranks of this workgroup's own)
-        const int p = count[a.ids[i]] + a.position[i];
-        a.position[i] = p;
-        a.order[p] = i;
-    }
+    if (!plan || gridDim.x == 1) return;
+    const int row = count_row(E);
+    uint8_t* counts = a.counts + (int64_t)blockIdx.x * row;
+    for (int e = threadIdx.x; e < row; e += blockDim.x) counts[e] = e < E ? (uint8_t)count[e] : (uint8_t)0;
 }
 
 // Parts of the spans that k_route_places sums side by side.
@@ -763,7 +884,7 @@ hipError_t launch_route(RouteArgs a, hipStream_t s) {
         return hipGetLastError();
     }
     const LaneShape ls = lane_shape(a.shape.experts, a.shape.groups, a.shape.top_k, a.tokens);
-    a.shape.lanes_per_group = ls.per_group;
+    a.shape.lane_shift = __builtin_ctz((unsigned)ls.per_group);
     return route_lanes(a, ls, s);
 }
 

@@ -96,12 +96,26 @@ __device__ __forceinline__ float reduce16(float x, Op op) {
     return x;
 }
 
+// The value of the other one of a pair of rows of 16 (halves of 32) and the
+// own one, in either order: exchanged between registers, without LDS.
+__device__ __forceinline__ void row_pair(float x, float& a, float& b) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    a = __uint_as_float(r[0]);
+    b = __uint_as_float(r[1]);
+}
+__device__ __forceinline__ void half_pair(float x, float& a, float& b) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    a = __uint_as_float(r[0]);
+    b = __uint_as_float(r[1]);
+}
+
 // As reduce16 over the 64 lanes of the wave.
 template <typename Op>
 __device__ __forceinline__ float reduce64(float x, Op op) {
-    x = reduce16(x, op);
-    x = op(x, __shfl_xor(x, 16));
-    return op(x, __shfl_xor(x, 32));
+    float a, b;
+    row_pair(reduce16(x, op), a, b);
+    half_pair(op(a, b), a, b);
+    return op(a, b);
 }
 
 struct AddOp {
