@@ -227,83 +227,145 @@ __device__ __forceinline__ void load_row(const NormBwd<T>& a, int64_t r, int t, 
     }
 }
 
-// Whether the next row's elements fit in registers beside the current row's
-// (a workgroup of 1024 threads has 128 registers a thread).
-template <typename T>
-constexpr bool reads_ahead(int tpr, int nc) { return tpr < 1024 || nc * sizeof(T) <= 4; }
+// Whether a row's and the next row's elements fit in registers (a workgroup of
+// 1024 threads has 128 a thread).
+constexpr bool reads_ahead(int tpr, int nc) { return tpr < 1024 || nc == 1; }
 
-// Row group g takes rows g, g + groups, ... and leaves its sum of dy * xhat in
-// parts[g].  The next row's elements are under way while the current row's sum
-// goes round, so that the loads never wait for a reduction.
+// A chunk's terms: adds to dw and returns the chunk's part of sum g xhat.
+template <typename T>
+__device__ __forceinline__ float bwd_terms(const Raw<T>& dy, const Raw<T>& h, const float w[8], float rstd, float dw[8]) {
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float d = dy.value(j), xh = h.value(j) * rstd;
+        dw[j] = __builtin_fmaf(d, xh, dw[j]);
+        s = __builtin_fmaf(d * w[j], xh, s);
+    }
+    return s;
+}
+
+template <typename T>
+__device__ __forceinline__ void bwd_store(const Raw<T>& dy, const Raw<T>& h, const Raw<T>& dh, const float w[8], float rstd,
+                                          float s, T* dx, int64_t n) {
+    float q[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float gx = __builtin_fmaf(-(h.value(j) * rstd), s, dy.value(j) * w[j]);
+        q[j] = __builtin_fmaf(rstd, gx, dh.value(j));
+    }
+    store_upto8(dx, n, q);
+}
+
+// Row group g takes rows g, g + groups, ...; a workgroup's groups leave their
+// sum of dy * xhat in parts[blockIdx.x].  The next row's elements are under way
+// while the current row's sum goes round, so that the loads never wait for a
+// reduction; rows too wide for that are read once for the sum and, from the
+// cache, once more for the outputs.
 template <typename T, int TPR, int NC>
 __global__ void __launch_bounds__(block_of(TPR)) k_rmsnorm_backward(const NormBwd<T> a) {
-    constexpr bool AHEAD = reads_ahead<T>(TPR, NC);
+    constexpr int per = block_of(TPR) / TPR;
     __shared__ float red[2][TPR > 64 ? TPR / 64 : 1];
     const int t = threadIdx.x % TPR;
-    const int64_t g = (int64_t)blockIdx.x * (block_of(TPR) / TPR) + threadIdx.x / TPR;
-    float w[NC][8], dw[NC][8];
+    const int64_t g = (int64_t)blockIdx.x * per + threadIdx.x / TPR;
+    float dw[NC][8];
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-        const int64_t c = 8 * ((int64_t)i * TPR + t), n = a.cols - c;
+    for (int i = 0; i < NC; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[i][j] = dw[i][j] = 0.0f;
-        if (n > 0) load_weight(a.weight, a.w_bf16, c, n, w[i]);
-    }
+        for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
     // every group of a workgroup makes the same number of turns (row_sum needs
     // all lanes); turns past the last row read it again and add nothing
     const int64_t turns = (a.rows + a.groups - 1) / a.groups, last = a.rows - 1;
     const float inv_n = 1.0f / (float)a.cols;
     int buf = 0;
-    BwdRow<T, NC> cur, next;
-    if constexpr (AHEAD) load_row<T, TPR, NC>(a, min(g, last), t, cur);
-    for (int64_t k = 0; k < turns; ++k) {
-        const int64_t row = g + k * a.groups;
-        if constexpr (AHEAD) {
-            if (k + 1 < turns) load_row<T, TPR, NC>(a, min(row + a.groups, last), t, next);
-        } else {
-            load_row<T, TPR, NC>(a, min(row, last), t, cur);
+    if constexpr (reads_ahead(TPR, NC)) {
+        float w[NC][8];
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int64_t c = 8 * ((int64_t)i * TPR + t), n = a.cols - c;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[i][j] = 0.0f;
+            if (n > 0) load_weight(a.weight, a.w_bf16, c, n, w[i]);
         }
-        const bool live = row <= last;
-        if (!live) {
-            cur.rstd = 0.0f;
+        BwdRow<T, NC> cur, next;
+        load_row<T, TPR, NC>(a, min(g, last), t, cur);
+        for (int64_t k = 0; k < turns; ++k) {
+            const int64_t row = g + k * a.groups;
+            if (k + 1 < turns) load_row<T, TPR, NC>(a, min(row + a.groups, last), t, next);
+            const bool live = row <= last;
+            if (!live) {
+                cur.rstd = 0.0f;
+#pragma unroll
+                for (int i = 0; i < NC; ++i) {
+                    cur.dy[i].clear();
+                    cur.h[i].clear();
+                }
+            }
+            float s = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NC; ++i) s += bwd_terms(cur.dy[i], cur.h[i], w[i], cur.rstd, dw[i]);
+            s = row_sum<TPR>(s, red[buf]) * inv_n;
+            buf ^= 1;
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
-                cur.dy[i].clear();
-                cur.h[i].clear();
+                const int64_t c = 8 * ((int64_t)i * TPR + t), n = a.cols - c;
+                if (n > 0 && live)
+                    bwd_store(cur.dy[i], cur.h[i], cur.dh[i], w[i], cur.rstd, s, a.dx + row * a.lddx + c, n);
+            }
+            cur = next;
+        }
+    } else {  // (a group is a workgroup: each of its rows exists)
+        for (int64_t row = g; row <= last; row += a.groups) {
+            const float rstd = a.rstd[row];
+            float s = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                const int64_t c = 8 * ((int64_t)i * TPR + t), n = a.cols - c;
+                if (n <= 0) continue;
+                Raw<T> dy, h;
+                float w[8];
+                dy.load(a.dy + row * a.lddy + c, n);
+                h.load(a.h + row * a.ldh + c, n);
+                load_weight(a.weight, a.w_bf16, c, n, w);
+                s += bwd_terms(dy, h, w, rstd, dw[i]);
+            }
+            s = row_sum<TPR>(s, red[buf]) * inv_n;
+            buf ^= 1;
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                const int64_t c = 8 * ((int64_t)i * TPR + t), n = a.cols - c;
+                if (n <= 0) continue;
+                Raw<T> dy, h, dh;
+                float w[8];
+                dy.load(a.dy + row * a.lddy + c, n);
+                h.load(a.h + row * a.ldh + c, n);
+                dh.clear();
+                if (a.dh) dh.load(a.dh + row * a.lddh + c, n);
+                load_weight(a.weight, a.w_bf16, c, n, w);
+                bwd_store(dy, h, dh, w, rstd, s, a.dx + row * a.lddx + c, n);
             }
         }
-        const float rstd = cur.rstd;
-        float s = 0.0f;
+    }
+    float* part = a.parts + (int64_t)blockIdx.x * a.cols;
+    if constexpr (per == 1) {
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int64_t c = 8 * ((int64_t)i * TPR + t), n = a.cols - c;
+            if (n > 0) store_upto8(part + c, n, dw[i]);
+        }
+    } else {
+        __shared__ float of[per][TPR * NC * 8];
 #pragma unroll
         for (int i = 0; i < NC; ++i)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float dy = cur.dy[i].value(j), xh = cur.h[i].value(j) * rstd;
-                dw[i][j] = __builtin_fmaf(dy, xh, dw[i][j]);
-                s = __builtin_fmaf(dy * w[i][j], xh, s);
-            }
-        s = row_sum<TPR>(s, red[buf]) * inv_n;
-        buf ^= 1;
+            for (int j = 0; j < 8; ++j) of[threadIdx.x / TPR][8 * (i * TPR + t) + j] = dw[i][j];
+        __syncthreads();
+        for (int c = threadIdx.x; c < (int)a.cols; c += block_of(TPR)) {
+            float v = of[0][c];
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            const int64_t c = 8 * ((int64_t)i * TPR + t), n = a.cols - c;
-            if (n <= 0 || !live) continue;
-            float q[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float gx = __builtin_fmaf(-(cur.h[i].value(j) * rstd), s, cur.dy[i].value(j) * w[i][j]);
-                q[j] = __builtin_fmaf(rstd, gx, cur.dh[i].value(j));
-            }
-            store_upto8(a.dx + row * a.lddx + c, n, q);
+            for (int k = 1; k < per; ++k) v += of[k][c];
+            part[c] = v;
         }
-        if constexpr (AHEAD) cur = next;
     }
-    if (g < a.groups)
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            const int64_t c = 8 * ((int64_t)i * TPR + t), n = a.cols - c;
-            if (n > 0) store_upto8(a.parts + g * a.cols + c, n, dw[i]);
-        }
 }
 
 // dweight[c] = sum over g of parts[g][c] in a fixed order: 32 columns a
@@ -347,14 +409,14 @@ struct BwdPlan {
 };
 
 // Row groups of the backward pass: two workgroups a compute unit at most, and
-// at least two rows a group where there are that many (each group costs a
+// at least two rows a group where there are that many (each workgroup costs a
 // row of binary32 partial sums, written and read again).
 BwdPlan bwd_plan(int64_t rows, int64_t cols) {
     BwdPlan p;
     p.tpr = threads_per_row(rows, cols);
     const int64_t per = block_of(p.tpr) / p.tpr;
     p.blocks = std::min<int64_t>(512, n_cdiv(n_cdiv(rows, 2), per));
-    p.groups = std::min(rows, p.blocks * per);
+    p.groups = p.blocks * per;
     return p;
 }
 
@@ -362,8 +424,8 @@ BwdPlan bwd_plan(int64_t rows, int64_t cols) {
     do {                                                                                                    \
         const int64_t nc = n_cdiv(n_cdiv(a.cols, 8), TPR);                                                  \
         if (nc <= 1) hipLaunchKernelGGL((K<T, TPR, 1>), __VA_ARGS__, a);                                    \
-        else if (nc <= 2) hipLaunchKernelGGL((K<T, TPR, 2>), __VA_ARGS__, a);                               \
-        else hipLaunchKernelGGL((K<T, TPR, kMaxNC>), __VA_ARGS__, a);                                       \
+        else if (nc <= 2 || TPR < 1024) hipLaunchKernelGGL((K<T, TPR, 2>), __VA_ARGS__, a);                 \
+        else hipLaunchKernelGGL((K<T, TPR, (TPR < 1024 ? kNC : kMaxNC)>), __VA_ARGS__, a);                  \
     } while (0)
 
 // More rows than fill the chip with 1024 threads a compute unit: that many
@@ -394,8 +456,8 @@ hipError_t norm_typed(const NormFwd<T>& a, hipStream_t s) {
     const int64_t nc = n_cdiv(n_cdiv(a.cols, 8), tpr);
 #define NVFP4_NORM_FWD(TPR)                                       \
     if (nc <= 1) norm_launch<T, TPR, 1>(a, s);                    \
-    else if (nc <= 2) norm_launch<T, TPR, 2>(a, s);               \
-    else norm_launch<T, TPR, kMaxNC>(a, s)
+    else if (nc <= 2 || TPR < 1024) norm_launch<T, TPR, 2>(a, s); \
+    else norm_launch<T, TPR, (TPR < 1024 ? kNC : kMaxNC)>(a, s)
     switch (tpr) {
         case 16: NVFP4_NORM_FWD(16); break;
         case 64: NVFP4_NORM_FWD(64); break;
@@ -421,7 +483,7 @@ hipError_t norm_bwd_typed(NormBwd<T> a, float* dweight, hipStream_t s) {
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(k_sum_parts, dim3((unsigned)n_cdiv(a.cols, 32)), dim3(1024), 0, s, a.parts, p.groups, a.cols,
+    hipLaunchKernelGGL(k_sum_parts, dim3((unsigned)n_cdiv(a.cols, 32)), dim3(1024), 0, s, a.parts, p.blocks, a.cols,
                        dweight);
     return hipGetLastError();
 }
@@ -473,7 +535,7 @@ hipError_t norm_bwd_any(const RmsNormBackward& n, hipStream_t s) {
 }  // namespace
 
 int64_t rmsnorm_backward_workspace_floats(int64_t rows, int64_t cols) {
-    return rows == 0 ? 0 : bwd_plan(rows, cols).groups * cols;
+    return rows == 0 ? 0 : bwd_plan(rows, cols).blocks * cols;
 }
 
 hipError_t launch_rmsnorm(const RmsNorm& n, hipStream_t s) {
