@@ -42,10 +42,10 @@ __device__ __forceinline__ float load1(const void* p, bool bf16, int64_t i) {
 
 __device__ __forceinline__ float sigmoid32(float l) { return 1.0f / (1.0f + expf(-l)); }
 
-// Scores for the choice alone, by the hardware's exponential and reciprocal.
-// An exponential e^-x is off by at most (x + 2) U (U = 2^-24) of itself, which
-// is under 3 U of 1 for every x >= 0: the sigmoid, whose slope in log e is
-// p (1 - p), by under 2^-21 (its reciprocal's step included).
+// Scores for the choice alone, by the hardware's exponential and reciprocal (a
+// unit in the last place each).  With U = 2^-24, an exponential e^-x of a
+// difference is off by (2.2 x + 2) U of itself, under 2.1 U of 1 for every
+// x >= 0, and the sigmoid, whose slope in log e is p (1 - p), by under 3.3 U.
 __device__ __forceinline__ float quick_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
 __device__ __forceinline__ float quick_sigmoid(float l) { return __builtin_amdgcn_rcpf(1.0f + quick_exp(-l)); }
 
@@ -58,10 +58,14 @@ __device__ __forceinline__ float exp_diff(float l, float m) {
     return __builtin_isfinite(err) ? __builtin_fmaf(e, err, e) : e;
 }
 
-// Reductions over the LPT (16 or 64) lanes of a token, result in every lane.
+// Reductions over the LPT (16, 32 or 64) lanes of a token, result in every lane.
 template <int LPT, typename Op>
 __device__ __forceinline__ float lanes_reduce(float x, Op op) {
-    return LPT == 16 ? reduce16(x, op) : reduce64(x, op);
+    if constexpr (LPT == 16) return reduce16(x, op);
+    if constexpr (LPT == 64) return reduce64(x, op);
+    float a, b;
+    row_pair(reduce16(x, op), a, b);
+    return op(a, b);
 }
 template <int LPT>
 __device__ __forceinline__ float lanes_max(float x) { return lanes_reduce<LPT>(x, MaxOp()); }
@@ -71,9 +75,11 @@ __device__ __forceinline__ int lanes_max(int x) {
     x = max(x, (int)lane_xor2((uint32_t)x));
     x = max(x, (int)quad_perm<0x141>((uint32_t)x));  // (mirrors, as reduce16)
     x = max(x, (int)quad_perm<0x140>((uint32_t)x));
-    if constexpr (LPT == 64) {
+    if constexpr (LPT >= 32) {
         const auto a = __builtin_amdgcn_permlane16_swap(x, x, false, false);
         x = max((int)a[0], (int)a[1]);
+    }
+    if constexpr (LPT == 64) {
         const auto b = __builtin_amdgcn_permlane32_swap(x, x, false, false);
         x = max((int)b[0], (int)b[1]);
     }
@@ -84,7 +90,7 @@ __device__ __forceinline__ int lanes_max(int x) {
 template <int LPT>
 __device__ __forceinline__ uint64_t own_bits(uint64_t mask) {
     if constexpr (LPT == 64) return mask;
-    else return (mask >> (threadIdx.x & 48)) & 0xFFFFull;
+    else return (mask >> (threadIdx.x & 63 & ~(LPT - 1))) & ((1ull << LPT) - 1);
 }
 
 // Elements p[0 .. min(n, V) - 1] as binary32 (what lies beyond stays as it was).
@@ -123,10 +129,10 @@ __device__ __forceinline__ F comparable(F s) {
 }
 
 // How far binary32 scores are off, counted twice (two are compared): a score
-// of size x by tol(x).  Sigmoid: 4 U = 2^-22.  Softmax, p <= 1 / total: 3 U of
-// that and the sum's relative error, 38 U of its additions and (2 x + 2) U of
-// its terms, x = m - l, whose mean under p is at most log E < 8.  Both: U of
-// the sum with the bias.
+// of size x by tol(x).  Sigmoid: 3.3 U, and U x of the sum with the bias.
+// Exponentials that are not divided by their sum: 2.1 U.  Softmax, p <= 1 /
+// total: 2.1 U of that and the sum's relative error, 38 U of its additions and
+// (2.2 x + 2) U of its terms, x = m - l, whose mean under p is at most log E < 8.
 struct Tolerance {
     float absolute, relative;
     __device__ __forceinline__ float operator()(float x) const { return absolute + relative * x; }
@@ -233,6 +239,21 @@ __device__ __forceinline__ void take(int key[V], int it, int base, int* out, int
     key[V - 1] = win ? kNone : key[V - 1];
 }
 
+// The largest of the wave's binary64 values, in every lane.
+template <int CTRL>
+__device__ __forceinline__ double quad_perm64(double x) {
+    const uint64_t b = (uint64_t)__double_as_longlong(x);
+    return __longlong_as_double((long long)((uint64_t)quad_perm<CTRL>((uint32_t)(b >> 32)) << 32 | quad_perm<CTRL>((uint32_t)b)));
+}
+__device__ __forceinline__ double wave_max(double x) {
+    x = fmax(x, quad_perm64<0xB1>(x));
+    x = fmax(x, quad_perm64<0x4E>(x));
+    x = fmax(x, quad_perm64<0x141>(x));
+    x = fmax(x, quad_perm64<0x140>(x));
+    x = fmax(x, __shfl_xor(x, 16));
+    return fmax(x, __shfl_xor(x, 32));
+}
+
 // The selection score of expert c in binary64 (without a bias its logit, which
 // orders alike): row, m, base and have as route_token has them.
 template <int LPT>
@@ -263,6 +284,7 @@ __device__ __forceinline__ int choose_exactly(const RouteArgs& a, int64_t t, dou
     float m = kLowest;
     double total = 1.0;
     if (!a.sigmoid) {
+#pragma unroll 1
         for (int e = lane; e < E; e += 64) m = fmaxf(m, logit(load1(a.logits, a.bf16, row + e)));
         m = lanes_max<64>(m);
         total = 0.0;
@@ -278,6 +300,7 @@ __device__ __forceinline__ int choose_exactly(const RouteArgs& a, int64_t t, dou
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d);
     }
+#pragma unroll 1
     for (int e = lane; e < E; e += 64) {
         const double p = score[e] / total;
         score[e] = a.bias ? comparable(p + (double)a.bias[e]) : p;
@@ -286,43 +309,42 @@ __device__ __forceinline__ int choose_exactly(const RouteArgs& a, int64_t t, dou
     if (g.top_groups < g.groups) {
         double best = none, second = none;
         if (lane < g.groups)
+#pragma unroll 1
             for (int e = lane * g.group_size; e < (lane + 1) * g.group_size; ++e) {
                 second = fmax(second, fmin(best, score[e]));
                 best = fmax(best, score[e]);
             }
         const double gs = g.group_top2 && second > none ? best + second : best;
         int ahead = 0;
+#pragma unroll 1
         for (int o = 0; o < g.groups; ++o) {
             const double q = __shfl(gs, o);
             ahead += (q > gs || (q == gs && o < lane)) ? 1 : 0;
         }
         const uint64_t kept = __ballot(lane < g.groups && ahead < g.top_groups);
         __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
         for (int e = lane; e < E; e += 64)
             if (!(kept >> (e / g.group_size) & 1)) score[e] = none;
     }
     // without a bias, the kept experts by their logits (their scores may
     // underflow to ties)
     if (!a.bias)
+#pragma unroll 1
         for (int e = lane; e < E; e += 64)
             if (score[e] > none) score[e] = (double)logit(load1(a.logits, a.bf16, row + e));
+#pragma unroll 1
     for (int it = 0; it < g.top_k; ++it) {
         double best = none;
         int at = E;
+#pragma unroll 1
         for (int e = lane; e < E; e += 64)
-            if (score[e] > best) {
-                best = score[e];
+            if (const double v = score[e]; v > best) {
+                best = v;
                 at = e;
             }
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const double o = __shfl_xor(best, d);
-            const int oat = __shfl_xor(at, d);
-            if (o > best || (o == best && oat < at)) {
-                best = o;
-                at = oat;
-            }
-        }
+        const double most = wave_max(best);
+        at = -lanes_max<64>(best == most ? -at : -E);
         if (lane == to + it) id = at;
         if ((at & 63) == lane) score[at] = none;
     }
@@ -347,10 +369,6 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int* 
     const float none = -__builtin_inff();
     float s[V];
     load_values<V>(static_cast<const char*>(a.logits) + (row + base) * (a.bf16 ? 2 : 4), a.bf16, have, s);
-    float b[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) b[j] = 0.0f;
-    if (a.bias) load_values<V>(a.bias + base, false, have, b);
     float m = kLowest;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -378,7 +396,7 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int* 
     // apart than their error; nearer ones are settled in binary64 (16384
     // tokens of 256 experts: some tens).
     const float inv_total = 1.0f / total;
-    const Tolerance tol = {softmax ? 0x1p-17f * (a.bias ? inv_total : 1.0f) : 0x1p-20f, 0x1p-20f};
+    const Tolerance tol = {softmax && a.bias ? 0x1p-17f * inv_total : 0x1p-21f, 0x1p-23f};
     if (a.bias) {
         if (softmax) {
 #pragma unroll
@@ -387,6 +405,10 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int* 
 #pragma unroll
             for (int j = 0; j < V; ++j) s[j] = quick_sigmoid(s[j]);
         }
+        float b[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) b[j] = 0.0f;
+        load_values<V>(a.bias + base, false, have, b);
         asm volatile("" : "+v"(have));
 #pragma unroll
         for (int j = 0; j < V; ++j) s[j] = j < have ? comparable(s[j] + b[j]) : none;
@@ -435,7 +457,7 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int* 
         // one more than top_k, to see how far the next one is behind
         for (int it = 0; it <= k; ++it) take<LPT, V, false>(key, it, base, out, last);
         // the steps of the keys, and the scores' own error where they are not exact
-        const Tolerance step = {a.bias ? tol.absolute + 0x1p-120f : 0x1p-120f, 0x1p-20f + (float)(low + 1) * 0x1p-22f};
+        const Tolerance step = {a.bias ? tol.absolute + 0x1p-120f : 0x1p-120f, (float)(low + 2) * 0x1p-23f};
         const float at = value_of(last & ~low);
         const float before = __shfl_up(at, 1, LPT);
         const bool near = lane > 0 && lane <= k && last != kNone && before - at <= step(fmaxf(fabsf(before), fabsf(at)));
@@ -458,6 +480,7 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int* 
             const int c = in ? out[lane] : 0;
             const double score = exact_score<LPT>(a, row, m, base, have, c);
             int ahead = 0;
+#pragma unroll 1
             for (int i = 0; i < n; ++i) {
                 const double o = __shfl(score, i, LPT);
                 const int oc = __shfl(c, i, LPT), there = __shfl((int)in, i, LPT);
@@ -471,10 +494,11 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int* 
     }
     // a token whose lanes are not all certain
     uint64_t open = __ballot(!certain);
+#pragma clang loop unroll(disable)
     while (open) {
         const int u = (__ffsll((unsigned long long)open) - 1) & ~(LPT - 1);  // its first lane
         id = choose_exactly(a, __shfl(t, u), exact, u, id);
-        open = LPT == 64 ? 0 : open & ~(0xFFFFull << u);
+        open = LPT == 64 ? 0 : open & ~(((1ull << (LPT & 63)) - 1) << u);
     }
     // the chosen scores from their logits
     const bool mine = lane < g.top_k;
@@ -537,6 +561,9 @@ __host__ __device__ __forceinline__ int route_lds_words(int experts, int waves, 
 
 extern __shared__ __attribute__((aligned(16))) int route_lds[];
 
+// Threads of a workgroup at most: with 1024, a thread has 128 registers.
+__host__ __device__ constexpr int most_threads(int lpt, int v) { return lpt == 32 && v == 16 ? 512 : 1024; }
+
 // The choice over the tokens of span blockIdx.x, 64 / LPT for each wave at a
 // time.  With the plan, position gets the rank of each assignment among those
 // of its expert in the span (the experts of a token are distinct: the bits of
@@ -544,7 +571,7 @@ extern __shared__ __attribute__((aligned(16))) int route_lds[];
 // and counts[span][expert] their number; a lone workgroup (a round of tokens: a
 // second launch would cost more than its work) goes on to the sorted places.
 template <int LPT, int V>
-__global__ void __launch_bounds__(1024) k_route(const RouteArgs a) {
+__global__ void __launch_bounds__(most_threads(LPT, V)) k_route(const RouteArgs a) {
     const int E = a.shape.experts, k = a.shape.top_k;
     const int wave = threadIdx.x >> 6, waves = blockDim.x >> 6, lane = threadIdx.x & (LPT - 1);
     const int u = threadIdx.x / LPT, round = blockDim.x / LPT;
@@ -559,6 +586,7 @@ __global__ void __launch_bounds__(1024) k_route(const RouteArgs a) {
         for (int e = threadIdx.x; e < 3 * E; e += blockDim.x) count[e] = 0;
         __syncthreads();
     }
+#pragma unroll 1
     for (int64_t r = t0; r < t1; r += round) {
         const int64_t t = r + u;
         int id = 0;
@@ -784,19 +812,20 @@ inline int64_t r_cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // Lanes per token and values per lane for a routing shape; {0, 0} when the
 // groups do not fit.  A group's experts lie on LPT / (groups rounded up to a
 // power of two) lanes, in index order, so that the lowest lane and the lowest
-// value among equal ones is the lowest expert.  16 lanes do less work a token,
-// 64 come to its end sooner: those where the tokens are few.
+// value among equal ones is the lowest expert.  Fewer lanes do less work a
+// token (12616 of 304 experts in 8 groups: 41.6 us with 32, 63 with 64), 64 come to its end sooner: those where the tokens are few.
 struct LaneShape {
     int lpt, v, per_group;
 };
 LaneShape lane_shape(int experts, int groups, int top_k, int64_t tokens) {
     int slots = 1;
     while (slots < groups) slots *= 2;
-    for (int lpt : {16, 64}) {
-        if (slots > lpt || (lpt == 16 && (top_k >= 16 || tokens <= 256))) continue;
+    for (int lpt : {16, 32, 64}) {
+        if (slots > lpt || (lpt < 64 && tokens <= 256) || (lpt == 16 && top_k >= 16)) continue;
         const int per = lpt / slots, need = (int)r_cdiv(experts / groups, per);
         for (int v : {2, 4, 8, 16, 32}) {
-            if (lpt == 16 ? v > 16 : v < 4) continue;
+            // (32 lanes: what 16 of them cannot hold)
+            if (lpt == 16 ? v > 16 : lpt == 32 ? v < 8 || v > 16 : v < 4) continue;
             if (need <= v) return {lpt, v, per};
         }
     }
@@ -816,7 +845,7 @@ int64_t route_span_tokens(int64_t tokens, int round) {
 template <int LPT, int V>
 hipError_t route_shaped(RouteArgs a, hipStream_t s) {
     const int E = a.shape.experts;
-    int threads = route_threads(E);
+    int threads = std::min(route_threads(E), most_threads(LPT, V));
     if (a.tokens * LPT < threads) threads = std::max<int>((int)r_cdiv(a.tokens * LPT, 64) * 64, std::min(threads, 256));
     const int round = threads / LPT;
     a.span = route_span_tokens(a.tokens, round);
@@ -840,6 +869,7 @@ hipError_t route_lanes(const RouteArgs& a, LaneShape ls, hipStream_t s) {
             default: return route_shaped<16, 16>(a, s);
         }
     }
+    if (ls.lpt == 32) return ls.v == 8 ? route_shaped<32, 8>(a, s) : route_shaped<32, 16>(a, s);
     switch (ls.v) {
         case 4: return route_shaped<64, 4>(a, s);
         case 8: return route_shaped<64, 8>(a, s);
