@@ -634,7 +634,8 @@ void gemv_launch(const GemvArgs& p, hipStream_t s) {
 template <int FMT, bool XF32, bool SWIGLU, bool EXPERT>
 hipError_t gemv_shaped(GemvArgs p, hipStream_t s) {
     p.rows = (int)std::min<int64_t>(EXPERT ? p.assignments / p.top_k : p.m, XF32 ? 8 : kCols);
-    if (p.rows <= 4) {
+    // (two assignments or fewer to an expert on the average seldom make five)
+    if (p.rows <= 4 || (EXPERT && p.assignments <= 2 * p.experts)) {
         gemv4_launch<FMT, XF32, SWIGLU, EXPERT>(p, s);
     } else {
         if constexpr (!XF32) {

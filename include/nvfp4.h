@@ -496,9 +496,9 @@ size_t nvfp4_expert_gemv_workspace_size(int64_t tokens, int32_t top_k, int64_t n
  *   x_rows == tokens: the assignments of a token share its row of x;
  *   x_rows == tokens * top_k: each has its own (as the first form's y gives).
  *   weights NULL: y has a row for each assignment (tokens * top_k rows);
- *   weights (tokens x top_k floats): y[t] = sum over the places j, in order,
- *   of weights[t][j] * product, in binary32 (tokens rows; assignments
- *   without an expert add nothing); ws_bytes >=
+ *   weights (tokens x top_k floats): y[t] = sum over the places j of
+ *   weights[t][j] * product, in binary32 and a fixed order (tokens rows;
+ *   assignments without an expert add nothing); ws_bytes >=
  *   nvfp4_expert_gemv_workspace_size(tokens, top_k, output columns).
  * An expert's matrix is read once for every 16 of its assignments.
  * Requirements as for nvfp4_gemv; W->rows % experts == 0 (SCALE_2D: N % 16 ==
