@@ -710,8 +710,8 @@ __global__ void __launch_bounds__(1024) k_route_places(const RouteArgs a, int sp
 
 // ---------------------------------------------------------------- backward
 // LPT lanes a token, NC chunks of 8 consecutive experts a lane (chunk c of lane
-// i starts at 8 (c LPT + i)); the chosen experts' terms are added through a row
-// of LDS per token.
+// i starts at 8 (c LPT + i)); the chosen experts' logits are read from, and
+// their terms added through, a row of LDS per token.
 template <typename T, int LPT, int NC>
 __global__ void __launch_bounds__(64) k_route_backward(const RouteBackward a) {
     constexpr int W = LPT * NC * 8;  // row of LDS: covers the experts
@@ -728,25 +728,38 @@ __global__ void __launch_bounds__(64) k_route_backward(const RouteBackward a) {
     for (int c = 0; c < NC; ++c) {
         const int e = 8 * (c * LPT + lane), n = E - e;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            l[c][j] = ds[c][j] = 0.0f;
-            chosen[u][e + j] = 0.0f;
-        }
+        for (int j = 0; j < 8; ++j) l[c][j] = ds[c][j] = 0.0f;
         if (n > 0) {
             load_upto8(row + e, n, l[c]);
             if (a.dscores) load_upto8(a.dscores + t * a.ldds + e, n, ds[c]);
         }
+    }
+    // the chosen experts: lane i < k holds one (an index out of range has none)
+    int id = -1;
+    float dw = 0.0f;
+    if (lane < a.top_k) {
+        id = a.ids[t * a.top_k + lane];
+        dw = a.dweights[t * a.top_k + lane];
+    }
+    const bool mine = id >= 0 && id < E;
+    dw = mine ? dw : 0.0f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        const int e = 8 * (c * LPT + lane), n = E - e;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             l[c][j] = j < n ? logit(l[c][j]) : -__builtin_inff();
             m = fmaxf(m, l[c][j]);
+            chosen[u][e + j] = l[c][j];
         }
     }
-    // the chosen experts: lane i < k holds one (an index out of range has none)
-    const int id = lane < a.top_k ? a.ids[t * a.top_k + lane] : -1;
-    const bool mine = id >= 0 && id < E;
-    const float lc = mine ? logit(load1(row, sizeof(T) == 2, id)) : -__builtin_inff();
-    const float dw = mine ? a.dweights[t * a.top_k + lane] : 0.0f;
+    __syncthreads();  // (one wave)
+    const float lc = mine ? chosen[u][id] : -__builtin_inff();
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) chosen[u][8 * (c * LPT + lane) + j] = 0.0f;
     float total = 1.0f;
     const bool softmax = !a.sigmoid;
     if (softmax) {
