@@ -15,6 +15,15 @@
 //   sigmoid: dl_e = (1 - p_e) (p_e ds_e + [e chosen] w_e (dw_e - D))
 // (the division by the chosen sum cancels, so nothing is divided by a small
 // number).
+//
+// The bytes are few (16384 tokens of 256 experts: 19 MB with the plan, 4 us);
+// what bounds the choice is the instructions and the latency of top_k rounds
+// of selection.  A token is shared by 16 lanes (4 tokens a wave) where they
+// hold its scores, so a round's reduction is four register exchanges; a lane
+// sorts its keys once, and a round takes the largest head.  Measured: 16384
+// tokens, top 8 of 256 in 8 groups, sigmoid with bias, 27.7 us (choice 21, plan
+// 7); top 4 of 32, softmax, 12.9 us (7 and 5); one token 8.7 us; backward with
+// score gradients, 16384 x 256 BF16, 10.3 us (3.3 TB/s).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
