@@ -98,7 +98,7 @@ __device__ __forceinline__ float rsqrt32(float x) {
     const float r = 1.0f / __builtin_sqrtf(x);
     const float t = x * r, te = __builtin_fmaf(x, r, -t);
     const float e = __builtin_fmaf(-te, r, __builtin_fmaf(-t, r, 1.0f));
-    return __builtin_fmaf(0.5f * e, r, r);
+    return e == e ? __builtin_fmaf(0.5f * e, r, r) : r;  // (an infinite x: 0)
 }
 
 // The sum of 8 squares, by halves.

@@ -467,8 +467,8 @@ nvfp4_status nvfp4_route_backward(const float* dweights, const void* logits, int
 /* y = x * W^T for a few rows x (m x K, dtype dt, row stride ldx, not
  * quantized) and an NVFP4 weight W (N x K, SCALE_1D or SCALE_2D):
  *   y[i][n] = s_W * sum_k x[i][k] (v_W sb_W)[n][k], exact products of BF16 x
- *   (of binary32 x: of its three BF16 parts) summed in binary32, rounded once
- *   to y_dt; m x N, row stride ldy.
+ *   (of binary32 x: of its three BF16 parts, which hold it to 2^-133) summed in
+ *   binary32, rounded once to y_dt; m x N, row stride ldy.
  * EPI_SWIGLU: N = 2F, F % 16 == 0; y (m x F) = gate * sigmoid(gate) * up as
  * for nvfp4_gemm, in either dtype.
  * This is the product of a decode step: it reads the weight once for every 16

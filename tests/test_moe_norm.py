@@ -287,3 +287,58 @@ def test_backward_strides_and_in_place(nv):
     dx, dw = nv.nvfp4_rmsnorm_backward(dy.contiguous(), h.contiguous(), rstd, w, dh=dh.contiguous())
     got, dw2 = nv.nvfp4_rmsnorm_backward(dy, h, rstd, w, dh=dh, dx=dy)
     assert got is dy and torch.equal(dy, dx) and torch.equal(dw, dw2)
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits(nv):
+    """Two rows over 2^31 elements apart."""
+    ld = 2 ** 31 + 32
+    bufs = [torch.empty(ld + 96, dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+    x, res, dh = (b.as_strided((2, 96), (ld, 1)) for b in bufs)
+    for i, t in enumerate((x, res, dh)):
+        t.copy_(make(30 + i, 2, 96, torch.bfloat16))
+    w = torch.ones(96, device="cuda")
+    want = nv.nvfp4_rmsnorm(x.contiguous(), w, residual=res.contiguous(), rstd=True)
+    grads = nv.nvfp4_rmsnorm_backward(x.contiguous(), want.h, want.rstd, w, dh=dh.contiguous())
+    got = nv.nvfp4_rmsnorm(x, w, residual=res, rstd=True, out=nv.RMSNormOutput(res, torch.empty_like(want.y), None,
+                                                                             torch.empty_like(want.rstd)))
+    assert got.h is res and torch.equal(res, want.h) and torch.equal(got.y, want.y)
+    dx, dw = nv.nvfp4_rmsnorm_backward(x, res, got.rstd, w, dh=dh, dx=dh)
+    assert torch.equal(dx, grads[0]) and torch.equal(dw, grads[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_row_with_infinity_leaves_the_others(nv, dtype):
+    """(The row itself is unspecified.)"""
+    x = make(33, 9, 256, DT[dtype])
+    w = torch.ones(256, device="cuda")
+    want = nv.nvfp4_rmsnorm(x, w, mx_elem=nv.NVFP4_MX_E4M3, rstd=True)
+    x2 = x.clone()
+    x2[4, 7] = float("inf")
+    got = nv.nvfp4_rmsnorm(x2, w, mx_elem=nv.NVFP4_MX_E4M3, rstd=True)
+    keep = [0, 1, 2, 3, 5, 6, 7, 8]
+    for a, b in ((want.y, got.y), (want.rstd, got.rstd), (want.mx.codes, got.mx.codes), (want.mx.scales, got.mx.scales)):
+        assert torch.equal(a[keep], b[keep])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,cols", [(3, 9001), (513, 100), (1100, 2050), (40, 16390), (2049, 640)])
+def test_many_rows_and_wide_rows(nv, rows, cols):
+    """Row counts around the groups' and widths in which a thread holds
+    several chunks, forward and backward, odd strides."""
+    for dt in (torch.bfloat16, torch.float32):
+        x, res, dh = (make(s, rows, cols, dt, cols + 3, 1) for s in (40, 41, 42))
+        w = (1.0 + 0.1 * make(43, 1, cols, torch.float32)[0]).to(dt)
+        elem = nv.NVFP4_MX_E2M1 if cols % 32 == 0 else None
+        out = nv.nvfp4_rmsnorm(x, w, residual=res, eps=EPS, mx_elem=elem, rstd=True)
+        check_forward(nv, x, res, w, out, dt, elem)
+        a = nv.nvfp4_rmsnorm_backward(res, x, out.rstd, w, dh=dh)
+        b = nv.nvfp4_rmsnorm_backward(res.contiguous(), x.contiguous(), out.rstd, w, dh=dh.contiguous())
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        _, dw = P.rmsnorm_backward(P.host(res), P.host(x), P.host(out.rstd), P.host(w), None)
+        # (the sums' tolerance as in test_backward)
+        groups = nv.nvfp4_rmsnorm_backward_workspace_size(rows, cols) // (4 * cols)
+        n = -(-rows // groups) + -(-groups // 8) + 8 + 2
+        xh = np.abs(P.host(x) * P.host(out.rstd)[:, None])
+        assert (np.abs(P.host(a[1]) - dw) <= n * P.U * (np.abs(P.host(res)) * xh).sum(axis=0)).all()

@@ -331,3 +331,44 @@ def test_backward_masks_and_foreign_ids(nv):
             buf = l.clone()
             assert nv.nvfp4_route_backward(dw, buf, ids, score=score, renorm=renorm, out=buf) is buf
             assert torch.equal(buf, dl)
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits(nv):
+    ld = 2 ** 31 + 32
+    buf = torch.empty(ld + 64, dtype=torch.bfloat16, device="cuda").as_strided((2, 64), (ld, 1))
+    buf.copy_(make(20, 2, 64, torch.bfloat16))
+    r = check(nv, buf, 8, torch.zeros(64, device="cuda"), True, 4, 2)
+    dw = torch.ones(2, 8, device="cuda")
+    want = nv.nvfp4_route_backward(dw, buf.contiguous(), r.ids)
+    assert torch.equal(nv.nvfp4_route_backward(dw, buf, r.ids, out=buf), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("n,groups,k", [(256, 8, 8), (304, 8, 8), (340, 2, 15), (48, 16, 16)])
+def test_equal_rows(nv, n, groups, k, sigmoid):
+    """Rows whose logits are all alike (padding tokens), among others, at token
+    counts of every layout: the lowest experts, in order; with a bias of few
+    values the lowest of the largest."""
+    for T in (3, 300):
+        l = make(T, T, n, torch.float32)
+        l[::3] = 0.0
+        l[1::7] = -3.5
+        few = torch.from_numpy((0.25 * np.random.default_rng(n).integers(0, 2, n)).astype(np.float32)).cuda()
+        for b in (None, torch.zeros(n, device="cuda"), few):
+            check(nv, l, k, b, sigmoid, groups, max(groups // 2, 1))
+            check(nv, l.bfloat16(), k, b, sigmoid, groups, max(groups // 2, 1))
+            check(nv, l, k, b, sigmoid)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,n,groups,top_groups,k", [(700, 304, 8, 3, 8), (300, 512, 1, 1, 8), (300, 330, 2, 1, 16),
+                                                      (290, 272, 17, 5, 4), (1030, 1024, 4, 2, 15)])
+def test_shapes_of_many_tokens(nv, T, n, groups, top_groups, k):
+    l = make(T + n, T, n, torch.float32)
+    bias = 0.05 * torch.randn(n, generator=torch.Generator().manual_seed(n)).cuda()
+    for dt in (torch.float32, torch.bfloat16):
+        check(nv, l.to(dt), k, bias, True, groups, top_groups)
+        check(nv, l.to(dt), k, None, False, groups, top_groups)
+        check(nv, l.to(dt), k, bias, False, groups, top_groups, top2=False)
