@@ -623,7 +623,11 @@ void gemv_launch(const GemvArgs& p, hipStream_t s) {
     constexpr int R = 2, G = SWIGLU ? R / 2 : R;
     const int64_t tiles_x = v_cdiv(SWIGLU ? p.N / 2 : p.N, 16 * G), tiles_y = EXPERT ? p.assignments : v_cdiv(p.m, p.rows);
     const int64_t wave_bytes = (int64_t)p.rows * std::max<int>(kRowBytes * (XF32 ? 3 : 1), (R * 16 + 4) * 4);
-    const int waves = (int)std::clamp<int64_t>(v_cdiv(p.K, kUnit), 1, std::min<int64_t>(8, (EXPERT ? 61440 : 65536) / wave_bytes));
+    // A compute unit holds 8 of these waves.  More workgroups than units: two
+    // of 4 waves take turns (20480 x 5120, 8 BF16 rows: 20.8 us, one of 8 24.0;
+    // binary32 31.2, 42.2); else all 8 (8192 x 8192 MXFP4: 11.1 us, 12.3 with 4).
+    const int64_t most = tiles_x * tiles_y > 256 ? 4 : 8;
+    const int waves = (int)std::clamp<int64_t>(v_cdiv(p.K, kUnit), 1, std::min<int64_t>(most, (EXPERT ? 61440 : 65536) / wave_bytes));
     hipLaunchKernelGGL((k_gemv<FMT, XF32, R, XP, SWIGLU, EXPERT>), dim3((unsigned)tiles_x, (unsigned)tiles_y),
                        dim3(64 * waves), (size_t)(waves * wave_bytes), s, p);
 }
