@@ -605,14 +605,19 @@ __global__ void __launch_bounds__(256) k_expert_sum(const float* __restrict__ pa
 
 inline int64_t v_cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Up to 4 rows of x.  Waves of a workgroup: as few as leave 2560 in all (10 a
-// compute unit), where long streams a wave pay (20480 x 5120: 1, 2, 4 waves:
-// 15.2, 13.0, 13.7 us; 13 experts' 7168 x 2048: 24.6, 28.2, 36.6).
+// Up to 4 rows of x.  Waves of a workgroup: 1, 2, 4 or 8, as many as make 1280
+// in all (5 a compute unit), but two unless there are 6 tiles a unit: longer
+// streams a wave pay beyond that (one BF16 row: 20480 x 5120 with 1, 2, 4 waves 13.5,
+// 12.0, 13.7 us; 8192 x 8192 with 3, 4, 5 11.9, 12.4, 14.3; 5120 x 20480 with 4,
+// 5, 8 18.6, 22.1, 20.1; 13 experts' 7168 x 2048 with 1, 2, 4 24.6, 28.2, 36.6).
 template <int FMT, bool XF32, bool SWIGLU, bool EXPERT>
 void gemv4_launch(const GemvArgs& p, hipStream_t s) {
     constexpr int R = 4, G = SWIGLU ? R / 2 : R;
     const int64_t tiles_x = v_cdiv(SWIGLU ? p.N / 2 : p.N, 4 * G), tiles_y = EXPERT ? p.assignments : v_cdiv(p.m, 4);
-    const int waves = (int)std::clamp<int64_t>(std::min(v_cdiv(p.K, kWide), v_cdiv(2560, tiles_x * tiles_y)), 1, 8);
+    const int64_t tiles = tiles_x * tiles_y, units = v_cdiv(p.K, kWide);
+    int waves = tiles <= 1536 ? 2 : 1;
+    while (waves < 8 && waves * tiles < 1280) waves *= 2;
+    waves = (int)std::clamp<int64_t>(units, 1, waves);
     hipLaunchKernelGGL((k_gemv4<FMT, XF32, R, SWIGLU, EXPERT>), dim3((unsigned)tiles_x, (unsigned)tiles_y), dim3(64 * waves),
                        0, s, p);
 }
