@@ -4,25 +4,33 @@
 // Forward, per row of n elements:
 //   h = round(x + residual)            (the row type: the residual stream as stored)
 //   rstd = 1 / sqrt(sum h^2 / n + eps)
-//   y = (h * weight) * rstd     (BF16 h and weight: the product is exact)
+//   y = h * rstd * weight
 // y is written in the row type, as MX codes and scales of the binary32 y, or
 // both.  Backward, with g = dy * weight and xhat = h * rstd:
 //   dx = rstd * (g - xhat * mean(g * xhat)) + dh
 //   dweight = sum over rows of dy * xhat
-// All sums are binary32 in a fixed order.
+// The forward sum joins groups of 8 squares in binary64, y uses what rstd's
+// rounding to binary32 leaves too, and where a binary32 y lies on the border of
+// two MX codes it is told which side it comes from: the codes are those of the
+// formula's y, but for at most one in 10^7 of BF16 rows, whose groups of 8 are
+// summed in binary32.  (8192 x 5120 with binary32 sums and y as (h * weight) * rstd: 77
+// us, codes in 10^6 on the other side of a border; this: 84; with every square in
+// binary64 and every y rounded to odd: 87.)  The backward sums are binary32.  All
+// are in a fixed order.
 //
 // Both are HBM-bound streams.  A row's elements stay in registers between the
 // sum and the outputs, so every array is read or written once: TPR threads
 // share a row (16, 64, 256, 512 or 1024), each holding NC chunks of 8 consecutive
 // elements (chunk i of thread t starts at 8 (i TPR + t)), so a wave's 16-byte
 // accesses are contiguous and four lanes hold one 32-element MX block.
-// Measured, BF16: forward with h, y and MXFP8 codes, 8192 x 5120, 76.9 us or
-// 4.92 TB/s; backward with dh, 16384 x 7168, 185 us or 5.07 TB/s (a large copy
+// Measured, BF16: forward with h, y and MXFP8 codes, 8192 x 5120, 84.1 us or
+// 4.50 TB/s; backward with dh, 16384 x 7168, 185 us or 5.07 TB/s (a large copy
 // reaches 5.07).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "launch.hpp"
 #include "nvfp4_device.hpp"
@@ -32,8 +40,8 @@ namespace nvfp4 {
 
 namespace {
 
-// Chunks a thread: at most kNC (8192 x 5120 forward with 4: 81.5 us, with 2:
-// 76.9) but in the widest rows, which 1024 threads hold in kMaxNC.
+// Chunks a thread: at most kNC (8192 x 5120 forward, with binary32 sums: 4 took
+// 81.5 us, 2 76.9) but in the widest rows, which 1024 threads hold in kMaxNC.
 constexpr int kNC = 2, kMaxNC = 4;
 
 template <typename T>
@@ -47,7 +55,7 @@ struct NormFwd {
     uint8_t* scales;
     float* rstd;        // nullable
     int64_t rows, cols, ldx, ldr, ldh, ldy, groups, turns;
-    float eps;
+    double eps, inv_cols;
     bool w_bf16, mx_e2m1;
 };
 
@@ -91,22 +99,49 @@ struct Raw {
 
 constexpr int block_of(int tpr) { return tpr > 256 ? tpr : 256; }
 
-// 1 / sqrt(x), the correctly rounded root's reciprocal taken one Newton step
-// further: with t = x r, r (1 + (1 - t r) / 2), t's own rounding error put back.
-// An MX code that lies between two grid values goes by y's last bits.
-__device__ __forceinline__ float rsqrt32(float x) {
-    const float r = 1.0f / __builtin_sqrtf(x);
-    const float t = x * r, te = __builtin_fmaf(x, r, -t);
-    const float e = __builtin_fmaf(-te, r, __builtin_fmaf(-t, r, 1.0f));
-    return e == e ? __builtin_fmaf(0.5f * e, r, r) : r;  // (an infinite x: 0)
+// 1 / sqrt(x): the hardware's binary64 approximation and one step of third order.
+__device__ __forceinline__ double rsqrt64(double x) {
+    const double r = __builtin_amdgcn_rsq(x);
+    const double e = __builtin_fma(-(x * r), r, 1.0);
+    return e == e ? __builtin_fma(r * e, __builtin_fma(e, 0.375, 0.5), r) : r;  // (an x of 0 or infinity)
 }
 
-// The sum of 8 squares, by halves.
-__device__ __forceinline__ float squares8(const float v[8]) {
-    float q[4];
+// The sum of 8 squares, by halves: of BF16 values, whose squares are exact, in
+// binary32, of binary32 ones in binary64.
+template <typename T>
+__device__ __forceinline__ double squares8(const float v[8]) {
+    using S = typename std::conditional<sizeof(T) == 2, float, double>::type;
+    S q[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) q[j] = __builtin_fmaf(v[2 * j + 1], v[2 * j + 1], v[2 * j] * v[2 * j]);
-    return (q[0] + q[1]) + (q[2] + q[3]);
+    for (int j = 0; j < 4; ++j) {
+        const S a = v[2 * j], b = v[2 * j + 1];
+        if constexpr (sizeof(T) == 2) q[j] = __builtin_fmaf(b, b, a * a);
+        else q[j] = __builtin_fma(b, b, a * a);
+    }
+    return (double)((q[0] + q[1]) + (q[2] + q[3]));
+}
+
+// h (hi + lo) w, within a hair of half a step of binary32.  The clamp changes
+// no finite product: it keeps an infinite w's from turning inf into NaN.
+__device__ __forceinline__ float scaled(float h, float hi, float lo, float w) {
+    const float a = h * hi, ae = __builtin_fmaf(h, lo, __builtin_fmaf(h, hi, -a));
+    return __builtin_fmaf(a, w, __builtin_amdgcn_fmed3f(ae * w, -3.402823466e38f, 3.402823466e38f));
+}
+
+// The values of scaled(), rounded to odd: of the two neighbours
+// of one that is not exact, the one whose last bit is 1.  Rounding that again to
+// an MX code goes as rounding the product itself would.
+__device__ __forceinline__ void scaled_odd(const float h[8], float hi, float lo, const float w[8], float y[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float a = h[j] * hi, ae = __builtin_fmaf(h[j], lo, __builtin_fmaf(h[j], hi, -a));
+        const float rest = __builtin_fmaf(ae, w[j], __builtin_fmaf(a, w[j], -y[j]));
+        const int b = (int)__float_as_uint(y[j]);
+        const int away = ((b ^ (int)__float_as_uint(rest)) >> 31) | 1;  // -1: towards zero
+        // (infinity and NaN leave a rest of infinity or NaN: they stay)
+        if (__builtin_fabsf(rest) > 0.0f && __builtin_fabsf(rest) < 1e30f && y[j] != 0.0f && !(b & 1))
+            y[j] = __uint_as_float((uint32_t)(b + away));
+    }
 }
 
 template <typename T, int NC>
@@ -132,11 +167,10 @@ __device__ __forceinline__ void load_row(const NormFwd<T>& a, int64_t r, int t, 
 // are under way while the current row's sum goes round and its outputs leave.
 template <typename T, int TPR, int NC, bool AHEAD>
 __global__ void __launch_bounds__(block_of(TPR)) k_rmsnorm(const NormFwd<T> a) {
-    __shared__ float red[2][TPR > 64 ? TPR / 64 : 1];
+    __shared__ double red[2][TPR > 64 ? TPR / 64 : 1];
     const int t = threadIdx.x % TPR;
     const int64_t g = (int64_t)blockIdx.x * (block_of(TPR) / TPR) + threadIdx.x / TPR;
     const int64_t last = a.rows - 1;
-    const float cols = (float)a.cols;
     int buf = 0;
     FwdRow<T, NC> cur, next;
     load_row<T, TPR, NC>(a, min(g, last), t, cur);
@@ -149,7 +183,7 @@ __global__ void __launch_bounds__(block_of(TPR)) k_rmsnorm(const NormFwd<T> a) {
         }
         const bool live = row <= last;
         float v[NC][8];
-        float ss = 0.0f;
+        double ss = 0.0;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int64_t c = 8 * ((int64_t)i * TPR + t), n = a.cols - c;
@@ -159,11 +193,12 @@ __global__ void __launch_bounds__(block_of(TPR)) k_rmsnorm(const NormFwd<T> a) {
                 if (a.residual) v[i][j] = rounded_to<T>(v[i][j] + cur.residual[i].value(j));
             }
             if (a.h && live && n > 0) store_upto8(a.h + r * a.ldh + c, n, v[i]);
-            ss += squares8(v[i]);
+            ss += squares8<T>(v[i]);
         }
-        ss = row_sum<TPR>(ss, red[buf]);
+        ss = row_sum64<TPR>(ss, red[buf]);
         buf ^= 1;
-        const float rstd = rsqrt32(ss / cols + a.eps);
+        const double scale = rsqrt64(__builtin_fma(ss, a.inv_cols, a.eps));
+        const float rstd = (float)scale, rstd_lo = (float)(scale - (double)rstd);
         if (a.rstd && live && t == 0) a.rstd[r] = rstd;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
@@ -172,9 +207,16 @@ __global__ void __launch_bounds__(block_of(TPR)) k_rmsnorm(const NormFwd<T> a) {
             float w[8], y[8];
             load_weight(a.weight, a.w_bf16, c, n, w);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = (v[i][j] * w[j]) * rstd;
+            for (int j = 0; j < 8; ++j) y[j] = scaled(v[i][j], rstd, rstd_lo, w[j]);
             if (a.y && live) store_upto8(a.y + r * a.ldy + c, n, y);
             if (a.codes) {  // cols % 32 == 0: the four lanes of a block agree on n > 0
+                // Halfway between two codes, or at a power of two, which sets a
+                // block's scale, a binary32 number ends in 19 zeros, and which
+                // side y lies on is lost: about one wave in a thousand.
+                uint32_t ends = ~0u;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) ends = min(ends, __float_as_uint(y[j]) << 13);
+                if (__builtin_expect(ends == 0, 0)) scaled_odd(v[i], rstd, rstd_lo, w, y);
                 uint32_t cw[2];
                 const uint32_t sb = a.mx_e2m1 ? mx_block_rne8<kMxE2M1>(y, cw) : mx_block_rne8<kMxE4M3>(y, cw);
                 if (live) {
@@ -429,9 +471,9 @@ BwdPlan bwd_plan(int64_t rows, int64_t cols) {
     } while (0)
 
 // More rows than fill the chip with 1024 threads a compute unit: that many
-// workgroups take the rows in turn, reading ahead (8192 x 5120: one workgroup
-// a row 82.8 us, reading ahead 76.9 with 1024 threads a unit and 78.0 with
-// 2048).
+// workgroups take the rows in turn, reading ahead (8192 x 5120, with binary32
+// sums: one workgroup a row 82.8 us, reading ahead 76.9 with 1024 threads a
+// unit and 78.0 with 2048).
 template <typename T, int TPR, int NC>
 void norm_launch(NormFwd<T> a, hipStream_t s) {
     constexpr int per = block_of(TPR) / TPR;
@@ -507,6 +549,7 @@ hipError_t norm_any(const RmsNorm& n, hipStream_t s) {
     a.ldh = n.ldh;
     a.ldy = n.ldy;
     a.eps = n.eps;
+    a.inv_cols = 1.0 / (double)n.cols;
     a.w_bf16 = n.w_bf16;
     a.mx_e2m1 = n.elem == kMxE2M1;
     return norm_typed(a, s);

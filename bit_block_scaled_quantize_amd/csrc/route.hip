@@ -249,11 +249,6 @@ __device__ __forceinline__ void take(int key[V], int it, int base, int* out, int
 }
 
 // The largest of the wave's binary64 values, in every lane.
-template <int CTRL>
-__device__ __forceinline__ double quad_perm64(double x) {
-    const uint64_t b = (uint64_t)__double_as_longlong(x);
-    return __longlong_as_double((long long)((uint64_t)quad_perm<CTRL>((uint32_t)(b >> 32)) << 32 | quad_perm<CTRL>((uint32_t)b)));
-}
 __device__ __forceinline__ double wave_max(double x) {
     x = fmax(x, quad_perm64<0xB1>(x));
     x = fmax(x, quad_perm64<0x4E>(x));

@@ -147,6 +147,42 @@ __device__ __forceinline__ float row_sum(float x, float* lds) {
     return x;
 }
 
+// A binary64 value of another lane, by the same exchanges of its two words.
+template <int CTRL>
+__device__ __forceinline__ double quad_perm64(double x) {
+    const uint64_t b = (uint64_t)__double_as_longlong(x);
+    return __longlong_as_double((long long)((uint64_t)quad_perm<CTRL>((uint32_t)(b >> 32)) << 32 | quad_perm<CTRL>((uint32_t)b)));
+}
+
+// row_sum in binary64.
+template <int TPR>
+__device__ __forceinline__ double row_sum64(double x, double* lds) {
+    x += quad_perm64<0xB1>(x);
+    x += quad_perm64<0x4E>(x);
+    x += quad_perm64<0x141>(x);
+    x += quad_perm64<0x140>(x);
+    if constexpr (TPR > 16) {
+        const uint64_t b = (uint64_t)__double_as_longlong(x);
+        auto hi = __builtin_amdgcn_permlane16_swap((uint32_t)(b >> 32), (uint32_t)(b >> 32), false, false);
+        auto lo = __builtin_amdgcn_permlane16_swap((uint32_t)b, (uint32_t)b, false, false);
+        x = __longlong_as_double((long long)((uint64_t)hi[0] << 32 | lo[0])) +
+            __longlong_as_double((long long)((uint64_t)hi[1] << 32 | lo[1]));
+        const uint64_t c = (uint64_t)__double_as_longlong(x);
+        hi = __builtin_amdgcn_permlane32_swap((uint32_t)(c >> 32), (uint32_t)(c >> 32), false, false);
+        lo = __builtin_amdgcn_permlane32_swap((uint32_t)c, (uint32_t)c, false, false);
+        x = __longlong_as_double((long long)((uint64_t)hi[0] << 32 | lo[0])) +
+            __longlong_as_double((long long)((uint64_t)hi[1] << 32 | lo[1]));
+    }
+    if constexpr (TPR > 64) {
+        if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
+        lds_barrier();
+        x = 0.0;
+#pragma unroll
+        for (int w = 0; w < TPR / 64; ++w) x += lds[w];
+    }
+    return x;
+}
+
 // ---------------------------------------------------------------- MX blocks
 // Nearest-even MX codes of a lane's 8 consecutive elements, four lanes holding
 // one 32-element block, and the block's scale byte (rules of include/nvfp4.h:

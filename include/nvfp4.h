@@ -370,13 +370,13 @@ size_t nvfp4_mx_gemm_workspace_size(const nvfp4_mx_tensor* A, const nvfp4_mx_ten
  * norm that feeds them, the routing that plans them and the products of a few
  * tokens.  Matrices of these operators (x, residual, h, y, logits and their
  * gradients) need only their element's alignment and a leading dimension >=
- * cols; sums are binary32 in a fixed order, so results repeat bit for bit.
+ * cols; sums are binary32 or more in a fixed order, so results repeat bit for bit.
  * ---------------------------------------------------------------------- */
 
 /* RMS norm with the residual's addition.  Per row:
  *   h = x + residual, rounded to dt (residual NULL: h = x);
- *   rstd = 1 / sqrt(sum h^2 / cols + eps), binary32;
- *   y = (h * weight) * rstd, binary32.
+ *   rstd = 1 / sqrt(sum h^2 / cols + eps), stored as binary32;
+ *   y = h * rstd * weight with rstd before that rounding, as binary32.
  * Outputs, each optional (NULL) but one of y and mx: h (rows x cols, dt; may
  * be x or residual itself, same leading dimension), y rounded to dt, mx the
  * ROW_1D nearest-even MX quantization of the binary32 y (mx->elem selects the

@@ -342,3 +342,66 @@ def test_many_rows_and_wide_rows(nv, rows, cols):
         n = -(-rows // groups) + -(-groups // 8) + 8 + 2
         xh = np.abs(P.host(x) * P.host(out.rstd)[:, None])
         assert (np.abs(P.host(a[1]) - dw) <= n * P.U * (np.abs(P.host(res)) * xh).sum(axis=0)).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,cols", [(1, 32), (3, 96), (40, 1003), (9, 5120), (5, 9001), (3, 32768)])
+def test_y_is_the_nearest_binary32(nv, rows, cols):
+    """Whole numbers up to 1000, whose squares sum in eights without rounding,
+    and an eps that is a power of two leave no error before the binary64 part:
+    y is within half a step and what a binary32 pair leaves of the product, each
+    of its three roundings 2^-24 of a half step."""
+    g = np.random.default_rng(50 + cols)
+    x = torch.from_numpy(g.integers(-1000, 1001, (rows, cols))).float().cuda()
+    w = torch.from_numpy(g.standard_normal(cols)).float().cuda()
+    _, y = P.rmsnorm(P.host(x), P.host(w), 2.0 ** -20)
+    step = np.exp2(np.floor(np.log2(np.maximum(np.abs(y), 2.0 ** -126))) - 23)
+    got = P.host(nv.nvfp4_rmsnorm(x, w, eps=2.0 ** -20).y)
+    assert (np.abs(got - y) <= 0.5 * step * (1 + 2.0 ** -20)).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_an_infinite_weight(nv, dtype):
+    """y is infinite in its column, of h's sign, and as ever in the others."""
+    x = make(34, 6, 256, DT[dtype])
+    w = torch.ones(256, device="cuda")
+    want = nv.nvfp4_rmsnorm(x, w).y
+    w[9], w[200] = float("inf"), float("-inf")
+    got = nv.nvfp4_rmsnorm(x, w).y
+    assert torch.equal(got[:, 9], torch.sign(x[:, 9]) * float("inf"))
+    assert torch.equal(got[:, 200], -torch.sign(x[:, 200]) * float("inf"))
+    keep = [c for c in range(256) if c not in (9, 200)]
+    assert torch.equal(got[:, keep], want[:, keep])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("elem", ["E4M3", "E2M1"])
+def test_codes_at_borders(nv, elem):
+    """Codes are those of the exact y, also where its nearest binary32 lies
+    halfway between two codes or at a power of two.  Rows of whole numbers with
+    rstd's error below 2^-47 (see above); each weight is, to binary32, what puts
+    the first row's value at such a place, so that the product falls to either
+    side of it by up to 2^-24, and 2^-44 or less in about one of 10^6."""
+    code = nv.NVFP4_MX_E4M3 if elem == "E4M3" else nv.NVFP4_MX_E2M1
+    g = np.random.default_rng(61)
+    cols = 4096
+    x = np.abs(g.integers(1, 1001, (2, cols))).astype(np.float64)
+    rstd = 1.0 / np.sqrt((x * x).mean(axis=1) + 2.0 ** -20)
+    emax, bits = (8, 3) if elem == "E4M3" else (2, 1)
+    border = (2 ** (bits + 1) + 2 * g.integers(0, 2 ** bits, cols) + 1) / 2.0 ** (bits + 1)  # halfway in [1, 2)
+    border[::32] = np.where(np.arange(cols // 32) % 2, 2.0, 1.75)  # a block's largest: a power of two or below it
+    border[1::32] = np.minimum(border[1::32], border[::32] - 0.25)
+    border = np.where(np.arange(cols) % 32 == 0, border, 0.5 * border)
+    w = torch.from_numpy(border / (x[0] * rstd[0])).float()
+    out = nv.nvfp4_rmsnorm(torch.from_numpy(x).float().cuda(), w.cuda(), eps=2.0 ** -20, mx_elem=code)
+    y = x * rstd[:, None] * P.host(w)
+    amax = np.abs(y).reshape(2, -1, 32).max(axis=2)
+    s = np.floor(np.log2(amax)) - emax
+    assert np.array_equal(out.mx.scales.cpu().numpy(), (s + 127).astype(np.uint8))
+    m = np.abs(y) / np.repeat(2.0 ** s, 32, axis=1)
+    low = -6 if elem == "E4M3" else 0
+    step = 2.0 ** (np.floor(np.log2(np.maximum(m, 2.0 ** low))) - bits)
+    want = np.minimum(np.round(m / step) * step, 448.0 if elem == "E4M3" else 6.0)
+    got = P.host(nv.nvfp4_mx_dequantize(out.mx, dtype=torch.float32)) / np.repeat(2.0 ** s, 32, axis=1)
+    assert np.array_equal(got, want)
