@@ -29,7 +29,7 @@
 // Measured (a large copy: 5.07 TB/s): one BF16 row, 20480 x 5120 with 16x16
 // scales, 12.0 us (4.4 TB/s); 8 rows, 8192 x 8192 MXFP4, 11.1 us (3.2); four
 // tokens through 4 of 32 experts of 7168 / 2048, up with SwiGLU, down and
-// weighted sum, 68 us (4.3).
+// weighted sum, 67 to 72 us (4.1 to 4.4).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
