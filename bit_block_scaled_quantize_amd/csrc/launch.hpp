@@ -98,6 +98,11 @@ GemmSplit mx_gemm_split_plan(int64_t M, int64_t N, int64_t K, double tile_us, in
 // A lone last-round tile's time per 1024 K for this element format and accumulation mode, in µs.
 double mx_split_tile_us(int elem, bool exact);
 
+// Workgroups that one launch can hold in a dimension of its grid: the runtime
+// takes more than 2^32 - 1 threads without an error, and runs what is left of
+// their number in 32 bits.
+constexpr int64_t max_blocks(int threads) { return 0xFFFFFFFFll / threads; }
+
 // RMS norm (see nvfp4_rmsnorm); cols in [1, kMaxNormCols], codes NULL for no
 // MX output.
 constexpr int64_t kMaxNormCols = 32768;

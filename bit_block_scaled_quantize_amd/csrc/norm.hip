@@ -470,12 +470,35 @@ BwdPlan bwd_plan(int64_t rows, int64_t cols) {
         else hipLaunchKernelGGL((K<T, TPR, (TPR < 1024 ? kNC : kMaxNC)>), __VA_ARGS__, a);                  \
     } while (0)
 
+// The rows of a from r on.
+template <typename T>
+NormFwd<T> rows_from(NormFwd<T> a, int64_t r) {
+    a.x += r * a.ldx;
+    if (a.residual) a.residual += r * a.ldr;
+    if (a.h) a.h += r * a.ldh;
+    if (a.y) a.y += r * a.ldy;
+    if (a.codes) {
+        a.codes += r * (a.mx_e2m1 ? a.cols / 2 : a.cols);
+        a.scales += r * (a.cols / 32);
+    }
+    if (a.rstd) a.rstd += r;
+    a.rows -= r;
+    return a;
+}
+
 // More rows than fill the chip with 1024 threads a compute unit: that many
 // workgroups take the rows in turn, reading ahead (8192 x 5120, with binary32
 // sums: one workgroup a row 82.8 us, reading ahead 76.9 with 1024 threads a
 // unit and 78.0 with 2048).
 template <typename T, int TPR, int NC>
 void norm_launch(NormFwd<T> a, hipStream_t s) {
+    // (rows that one grid cannot hold: over 4 million of over 8192 columns)
+    const int64_t most_rows = max_blocks(block_of(TPR)) * (block_of(TPR) / TPR);
+    for (; TPR == 1024 && a.rows > most_rows; a = rows_from(a, most_rows)) {
+        NormFwd<T> part = a;
+        part.rows = most_rows;
+        norm_launch<T, TPR, NC>(part, s);
+    }
     constexpr int per = block_of(TPR) / TPR;
     constexpr bool ahead = TPR < 1024;
     int64_t blocks = n_cdiv(a.rows, per);

@@ -1,0 +1,49 @@
+"""The MoE-block operators at sizes that one launch's grid cannot hold (2^32
+threads): every output is compared with those of a small call whose rows, or
+columns, the large one repeats.  The sizes are those at which the 32-bit number
+of threads has just been passed."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+GB = 1 << 30
+
+
+@pytest.fixture
+def nv():
+    from parity_utils import require_gpu
+    yield require_gpu()
+    torch.cuda.empty_cache()
+
+
+def needs(gib):
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < gib * GB:
+        pytest.skip(f"needs {gib} GiB of free device memory")
+
+
+def repeated(block, times):
+    """The block's rows, `times` times under each other."""
+    out = torch.empty((times,) + tuple(block.shape), dtype=block.dtype, device="cuda")
+    out.copy_(block)
+    return out.view((-1,) + tuple(block.shape[1:]))
+
+
+def repeats(got, block):
+    """Whether got's rows are the block's, again and again."""
+    got = got.view((-1,) + tuple(block.shape))
+    step = max(1, GB // (block.numel() * block.element_size()))
+    return all(bool((got[i:i + step] == block).all()) for i in range(0, got.shape[0], step))
+
+
+def test_norm_of_many_wide_rows(nv):
+    """4194368 rows of 8224 columns, a workgroup of 1024 threads each."""
+    needs(100)
+    rows, cols, times = 64, 8224, 65537
+    block = torch.randn(rows, cols, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    w = torch.linspace(0.5, 1.5, cols, device="cuda")
+    want = nv.nvfp4_rmsnorm(block, w, y=False, mx_elem=nv.NVFP4_MX_E2M1, rstd=True)
+    got = nv.nvfp4_rmsnorm(repeated(block, times), w, y=False, mx_elem=nv.NVFP4_MX_E2M1, rstd=True)
+    assert repeats(got.mx.codes, want.mx.codes) and repeats(got.mx.scales, want.mx.scales)
+    assert repeats(got.rstd, want.rstd)
