@@ -896,8 +896,22 @@ hipError_t route_lanes(const RouteArgs& a, LaneShape ls, hipStream_t s) {
 }
 
 template <typename T>
-hipError_t route_backward_typed(const RouteBackward& a, hipStream_t s) {
+hipError_t route_backward_typed(RouteBackward a, hipStream_t s) {
     const int lpt = a.experts <= 512 ? 16 : 64, nc = (int)r_cdiv(a.experts, 8 * lpt);
+    // (tokens that one grid cannot hold: over 2^28, of more than 512 experts 2^26)
+    const int64_t most = max_blocks(64) * (64 / lpt);
+    if (a.tokens > most) {
+        RouteBackward rest = a;
+        a.tokens = most;
+        rest.tokens -= most;
+        rest.dweights += most * a.top_k;
+        rest.ids += most * a.top_k;
+        rest.logits = static_cast<const T*>(a.logits) + most * a.ld;
+        rest.dlogits = static_cast<T*>(a.dlogits) + most * a.lddl;
+        if (a.dscores) rest.dscores += most * a.ldds;
+        const hipError_t e = route_backward_typed<T>(rest, s);
+        if (e != hipSuccess) return e;
+    }
     const dim3 g((unsigned)r_cdiv(a.tokens, 64 / lpt));
     if (lpt == 16) {
         if (nc <= 1) hipLaunchKernelGGL((k_route_backward<T, 16, 1>), g, dim3(64), 0, s, a);

@@ -47,3 +47,18 @@ def test_norm_of_many_wide_rows(nv):
     got = nv.nvfp4_rmsnorm(repeated(block, times), w, y=False, mx_elem=nv.NVFP4_MX_E2M1, rstd=True)
     assert repeats(got.mx.codes, want.mx.codes) and repeats(got.mx.scales, want.mx.scales)
     assert repeats(got.rstd, want.rstd)
+
+
+def test_routing_backward_of_many_tokens(nv):
+    """2^28 + 4096 tokens, four to a wave of 64 threads."""
+    needs(8)
+    g = torch.Generator().manual_seed(2)
+    times = (2 ** 28 + 4096) // 4096
+    l = torch.randn(4096, 1, generator=g).bfloat16().cuda()
+    dw, ds = torch.randn(4096, 1, generator=g).cuda(), torch.randn(4096, 1, generator=g).cuda()
+    ids = torch.zeros(4096, 1, dtype=torch.int32, device="cuda")
+    kw = dict(score=nv.NVFP4_ROUTE_SIGMOID, renorm=False)
+    want = nv.nvfp4_route_backward(dw, l, ids, dscores=ds, **kw)
+    got = nv.nvfp4_route_backward(repeated(dw, times), repeated(l, times), repeated(ids, times),
+                                  dscores=repeated(ds, times), **kw)
+    assert repeats(got, want)
