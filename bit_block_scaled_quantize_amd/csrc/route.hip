@@ -867,10 +867,26 @@ hipError_t route_shaped(RouteArgs a, hipStream_t s) {
     const int round = threads / LPT;
     a.span = route_span_tokens(a.tokens, round);
     const int spans = (int)r_cdiv(a.tokens, a.span);
-    hipLaunchKernelGGL((k_route<LPT, V>), dim3((unsigned)spans), dim3(threads),
-                       route_lds_words(E, threads / 64, LPT, a.offsets != nullptr) * sizeof(int), s, a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !a.offsets || spans == 1) return e;
+    const size_t lds = route_lds_words(E, threads / 64, LPT, a.offsets != nullptr) * sizeof(int);
+    // (spans that one grid cannot hold, over 4 million, go in equal parts: none
+    // of them is a lone workgroup, which would make the plan by itself)
+    const int64_t parts = r_cdiv(spans, max_blocks(threads)), per = r_cdiv(spans, parts);
+    for (int64_t first = 0; first < spans; first += per) {
+        const int64_t n = std::min(per, spans - first), t = first * a.span;
+        RouteArgs part = a;
+        part.logits = static_cast<const char*>(a.logits) + t * a.ld * (a.bf16 ? 2 : 4);
+        part.ids += t * a.shape.top_k;
+        part.weights += t * a.shape.top_k;
+        if (a.offsets) {
+            part.position += t * a.shape.top_k;
+            part.counts += first * count_row(E);
+        }
+        part.tokens = std::min(n * a.span, a.tokens - t);
+        hipLaunchKernelGGL((k_route<LPT, V>), dim3((unsigned)n), dim3(threads), lds, s, part);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    if (!a.offsets || spans == 1) return hipSuccess;
     a.group = (int)r_cdiv(spans, 256);
     hipLaunchKernelGGL(k_route_places, dim3((unsigned)r_cdiv(spans, a.group)), dim3(1024),
                        (2 * count_row(E) * (1 + route_parts(count_row(E))) + 16) * sizeof(int), s, a, spans);

@@ -62,3 +62,26 @@ def test_routing_backward_of_many_tokens(nv):
     got = nv.nvfp4_route_backward(repeated(dw, times), repeated(l, times), repeated(ids, times),
                                   dscores=repeated(ds, times), **kw)
     assert repeats(got, want)
+
+
+def test_routing_of_many_tokens(nv):
+    """805478400 tokens, 192 to a workgroup of 1024 threads, and their plan."""
+    needs(40)
+    period, times = 4096, 196650
+    block = torch.randn(period, 2, generator=torch.Generator().manual_seed(3)).bfloat16().cuda()
+    want = nv.nvfp4_route(block, 1, score=nv.NVFP4_ROUTE_SIGMOID, renorm=False)
+    got = nv.nvfp4_route(repeated(block, times), 1, score=nv.NVFP4_ROUTE_SIGMOID, renorm=False)
+    assert repeats(got.ids, want.ids) and repeats(got.weights, want.weights)
+    # an expert's assignments lie in order, each period's after the last one's
+    assert torch.equal(got.offsets, want.offsets * times)
+    counts = want.offsets.diff()
+    place = want.position - want.offsets[want.ids[:, 0].long()]  # within the expert and the period
+    at = got.position.view(times, period)
+    order = got.order
+    for i in range(0, times, 16384):
+        p = torch.arange(i, min(i + 16384, times), device="cuda").view(-1, 1)
+        e = want.ids[:, 0].long()
+        expect = got.offsets[e] + p * counts[e] + place
+        assert torch.equal(at[i:i + 16384], expect.int())
+        t = p * period + torch.arange(period, device="cuda")
+        assert torch.equal(order[expect], t.int())
