@@ -180,6 +180,10 @@ hipError_t launch_route_backward(const RouteBackward& a, bool bf16, hipStream_t 
 // nvfp4_expert_gemv).
 constexpr int64_t kMaxGemvRows = 1024;
 constexpr int kMaxGemvAssignments = 1024;
+// Rows of a matrix at most: one grid holds 256 threads (of so many tiles, the
+// most) for each 32 of them.
+constexpr int64_t kMaxGemvCols = ((int64_t)1 << 29) - 32;
+static_assert(kMaxGemvCols == 32 * max_blocks(256));
 struct GemvArgs {
     const void* x;
     int64_t m, ldx;

@@ -543,7 +543,7 @@ nvfp4_status check_gemv(const void* x, int32_t dt, int64_t x_rows, int64_t ldx, 
     nvfp4_status st = check_matrix(x, K > 0 ? x_rows : 0, K, ldx, dt);
     if (st == NVFP4_OK) st = check_matrix(y, outs > 0 ? y_rows : 0, outs, ldy, y_dt);
     if (st != NVFP4_OK) return st;
-    if (cdiv(N, 16) > 0x7FFFFFFF) return NVFP4_ERR_UNSUPPORTED;
+    if (N > kMaxGemvCols) return NVFP4_ERR_UNSUPPORTED;
     return NVFP4_OK;
 }
 

@@ -473,8 +473,8 @@ nvfp4_status nvfp4_route_backward(const float* dweights, const void* logits, int
  * for nvfp4_gemm, in either dtype.
  * This is the product of a decode step: it reads the weight once for every 16
  * rows.  Requirements: K % 16 == 0 (SCALE_2D: N % 16 == 0), codes 16-byte
- * aligned; m <= 1024 (else UNSUPPORTED).  m == 0 or N == 0 is a no-op; K == 0
- * writes zeros. */
+ * aligned; m <= 1024, N <= 2^29 - 32 (else UNSUPPORTED).  m == 0 or N == 0 is a
+ * no-op; K == 0 writes zeros. */
 nvfp4_status nvfp4_gemv(const void* x, int32_t dt /* nvfp4_dtype */, int64_t m, int64_t ldx, const nvfp4_tensor* W,
                         void* y, int32_t y_dt /* nvfp4_dtype */, int64_t ldy, int32_t ep /* nvfp4_epilogue */,
                         void* stream);

@@ -87,6 +87,23 @@ def test_expert_gemv_rejects_bad_arguments(lib):
     assert call(T=0, xr=0, x=None, ids=None, y=None, ws=None) == E["OK"]
 
 
+@pytest.mark.parametrize("rows", [2 ** 29, 2 ** 30, 2 ** 33])  # (of SwiGLU a multiple of 32)
+def test_more_rows_than_a_grid_holds(lib, rows):
+    """More than 2^29 - 32 rows of a matrix are refused: the workgroups of 256 threads
+    for each 32 of them would be more than one grid's 2^32 threads."""
+    def status(n):
+        w = lib.CTensor(65536, 65537, 65536, n, 16, 0)
+        yield lib.lib.nvfp4_gemv(65536, 1, 5, 16, ctypes.byref(w), 65536, 1, n, 0, None)
+        yield lib.lib.nvfp4_gemv(65536, 1, 5, 16, ctypes.byref(w), 65536, 1, n, 1, None)
+        m = lib.CMXTensor(65536, 65537, n, 32, 1)
+        yield lib.lib.nvfp4_mx_gemv(65536, 1, 5, 32, ctypes.byref(m), 65536, 1, n, None)
+        w = lib.CTensor(65536, 65537, 65536, 2 * n, 16, 0)
+        yield lib.lib.nvfp4_expert_gemv(65536, 1, 5, 16, 65536, 5, 1, ctypes.byref(w), 2, None, 65536, 1, n, 0, None, 0,
+                                        None)
+
+    assert set(status(rows)) == {E["UNSUP"]}
+
+
 def test_python_refusals(lib):
     x = torch.zeros(2, 64)
     w = lib.NVFP4Tensor.empty(32, 64, device="cpu")

@@ -85,3 +85,24 @@ def test_routing_of_many_tokens(nv):
         assert torch.equal(at[i:i + 16384], expect.int())
         t = p * period + torch.arange(period, device="cuda")
         assert torch.equal(order[expect], t.int())
+
+
+def repeated_weight(nv, rows, times):
+    """A weight of 16 columns whose rows repeat, and its first `rows`."""
+    g = torch.Generator().manual_seed(4)
+    codes = torch.randint(0, 256, (rows, 8), generator=g, dtype=torch.uint8).cuda()
+    scales = torch.randint(40, 80, (rows, 1), generator=g, dtype=torch.uint8).cuda()
+    ts = torch.full((1,), 0.5, device="cuda")
+    return (nv.NVFP4Tensor(codes, scales, ts, rows, 16),
+            nv.NVFP4Tensor(repeated(codes, times), repeated(scales, times), ts, rows * times, 16))
+
+
+@pytest.mark.parametrize("m", [1, 5])
+def test_product_with_many_rows(nv, m):
+    """The most rows of a weight that are taken, less 4096."""
+    needs(20)
+    small, large = repeated_weight(nv, 4096, 2 ** 17 - 1)
+    x = torch.randn(m, 16, generator=torch.Generator().manual_seed(5)).bfloat16().cuda()
+    want, got = nv.nvfp4_gemv(x, small), nv.nvfp4_gemv(x, large)
+    for i in range(m):
+        assert repeats(got[i], want[i])
