@@ -147,14 +147,27 @@ struct Tolerance {
     __device__ __forceinline__ float operator()(float x) const { return absolute + relative * x; }
 };
 
+// The error of a group's score x (+ y, unless -inf): those of x and y, each of
+// its own size however much of it cancels in the sum, and a rounding of the sum
+// and one of adding the error to it: absolute + 3 U (|x| + |y|), at most what
+// the tolerance's two counts of 2 U give, 1.5 times.  A score that stands for an infinity is
+// exact, and so is its sum with any under 2^70, which binary64 rounds away too.
+__device__ __forceinline__ float sum_error(float x, float y, Tolerance tol) {
+    const bool two = y > -__builtin_inff();
+    const float ax = fabsf(x), ay = two ? fabsf(y) : 0.0f, most = fmaxf(ax, ay), least = fminf(ax, ay);
+    if (most == -kLowest && (least < 0x1p70f || least == -kLowest)) return 0.0f;
+    return tol.absolute + 1.5f * tol.relative * (ax + ay);
+}
+
 // Which groups stay, from a and b, the best and second best key of the
 // caller's lane (-inf where there is none): `kept` tells whether the lane
 // belongs to one of the top_groups groups of the largest group score (ties to
-// the lower index).  score(a, b): the group score of a group's best two.
-// Returns false where a group that stays and one that does not are nearer than
-// twice the tolerance and not alike (`exact`: equal keys are equal scores).
-template <int LPT, typename Score, typename Tol>
-__device__ __forceinline__ bool keep_groups(float a, float b, const RouteShape& g, Score score, bool exact, Tol tol,
+// the lower index).  score(a, b): the group score of a group's best two;
+// error(a, b): how far it may be off.  Returns false where a group that stays
+// and one that does not are nearer than their errors and not alike (`exact`:
+// equal keys are equal scores; else equal ones without an error are).
+template <int LPT, typename Score, typename Error>
+__device__ __forceinline__ bool keep_groups(float a, float b, const RouteShape& g, Score score, Error error, bool exact,
                                             bool& kept) {
     const int lane = threadIdx.x & (LPT - 1), mine = lane >> g.lane_shift;
     const int first = threadIdx.x & 63 & ~(LPT - 1);  // the token's first lane of the wave
@@ -163,7 +176,7 @@ __device__ __forceinline__ bool keep_groups(float a, float b, const RouteShape& 
         b = fmaxf(fminf(a, a2), fmaxf(b, b2));
         a = fmaxf(a, a2);
     }
-    const float gs = score(a, b);
+    const float gs = score(a, b), err = error(a, b);
     const bool is = mine < g.groups;
     int ahead = 0;  // groups before the own one
     for (int o = 0; o < g.groups; ++o) {
@@ -172,16 +185,16 @@ __device__ __forceinline__ bool keep_groups(float a, float b, const RouteShape& 
     }
     kept = is && ahead < g.top_groups;
     const float none = -__builtin_inff();
-    const float least = -lanes_max<LPT>(kept ? -gs : none), most = lanes_max<LPT>(is && !kept ? gs : none);
-    const bool near = least - most <= 2.0f * tol(fmaxf(fabsf(least), fabsf(most)));
-    if (!__any(near)) return true;
+    const float least = -lanes_max<LPT>(kept ? err - gs : none), most = lanes_max<LPT>(is && !kept ? gs + err : none);
+    if (!__any(least <= most)) return true;
     bool certain = true;
     for (int o = 0; o < g.groups; ++o) {
         const int at = first + (o << g.lane_shift);
-        const float q = __shfl(gs, at), qa = __shfl(a, at), qb = __shfl(b, at);
+        const float qa = __shfl(a, at), qb = __shfl(b, at);
+        const float mine_of = score(a, b), q = score(qa, qb), off = error(a, b) + error(qa, qb);
         const bool other = __shfl((int)kept, at) != (int)kept;
-        if (is && other && fabsf(q - gs) <= 2.0f * tol(fmaxf(fabsf(q), fabsf(gs))) && !(exact && qa == a && qb == b))
-            certain = false;
+        const bool alike = exact ? qa == a && qb == b : q == mine_of && off == 0.0f;
+        if (is && other && fabsf(q - mine_of) <= off && !alike) certain = false;
     }
     return certain;
 }
@@ -427,15 +440,15 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int* 
         }
         bool kept;
         if (!g.group_top2 && !a.bias) {
-            keep_groups<LPT>(best, second, g, [](float x, float) { return x; }, true, [](float) { return -1.0f; }, kept);
+            keep_groups<LPT>(best, second, g, [](float x, float) { return x; }, [](float, float) { return -1.0f; }, true, kept);
         } else if (a.bias) {
             const bool two = g.group_top2;
-            certain = keep_groups<LPT>(best, second, g, [=](float x, float y) { return two && y > none ? x + y : x; }, false,
-                                       tol, kept);
+            certain = keep_groups<LPT>(best, second, g, [=](float x, float y) { return two && y > none ? x + y : x; },
+                                       [=](float x, float y) { return sum_error(x, two ? y : none, tol); }, false, kept);
         } else {
             const auto p = [=](float l) { return softmax ? quick_exp(l - m) : quick_sigmoid(l); };
-            certain = keep_groups<LPT>(best, second, g, [=](float x, float y) { return y > none ? p(x) + p(y) : p(x); }, true,
-                                       tol, kept);
+            certain = keep_groups<LPT>(best, second, g, [=](float x, float y) { return y > none ? p(x) + p(y) : p(x); },
+                                       [=](float x, float y) { return sum_error(p(x), y > none ? p(y) : none, tol); }, true, kept);
         }
 #pragma unroll
         for (int j = 0; j < V; ++j) s[j] = kept ? s[j] : none;

@@ -174,6 +174,46 @@ def test_scores_nearer_than_binary32(nv, sigmoid):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("size", [64.0, 1e3, 1e4, 1e6])
+def test_groups_whose_best_two_cancel(nv, size, sigmoid):
+    """A favoured and a barred expert in each group: the sum of their scores is
+    near 1, but each is rounded by its own size.  Ordinary logits, and logits so
+    near that the groups' sums differ by about those roundings."""
+    g = np.random.default_rng(12)
+    for n in (16, 64):
+        bias = np.full((8, n // 8), -2 * size)
+        bias[:, 0], bias[:, 1] = size, -size
+        bias = torch.from_numpy(bias.reshape(-1)).float().cuda()
+        for spread in (1.0, size * 2.0 ** -23):
+            l = torch.from_numpy(spread * g.standard_normal((1000, n))).float().cuda()
+            check(nv, l, 4, bias, sigmoid, 8, 4)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_groups_with_masked_experts(nv, sigmoid, dtype):
+    """Experts masked by a bias of -inf, of NaN or of the lowest value: groups
+    without a live one, with one (a sum that the masked one rounds away: ties to
+    the lower index) and with more; and experts that a bias of inf makes certain."""
+    inf, low = float("inf"), torch.finfo(torch.float32).min
+    l = make(13, 200, 64, DT[dtype])
+    for mask in (-inf, low, float("nan")):
+        bias = 0.05 * torch.randn(64, generator=torch.Generator().manual_seed(14))
+        bias[:8] = mask           # group 0: none left
+        bias[9:16] = mask         # 1 and 3: one
+        bias[24:31] = mask
+        bias[34:40] = mask        # 4: two
+        bias[56:] = mask          # 7: none
+        for top_groups in (2, 5, 7):
+            check(nv, l, 6, bias.cuda(), sigmoid, 8, top_groups)
+            check(nv, l, 6, bias.cuda(), sigmoid, 8, top_groups, top2=False)
+        bias[50], bias[20], bias[21] = inf, inf, inf
+        check(nv, l, 6, bias.cuda(), sigmoid, 8, 3)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_ties_go_to_the_lower_index(nv, dtype):
     g = np.random.default_rng(4)
