@@ -186,7 +186,8 @@ __device__ __forceinline__ bool keep_groups(float a, float b, const RouteShape& 
     kept = is && ahead < g.top_groups;
     const float none = -__builtin_inff();
     const float least = -lanes_max<LPT>(kept ? err - gs : none), most = lanes_max<LPT>(is && !kept ? gs + err : none);
-    if (!__any(least <= most)) return true;
+    // (a sum past binary32 has an infinite error: it may be any score)
+    if (!__any(least <= most || (is && err == -none))) return true;
     bool certain = true;
     for (int o = 0; o < g.groups; ++o) {
         const int at = first + (o << g.lane_shift);
@@ -194,7 +195,7 @@ __device__ __forceinline__ bool keep_groups(float a, float b, const RouteShape& 
         const float mine_of = score(a, b), q = score(qa, qb), off = error(a, b) + error(qa, qb);
         const bool other = __shfl((int)kept, at) != (int)kept;
         const bool alike = exact ? qa == a && qb == b : q == mine_of && off == 0.0f;
-        if (is && other && fabsf(q - mine_of) <= off && !alike) certain = false;
+        if (is && other && !(fabsf(q - mine_of) > off) && !alike) certain = false;
     }
     return certain;
 }

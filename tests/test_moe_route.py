@@ -191,6 +191,21 @@ def test_groups_whose_best_two_cancel(nv, size, sigmoid):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_group_sums_past_binary32(nv, sigmoid):
+    """Biases whose sums no binary32 holds, of either sign, beside ordinary and
+    masked groups."""
+    inf = float("inf")
+    l = make(15, 50, 16, torch.float32)
+    for bias in ([-3e38, -2e38, -3e38, -1e38, -3e38, -3e38, -3e38, -0.5e38, -1e38, -3.2e38, -inf, -inf, -2e38, -2e38, -3e38, -inf],
+                 [3e38, 2e38, 3e38, 1e38, 3e38, 3e38, 3e38, 0.5e38, 1e38, 3.2e38, inf, inf, 2e38, 2e38, 3e38, inf],
+                 [0, 0, -3e38, -1e38, -3e38, -3e38, 0, 0, 3e38, 1e38, 3e38, 3e38, -inf, -inf, 3e38, -3e38]):
+        bias = torch.tensor(bias, device="cuda")
+        for top_groups in range(1, 8):
+            check(nv, l, 2, bias, sigmoid, 8, top_groups)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("sigmoid", [False, True])
 def test_groups_with_masked_experts(nv, sigmoid, dtype):
