@@ -5,7 +5,8 @@
 // groups of the largest group score (the largest s, or the sum of the two
 // largest) stay; the top_k experts of the largest s among them are chosen
 // (ties to the lower index) and weighted by p, divided by the chosen ones' sum
-// with renorm.  The dispatch plan sorts the T * k assignments (token-major) by
+// with renorm.  Without a bias experts, and groups by their largest, go by the
+// logits themselves, in whose order their scores are.  The dispatch plan sorts the T * k assignments (token-major) by
 // expert, stably: order (assignment at each sorted place), its inverse
 // position, and offsets (the first place of each expert).
 //
@@ -322,6 +323,8 @@ __device__ __forceinline__ int choose_exactly(const RouteArgs& a, int64_t t, dou
     for (int e = lane; e < E; e += 64) {
         const double p = score[e] / total;
         score[e] = a.bias ? comparable(p + (double)a.bias[e]) : p;
+        // (as on the quick path: without a bias only sums of two compare scores)
+        if (!a.bias && !g.group_top2) score[e] = (double)logit(load1(a.logits, a.bf16, row + e));
     }
     __builtin_amdgcn_wave_barrier();
     if (g.top_groups < g.groups) {
@@ -345,8 +348,7 @@ __device__ __forceinline__ int choose_exactly(const RouteArgs& a, int64_t t, dou
         for (int e = lane; e < E; e += 64)
             if (!(kept >> (e / g.group_size) & 1)) score[e] = none;
     }
-    // without a bias, the kept experts by their logits (their scores may
-    // underflow to ties)
+    // without a bias, the kept experts by their logits
     if (!a.bias)
 #pragma unroll 1
         for (int e = lane; e < E; e += 64)

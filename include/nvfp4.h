@@ -428,8 +428,12 @@ size_t nvfp4_route_workspace_size(int64_t tokens, int64_t experts);
  * row stride ld): scores p (softmax of the row, or the sigmoid of each);
  * selection scores s = p + bias; the top_groups groups of the largest group
  * score stay, and the top_k experts of the largest s among them are chosen, in
- * that order; ties of scores go to the lower index, and scores are compared as
- * binary64 evaluation of these formulas orders them.
+ * that order; ties go to the lower index, and scores are compared as binary64
+ * evaluation of these formulas orders them.  Without a bias experts, and groups
+ * of NVFP4_GROUP_MAX, are compared by their logits: the scores' own order, which
+ * also tells apart those that binary64 rounds alike (sigmoids of 40 and 48, the
+ * softmax of -800 beside 0).  A bias of zeros compares the rounded scores, whose ties
+ * go to the lower index.
  *   ids      tokens x top_k: the chosen experts;
  *   weights  tokens x top_k floats: their p, divided by their sum with renorm.
  * The dispatch plan (offsets, order and position all given, or all NULL),

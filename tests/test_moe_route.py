@@ -191,6 +191,38 @@ def test_groups_whose_best_two_cancel(nv, size, sigmoid):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_scores_that_binary64_rounds_alike(nv, dtype):
+    """Sigmoids of 17 to 60, many of which are 1 in binary64, and softmax scores
+    that underflow: by the logits without a bias, ties with a bias of zeros."""
+    g = np.random.default_rng(16)
+    l = torch.from_numpy(g.uniform(17, 60, (60, 64))).to(DT[dtype]).cuda()
+    low = torch.from_numpy(g.uniform(-1500, -700, (60, 64))).to(DT[dtype]).cuda()
+    low[:, 5] = 0.0
+    zeros = torch.zeros(64, device="cuda")
+    for logits, sigmoid in ((l, True), (low, False)):
+        for b in (None, zeros):
+            check(nv, logits, 8, b, sigmoid)
+            check(nv, logits, 8, b, sigmoid, 8, 3)
+            check(nv, logits, 8, b, sigmoid, 8, 3, top2=False)
+    row = l[:1].sort(dim=1).values
+    r, z = (nv.nvfp4_route(row, 4, bias=b, score=nv.NVFP4_ROUTE_SIGMOID) for b in (None, zeros))
+    assert torch.equal(r.ids[0].long(), row[0].sort(descending=True, stable=True).indices[:4]) and z.ids[0, 0] < 60
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("top_k", [3, 8])
+def test_many_near_experts_in_groups_without_a_bias(nv, top_k):
+    """More near experts than the quick path settles: the groups of the largest
+    logits stay, though all sigmoids are 1 in binary64."""
+    l = torch.full((4, 128), 40.0, device="cuda")
+    l[0, 64:], l[1, 64:], l[2, :64] = 50.0, 40.000004, 50.0
+    r = check(nv, l, top_k, None, True, 2, 1, top2=False)
+    assert r.ids[:, 0].tolist() == [64, 64, 0, 0]
+    check(nv, l, top_k, None, True, 2, 1)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("sigmoid", [False, True])
 def test_group_sums_past_binary32(nv, sigmoid):
     """Biases whose sums no binary32 holds, of either sign, beside ordinary and
