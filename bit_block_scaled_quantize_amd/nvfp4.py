@@ -535,11 +535,12 @@ def nvfp4_route(logits, top_k, bias=None, score=NVFP4_ROUTE_SOFTMAX, groups=1, t
     [experts]) within the top_groups groups of the largest group score, and
     their weights.  plan=True also sorts the tokens * top_k assignments by
     expert (offsets feed nvfp4_grouped_gemm; order // top_k are the tokens to
-    gather).  out: a RouteOutput of preallocated tensors."""
+    gather).  out: a RouteOutput of preallocated tensors for some or all of what
+    is asked for; the result holds them and new ones for the others."""
     o = (None,) * 5 if out is None else (out.ids, out.weights, out.offsets, out.order, out.position)
     r = _native.route(logits, top_k, bias, score, groups, top_groups, group_score, renorm, plan, *o, workspace,
                       _handle(stream))
-    return RouteOutput(*r) if out is None else out
+    return RouteOutput(*r)
 
 
 @_launches_on_stream

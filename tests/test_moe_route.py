@@ -315,6 +315,25 @@ def test_strided_logits(nv, dtype):
 
 
 @pytest.mark.gpu
+def test_given_outputs(nv):
+    """Some tensors given: the result has them and new ones for the rest; without
+    a plan it holds none, whatever the given object still has of an earlier call."""
+    l = make(17, 30, 32, torch.float32)
+    want = nv.nvfp4_route(l, 4)
+    some = nv.RouteOutput(torch.empty_like(want.ids), torch.empty_like(want.weights))
+    got = nv.nvfp4_route(l, 4, out=some)
+    assert got.ids is some.ids and got.weights is some.weights
+    for a, b in zip((want.ids, want.weights, want.offsets, want.order, want.position),
+                    (got.ids, got.weights, got.offsets, got.order, got.position)):
+        assert torch.equal(a, b)
+    plan = [t.clone() for t in (got.offsets, got.order, got.position)]
+    again = nv.nvfp4_route(-l, 4, plan=False, out=got)
+    assert again.ids is got.ids and again.offsets is None and again.order is None and again.position is None
+    assert all(torch.equal(a, b) for a, b in zip(plan, (got.offsets, got.order, got.position)))
+    assert torch.equal(again.ids, nv.nvfp4_route(-l, 4).ids)
+
+
+@pytest.mark.gpu
 def test_no_tokens(nv):
     r = nv.nvfp4_route(torch.zeros(0, 16, device="cuda"), 4)
     assert r.ids.shape == (0, 4) and (r.offsets == 0).all()
