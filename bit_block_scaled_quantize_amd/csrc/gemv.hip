@@ -593,13 +593,19 @@ __global__ void __launch_bounds__(512) k_gemv4(const GemvArgs p) {
     }
 }
 
-// y[t] = sum over j of weights[t][j] parts[t top_k + j], in order.
+// y[t] = sum over j of weights[t][j] parts[t top_k + j], in order, of the
+// assignments that have an expert (whatever weight the others have).
 __global__ void __launch_bounds__(256) k_expert_sum(const float* __restrict__ parts, const float* __restrict__ weights,
-                                                    int top_k, int64_t n, void* y, bool bf16, int64_t ldy) {
+                                                    const int* __restrict__ ids, int experts, int top_k, int64_t n, void* y,
+                                                    bool bf16, int64_t ldy) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, t = blockIdx.y;
     if (i >= n) return;
     float v = 0.0f;
-    for (int j = 0; j < top_k; ++j) v = __builtin_fmaf(weights[t * top_k + j], parts[(t * top_k + j) * n + i], v);
+    for (int j = 0; j < top_k; ++j) {
+        const int id = ids[t * top_k + j];
+        const float sum = __builtin_fmaf(weights[t * top_k + j], parts[(t * top_k + j) * n + i], v);
+        v = id >= 0 && id < experts ? sum : v;
+    }
     store1(y, bf16, t * ldy + i, v);
 }
 
@@ -689,7 +695,7 @@ hipError_t launch_expert_gemv(GemvArgs p, bool swiglu, const float* weights, flo
     const hipError_t e = launch_gemv(p, swiglu, s);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(k_expert_sum, dim3((unsigned)v_cdiv(outs, 256), (unsigned)(p.assignments / p.top_k)), dim3(256), 0,
-                       s, ws, weights, p.top_k, outs, y, bf16, ldy);
+                       s, ws, weights, p.ids, p.experts, p.top_k, outs, y, bf16, ldy);
     return hipGetLastError();
 }
 

@@ -355,6 +355,20 @@ def test_expert_gemv_foreign_and_repeated_ids(nv):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("hole", [float("nan"), float("inf"), -float("inf"), 3e38])
+def test_weights_without_an_expert(nv, hole):
+    """Whatever weight an assignment without an expert has, it adds nothing."""
+    w = make_w(nv, 42, 3 * 48, 160, "nv2d", 3)
+    ids = torch.tensor([[0, -1, 2], [3, 2, 1], [1, 0, 9], [7, -9, 3]], dtype=torch.int32, device="cuda")
+    wt = torch.rand(4, 3, generator=torch.Generator().manual_seed(43)).cuda()
+    x = make_x(44, 4, 160, torch.bfloat16)
+    want = nv.nvfp4_expert_gemv(x, ids, w, 3, weights=wt)
+    holes = torch.where((ids >= 0) & (ids < 3), wt, torch.full_like(wt, hole))
+    got = nv.nvfp4_expert_gemv(x, ids, w, 3, weights=holes)
+    assert torch.equal(got, want) and (got[3] == 0).all()
+
+
+@pytest.mark.gpu
 def test_offsets_past_32_bits(nv):
     """A stack of experts of over 2^32 bytes of codes: its last one."""
     experts, n, K = 300, 2048, 14336
