@@ -4,11 +4,13 @@ of a mixture-of-experts block the compiled module _native.
 Argument marshalling only: every step of quantize / dequantize / GEMM runs in
 the HIP kernels behind the C ABI.  PyTorch supplies device memory (output
 tensors are allocated with torch) and the current HIP stream.  If the built
-library is missing, importing this module raises -- there is no fallback.
+library is missing, importing this module raises -- there is no fallback;
+without the compiled module the operators that need it raise.
 """
 import contextlib
 import ctypes
 import functools
+import importlib
 import os
 from dataclasses import dataclass
 
@@ -127,10 +129,25 @@ def _load():
 
 
 lib = _load()
+
+
+class _NoBinding:
+    """In place of _native where it does not load: the operators that go through
+    it raise what kept it from loading, the others run."""
+
+    def __init__(self, cause):
+        self._cause = cause
+
+    def __getattr__(self, name):
+        built = os.path.exists(os.path.join(_HERE, "_native.so"))
+        raise ImportError(f"the compiled binding _native.so {'does not load' if built else 'is not built'} "
+                          f"({self._cause}); run bit_block_scaled_quantize_amd/build.py") from self._cause
+
+
 try:
-    from . import _native  # (linked against the library just loaded)
+    _native = importlib.import_module("._native", __package__)  # (linked against the library just loaded)
 except ImportError as e:
-    raise ImportError("the Python binding _native.so is not built; run bit_block_scaled_quantize_amd/build.py") from e
+    _native = _NoBinding(e)
 
 
 class NVFP4Error(RuntimeError):
@@ -458,7 +475,10 @@ def nvfp4_mx_gemm(A, B, out_dtype=torch.float32, out=None, accum=NVFP4_MX_ACC_NA
 
 # ---------------------------------------------------------------- MoE-block operators
 # (checks, allocation and the calls themselves in csrc/binding.cpp)
-_native.setup(NVFP4Error, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+if not isinstance(_native, _NoBinding):
+    # (a torch without a GPU build has neither function, and no tensor that asks for them)
+    _native.setup(NVFP4Error, getattr(torch._C, "_cuda_getDevice", None),
+                  getattr(torch._C, "_cuda_getCurrentRawStream", None))
 
 
 def _handle(stream):
