@@ -14,7 +14,6 @@ Flags that matter for correctness:
                                no packed FP32 instructions are generated.
 """
 import concurrent.futures
-import importlib.util
 import os
 import shutil
 import subprocess
@@ -64,10 +63,13 @@ def _compile_binding():
     cxx = shutil.which("g++") or shutil.which("c++")
     if cxx is None:
         raise RuntimeError("no host C++ compiler found; the Python binding cannot be built")
-    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    import torch  # (the C library is built without it)
+    torch_dir = os.path.dirname(torch.__file__)
     inc = os.path.join(torch_dir, "include")
     obj = os.path.join(BUILD, "binding.o")
-    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall", "-Wno-unused-function", "-I", INCLUDE,
+    # (the std::string of torch's own interface)
+    abi = f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"
+    cmd = [cxx, "-O2", "-std=c++17", abi, "-fPIC", "-fvisibility=hidden", "-Wall", "-Wno-unused-function", "-I", INCLUDE,
            "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
            "-isystem", sysconfig.get_paths()["include"], "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -93,14 +95,13 @@ def build(verbose=False):
     with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         binding = ex.submit(_compile_binding)
         objs = list(ex.map(_compile, SOURCES))
-        binding = binding.result()
     tmp = LIB + ".tmp"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_binding(*binding)
+    _link_binding(*binding.result())  # (the library is there whether or not the binding can be)
     if verbose:
         print(LIB)
     return LIB
