@@ -248,6 +248,25 @@ def test_every_code_and_scale_exactly(nv, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows", [4, 16])
+@pytest.mark.parametrize("byte", [0, 1, 2, 3, 252, 253, 254])
+def test_mx_scale_bytes_at_the_ends(nv, byte, rows):
+    """Normal weights are exact, smaller ones exact or zero; of the largest scales
+    the weights that binary32 holds (the others are infinite)."""
+    top = {253: 3, 254: 2}.get(byte, 7)  # code of the largest magnitude below 2^128 / 2^(byte - 127)
+    low = np.arange(256) & 7
+    codes = np.arange(256)[(low <= top) & (np.arange(256) >> 4 & 7 <= top)][:64]
+    codes = torch.from_numpy(np.resize(codes, 64).astype(np.uint8)).cuda().repeat(16, 1)
+    w = nv.MXTensor(codes, torch.full((16, 4), byte, dtype=torch.uint8, device="cuda"), 16, 128, nv.NVFP4_MX_E2M1)
+    want = P.mx_weight(w).T
+    small = np.abs(want) < 2.0 ** -126
+    for dt in DT.values():
+        x = torch.eye(128, device="cuda").to(dt)
+        got = np.concatenate([P.host(nv.nvfp4_mx_gemv(x[i:i + rows], w, out_dtype=torch.float32)) for i in range(0, 128, rows)])
+        assert (((got == want) | (small & (got == 0)))).all()
+
+
+@pytest.mark.gpu
 def test_binary32_x_is_not_rounded(nv):
     """x values that need all 24 bits: each product with a power of two is exact."""
     g = np.random.default_rng(2)
