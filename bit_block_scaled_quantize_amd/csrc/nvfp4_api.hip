@@ -429,7 +429,7 @@ nvfp4_status nvfp4_rmsnorm(const void* x, int64_t ldx, const void* residual, int
 }
 
 size_t nvfp4_rmsnorm_backward_workspace_size(int64_t rows, int64_t cols) {
-    if (rows < 0 || cols < 1 || cols > kMaxNormCols) return 0;
+    if (rows < 0 || rows > 0x7FFFFFFF || cols < 1 || cols > kMaxNormCols) return 0;
     return (size_t)rmsnorm_backward_workspace_floats(rows, cols) * sizeof(float);
 }
 
@@ -458,7 +458,7 @@ nvfp4_status nvfp4_rmsnorm_backward(const void* dy, int64_t lddy, const void* h,
 
 // ---------------------------------------------------------------- routing
 size_t nvfp4_route_workspace_size(int64_t tokens, int64_t experts) {
-    if (tokens < 0 || experts < 1 || experts > kMaxExperts) return 0;
+    if (tokens < 0 || tokens > 0x7FFFFFFF || experts < 1 || experts > kMaxExperts) return 0;
     return route_workspace_bytes(tokens, (int)experts);
 }
 
@@ -481,7 +481,7 @@ nvfp4_status nvfp4_route(const void* logits, int32_t dt /* nvfp4_dtype */, int64
     if (!aligned(ids, 4) || !aligned(weights, 4) || !aligned(offsets, 8) || !aligned(order, 4) ||
         !aligned(position, 4) || !aligned(opts->bias, 4))
         return NVFP4_ERR_ALIGN;
-    if (experts > kMaxExperts || k > kMaxTopK || !route_shape_fits((int)experts, (int)G) || tokens * k > 0x7FFFFFFF)
+    if (experts > kMaxExperts || k > kMaxTopK || !route_shape_fits((int)experts, (int)G) || tokens > 0x7FFFFFFF / k)
         return NVFP4_ERR_UNSUPPORTED;
     const size_t need = offsets ? nvfp4_route_workspace_size(tokens, experts) : 0;
     if (need) {
