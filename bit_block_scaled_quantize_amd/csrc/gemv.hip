@@ -26,10 +26,16 @@
 // that together they stream whole rows, the next unit's loads under way while
 // one is multiplied, and their sums are added through LDS in a fixed order.
 //
-// Measured (a large copy: 5.07 TB/s): one BF16 row, 20480 x 5120 with 16x16
-// scales, 12.0 us (4.4 TB/s); 8 rows, 8192 x 8192 MXFP4, 11.1 us (3.2); four
-// tokens through 4 of 32 experts of 7168 / 2048, up with SwiGLU, down and
-// weighted sum, 67 to 72 us (4.1 to 4.4).
+// Measured (a large copy: 5.07 TB/s) on one weight again and again, which the
+// 256 MB memory-side cache then holds, and on 16 weights in turn, which it does
+// not: one BF16 row, 20480 x 5120 with 16x16 scales, 11.9 to 12.7 us and 14.0 (3.8
+// TB/s); 4 rows 15.4 and 16.6, binary32 24.9 and 26.3; 8 rows 19.6 and 21.5,
+// binary32 29.7 and 31.5; 8 rows, 8192 x 8192 MXFP4, 10.3 to 11.1 and 13.2 (2.7
+// TB/s).  Four tokens through 4 of 32 experts of 7168 / 2048, up with SwiGLU, down
+// and weighted sum: 68 to 71 us (4.2 to 4.3 TB/s, from memory); one token 25.0.
+// With more than 4 rows an NVFP4 weight costs 2.7 vector instructions, and binary32
+// x three times the matrix instructions (its instances for SwiGLU and for experts
+// keep 2 registers in scratch memory).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -612,10 +618,13 @@ __global__ void __launch_bounds__(256) k_expert_sum(const float* __restrict__ pa
 inline int64_t v_cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Up to 4 rows of x.  Waves of a workgroup: 1, 2, 4 or 8, as many as make 1280
-// in all (5 a compute unit), but two unless there are 6 tiles a unit: longer
-// streams a wave pay beyond that (one BF16 row: 20480 x 5120 with 1, 2, 4 waves 13.5,
+// in all (5 a compute unit), but two unless there are more than 6 tiles a unit:
+// longer streams a wave pay beyond that (one BF16 row: 20480 x 5120 with 1, 2, 4 waves 13.5,
 // 12.0, 13.7 us; 8192 x 8192 with 3, 4, 5 11.9, 12.4, 14.3; 5120 x 20480 with 4,
-// 5, 8 18.6, 22.1, 20.1; 13 experts' 7168 x 2048 with 1, 2, 4 24.6, 28.2, 36.6).
+// 5, 8 18.6, 22.1, 20.1; 13 experts' 7168 x 2048 with 1, 2, 4 24.6, 28.2, 36.6.
+// On each side of the step, one wave and two, weights in turn: of 5120 columns 1536
+// tiles 15.7 and 14.8, 1600 tiles 16.3 and 17.0; of 2048 columns 8.4 and 8.1, 8.5 and
+// 9.5; of 8192 columns 25.9 and 24.2, 27.4 and 27.6).
 template <int FMT, bool XF32, bool SWIGLU, bool EXPERT>
 void gemv4_launch(const GemvArgs& p, hipStream_t s) {
     constexpr int R = 4, G = SWIGLU ? R / 2 : R;
@@ -649,7 +658,10 @@ void gemv_launch(const GemvArgs& p, hipStream_t s) {
 template <int FMT, bool XF32, bool SWIGLU, bool EXPERT>
 hipError_t gemv_shaped(GemvArgs p, hipStream_t s) {
     p.rows = (int)std::min<int64_t>(EXPERT ? p.assignments / p.top_k : p.m, XF32 ? 8 : kCols);
-    // (two assignments or fewer to an expert on the average seldom make five)
+    // Two assignments or fewer to an expert on the average seldom make five; where
+    // they do, each four of them read the expert's matrix again (64 tokens, one
+    // expert each of 32, 7168 / 2048: spread 146 us, all on one expert 200, where
+    // the 16-column form takes 91).
     if (p.rows <= 4 || (EXPERT && p.assignments <= 2 * p.experts)) {
         gemv4_launch<FMT, XF32, SWIGLU, EXPERT>(p, s);
     } else {

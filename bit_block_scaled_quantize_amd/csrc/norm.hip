@@ -22,10 +22,16 @@
 // sum and the outputs, so every array is read or written once: TPR threads
 // share a row (16, 64, 256, 512 or 1024), each holding NC chunks of 8 consecutive
 // elements (chunk i of thread t starts at 8 (i TPR + t)), so a wave's 16-byte
-// accesses are contiguous and four lanes hold one 32-element MX block.
-// Measured, BF16: forward with h, y and MXFP8 codes, 8192 x 5120, 84.1 us or
-// 4.50 TB/s; backward with dh, 16384 x 7168, 185 us or 5.07 TB/s (a large copy
-// reaches 5.07).
+// accesses are contiguous and four lanes hold one 32-element MX block.  The widest
+// rows are the exceptions: the forward kernel of BF16 rows past 16384 columns, four
+// chunks a thread, keeps 44 of its values in scratch memory, and the backward
+// kernel reads rows past 8192 columns twice, the second time from the cache.
+// Measured (a large copy reaches 5.07 TB/s), BF16: forward with h, y and MXFP8
+// codes, 8192 x 5120, 84 us or 4.51 TB/s; without the codes 67 (5.0); MXFP4
+// without y 70; 2560 x 16384 with both 88, 1280 x 32768 114.  Binary32, 8192 x 5120:
+// 130 (5.2), with codes 138.  Backward with dh, 16384 x 7168, 183 us or 5.13 TB/s,
+// binary32 356; 2048 x 16384 67.5 (4.0), 1024 x 32768 89.6 (3.0).  Rows of zeros,
+// whose every y passes by the border check, cost nothing that shows (86).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

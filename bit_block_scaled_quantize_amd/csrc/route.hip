@@ -22,9 +22,18 @@
 // of selection.  A token is shared by 16 lanes (4 tokens a wave) where they
 // hold its scores, so a round's reduction is four register exchanges; a lane
 // sorts its keys once, and a round takes the largest head.  Measured: 16384
-// tokens, top 8 of 256 in 8 groups, sigmoid with bias, 27.7 us (choice 21, plan
-// 7); top 4 of 32, softmax, 12.9 us (7 and 5); one token 8.7 us; backward with
-// score gradients, 16384 x 256 BF16, 10.3 us (3.3 TB/s).
+// tokens, top 8 of 256 in 8 groups, sigmoid with bias, 27 to 29 us (choice 20 to
+// 25, plan 7); top 4 of 32, softmax, 12.7 us (7 and 5); one token 8.7 us; 4096
+// tokens of 512, 1024 and 2048 experts 18, 31 and 86; backward with score
+// gradients, 16384 x 256 BF16, 10.3 us (3.3 TB/s), sigmoid 12.9.
+//
+// The kernels of 16 values on 16 lanes and of 32 on 64 keep some of them in
+// scratch memory (15 and 64 registers).  Tokens that binary64 has to settle whole go
+// one by one through a wave (choose_exactly): more near scores than candidates
+// (binary32 logits all alike, 16384 x 256: 62 us, in groups 82; fewer live experts
+// than top_k: 62), and sums of two scores that all lie below the binary32 scores'
+// error (sigmoids of logits around -16 in groups without a bias: 79).  Experts and
+// groups masked by a bias do not: 25 to 29.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

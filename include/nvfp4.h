@@ -472,11 +472,14 @@ nvfp4_status nvfp4_route_backward(const float* dweights, const void* logits, int
  * quantized) and an NVFP4 weight W (N x K, SCALE_1D or SCALE_2D):
  *   y[i][n] = s_W * sum_k x[i][k] (v_W sb_W)[n][k], exact products of BF16 x
  *   (of binary32 x: of its three BF16 parts, which hold it to 2^-133) summed in
- *   binary32, rounded once to y_dt; m x N, row stride ldy.
+ *   binary32, rounded once to y_dt; m x N, row stride ldy.  A row of x that is not
+ *   finite gives unspecified results (an infinite binary32 x gives NaN), the
+ *   other rows theirs; sums of 16 products x v must stay in binary32's range.
  * EPI_SWIGLU: N = 2F, F % 16 == 0; y (m x F) = gate * sigmoid(gate) * up as
  * for nvfp4_gemm, in either dtype.
- * This is the product of a decode step: it reads the weight once for every 16
- * rows.  Requirements: K % 16 == 0 (SCALE_2D: N % 16 == 0), codes 16-byte
+ * This is the product of a decode step: it reads the weight once for up to 16
+ * rows of BF16 x (8 of binary32 x) and again for every 16 (8) more.
+ * Requirements: K % 16 == 0 (SCALE_2D: N % 16 == 0), codes 16-byte
  * aligned; m <= 1024, N <= 2^29 - 32 (else UNSUPPORTED).  m == 0 or N == 0 is a
  * no-op; K == 0 writes zeros. */
 nvfp4_status nvfp4_gemv(const void* x, int32_t dt /* nvfp4_dtype */, int64_t m, int64_t ldx, const nvfp4_tensor* W,
@@ -484,7 +487,8 @@ nvfp4_status nvfp4_gemv(const void* x, int32_t dt /* nvfp4_dtype */, int64_t m, 
                         void* stream);
 
 /* nvfp4_gemv for an MXFP4 weight (W->elem == NVFP4_MX_E2M1, else UNSUPPORTED;
- * K % 32 == 0).  Weights of magnitude below 2^-126 may count as zero. */
+ * K % 32 == 0).  Weights of magnitude below 2^-126 may count as zero, and those
+ * of 2^128 and more are infinite, as nvfp4_mx_dequantize gives them. */
 nvfp4_status nvfp4_mx_gemv(const void* x, int32_t dt /* nvfp4_dtype */, int64_t m, int64_t ldx,
                            const nvfp4_mx_tensor* W, void* y, int32_t y_dt /* nvfp4_dtype */, int64_t ldy,
                            void* stream);
@@ -504,7 +508,9 @@ size_t nvfp4_expert_gemv_workspace_size(int64_t tokens, int32_t top_k, int64_t n
  *   weights[t][j] * product, in binary32 and a fixed order (tokens rows;
  *   assignments without an expert add nothing); ws_bytes >=
  *   nvfp4_expert_gemv_workspace_size(tokens, top_k, output columns).
- * An expert's matrix is read once for every 16 of its assignments.
+ * An expert's matrix is read once for every 4 of its assignments where there are
+ * 4 tokens or fewer, or two assignments or fewer to an expert on the average; else
+ * for every 16 (8 of binary32 x).
  * Requirements as for nvfp4_gemv; W->rows % experts == 0 (SCALE_2D: N % 16 ==
  * 0); top_k >= 1; tokens * top_k <= 1024 (else UNSUPPORTED; nvfp4_grouped_gemm
  * is the path of many tokens).  tokens == 0 is a no-op. */
