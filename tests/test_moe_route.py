@@ -394,6 +394,31 @@ def test_backward(nv, T, n, k, sigmoid, dtype):
 
 
 @pytest.mark.gpu
+def test_sigmoids_below_the_normal_numbers(nv):
+    """Logits of -80 to -104 beside ordinary ones: weights and gradients down to
+    binary32's smallest numbers.  An exponential within 2 steps of 2^-149 and one
+    rounding after it; a gradient's term multiplies the steps by its factors and
+    is rounded four times."""
+    step = 2.0 ** -149
+    l = torch.from_numpy(np.random.default_rng(18).uniform(-104, -80, (40, 12))).float().cuda()
+    l[:, 5] = torch.linspace(-3, 3, 40)
+    g = np.random.default_rng(19)
+    dw, ds = g.standard_normal((40, 8)).astype(np.float32), g.standard_normal((40, 12)).astype(np.float32)
+    for renorm in (True, False):
+        r = nv.nvfp4_route(l, 8, score=nv.NVFP4_ROUTE_SIGMOID, renorm=renorm)
+        ids, w = P.route(P.host(l), 8, None, True, renorm=renorm)
+        assert np.array_equal(r.ids.cpu().numpy(), ids)
+        scale = 1.0 / P.scores(P.host(l), True).max(axis=1, keepdims=True) if renorm else 1.0
+        assert (np.abs(P.host(r.weights) - w) <= 16 * P.U * w + 2 * step * scale + step).all()
+        got = nv.nvfp4_route_backward(torch.from_numpy(dw).cuda(), l, r.ids, score=nv.NVFP4_ROUTE_SIGMOID, renorm=renorm,
+                                      dscores=torch.from_numpy(ds).cuda())
+        a = (dw.astype(np.float64), P.host(l), ids, True, renorm, ds.astype(np.float64))
+        want = P.route_backward(*a)
+        factors = np.abs(ds) + 2 * np.abs(dw).max(axis=1, keepdims=True) * scale
+        assert (np.abs(P.host(got) - want) <= backward_tol(*a, want, torch.float32, 12) + (2 * factors + 4) * step).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("sigmoid", [False, True])
 def test_backward_against_differences(nv, sigmoid):
     l = make(9, 6, 48, torch.float32)
