@@ -81,6 +81,14 @@ __device__ __forceinline__ float exp_diff(float l, float m) {
     return __builtin_isfinite(err) ? __builtin_fmaf(e, err, e) : e;
 }
 
+// The score of l by e^m, m the largest of the logits that share a sum: of
+// sigmoids of negative logits, which are to be normalised and of which binary32
+// may hold the quotients alone.
+__device__ __forceinline__ float share(float l, float m, bool softmax) {
+    const float e = exp_diff(l, m);
+    return softmax ? e : e / (1.0f + expf(l));
+}
+
 // Reductions over the LPT (16, 32 or 64) lanes of a token, result in every lane.
 template <int LPT, typename Op>
 __device__ __forceinline__ float lanes_reduce(float x, Op op) {
@@ -540,10 +548,8 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int* 
         const float mc = lanes_max<LPT>(lc);
         float p = 0.0f;
         if (!softmax && mine) p = sigmoid32(lc);
-        // sigmoids so small that their logits' exponentials are the same to
-        // 2^-64 are normalised as those (binary32 would underflow)
-        const bool by_exp = softmax || mc < -64.0f;
-        if (__any(by_exp) && mine && by_exp) p = exp_diff(lc, mc);
+        const bool by_exp = softmax || mc < 0.0f;
+        if (__any(by_exp) && mine && by_exp) p = share(lc, mc, softmax);
         weight = p / lanes_reduce<LPT>(p, AddOp());
     } else {
         weight = !mine ? 0.0f : softmax ? exp_diff(lc, m) / total : sigmoid32(lc);
@@ -813,8 +819,8 @@ __global__ void __launch_bounds__(64) k_route_backward(const RouteBackward a) {
     float S = 0.0f, term;
     if (a.renorm) {
         const float mc = fmaxf(lanes_max<LPT>(lc), kLowest);
-        const bool by_exp = softmax || mc < -64.0f;
-        float w = !mine ? 0.0f : by_exp ? exp_diff(lc, mc) : pc;
+        const bool by_exp = softmax || mc < 0.0f;
+        float w = !mine ? 0.0f : by_exp ? share(lc, mc, softmax) : pc;
         const float sum = lanes_reduce<LPT>(w, AddOp());
         w = mine ? w / sum : 0.0f;
         const float D = lanes_reduce<LPT>(dw * w, AddOp());

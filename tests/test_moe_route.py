@@ -419,6 +419,28 @@ def test_sigmoids_below_the_normal_numbers(nv):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("top", [-60.0, -40.0, -3.0, 0.5])
+def test_small_sigmoids_divided_by_small_sums(nv, top):
+    """Chosen logits from `top` down: weights that are normal numbers though the
+    sigmoids are not, and those of them that are not.  (Steps as above: what is
+    left of a sigmoid's own where the largest is not small.)"""
+    step = 2.0 ** -149
+    g = np.random.default_rng(21)
+    l = torch.from_numpy(top - g.uniform(0, 100, (60, 12))).float().cuda()
+    l[:, 3] = top
+    dw = g.standard_normal((60, 12)).astype(np.float32)
+    r = nv.nvfp4_route(l, 12, score=nv.NVFP4_ROUTE_SIGMOID)
+    ids, w = P.route(P.host(l), 12, None, True)
+    assert np.array_equal(r.ids.cpu().numpy(), ids)
+    assert (np.abs(P.host(r.weights) - w) <= 16 * P.U * w + 5 * step).all()
+    got = nv.nvfp4_route_backward(torch.from_numpy(dw).cuda(), l, r.ids, score=nv.NVFP4_ROUTE_SIGMOID)
+    a = (dw.astype(np.float64), P.host(l), ids, True, True, None)
+    want = P.route_backward(*a)
+    factors = 2 * np.abs(dw).max(axis=1, keepdims=True)
+    assert (np.abs(P.host(got) - want) <= backward_tol(*a, want, torch.float32, 12) + (5 * factors + 4) * step).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("sigmoid", [False, True])
 def test_backward_against_differences(nv, sigmoid):
     l = make(9, 6, 48, torch.float32)
