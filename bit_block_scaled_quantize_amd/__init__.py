@@ -15,4 +15,6 @@ from .nvfp4 import (  # noqa: F401
     RMSNormOutput, nvfp4_rmsnorm, nvfp4_rmsnorm_backward, nvfp4_rmsnorm_backward_workspace_size,
     RouteOutput, nvfp4_route, nvfp4_route_workspace_size, nvfp4_route_backward,
     nvfp4_gemv, nvfp4_mx_gemv, nvfp4_expert_gemv, nvfp4_expert_gemv_workspace_size,
+    NVFP4_KV_NVFP4, NVFP4_KV_MXFP4, NVFP4KVCache, nvfp4_kv_append, nvfp4_kv_gather,
+    nvfp4_kv_attention, nvfp4_kv_attention_workspace_size,
 )

@@ -27,7 +27,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libnvfp4.so")
 BINDING = os.path.join(HERE, "_native.so")
 BUILD = os.path.join(HERE, "_build")
-SOURCES = ["quantize.hip", "gemm.hip", "mx.hip", "mx_gemm.hip", "norm.hip", "route.hip", "gemv.hip", "nvfp4_api.hip"]
+SOURCES = ["quantize.hip", "gemm.hip", "mx.hip", "mx_gemm.hip", "norm.hip", "route.hip", "gemv.hip", "kv_cache.hip", "kv_attention.hip",
+           "nvfp4_api.hip"]
 ARCH = os.environ.get("NVFP4_OFFLOAD_ARCH", "gfx950")
 
 

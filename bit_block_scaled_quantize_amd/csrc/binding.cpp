@@ -1,4 +1,4 @@
-// Python entry points of the MoE-block operators over the C ABI
+// Python entry points of the MoE-block and cache operators over the C ABI
 // (include/nvfp4.h): argument checks, output and workspace allocation with
 // torch, and the call.  nvfp4.py gives them their names, defaults and result
 // types.  These operators are called once or more for every layer and token;
@@ -413,6 +413,165 @@ PyObject* expert_gemv(PyObject*, PyObject* const* v, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// rows x heads x dim of a tensor whose last dimension is consecutive.
+nvfp4_kv_rows heads_of(const char* name, const at::Tensor& t) {
+    TORCH_CHECK_VALUE(t.dim() == 3 && (t.stride(2) == 1 || t.size(2) <= 1), name,
+                      " must be rows x heads x head_dim with unit stride in the last dimension");
+    return {t.data_ptr(), t.stride(0), t.stride(1)};
+}
+
+nvfp4_kv_rows heads_of(const char* name, const at::Tensor& t, int64_t rows, int64_t heads, int64_t dim,
+                       at::ScalarType dtype, const at::Tensor& like) {
+    const nvfp4_kv_rows r = heads_of(name, t);
+    TORCH_CHECK_VALUE(t.size(0) == rows && t.size(1) == heads && t.size(2) == dim, name, " is ", t.size(0), " x ",
+                      t.size(1), " x ", t.size(2), ", expected ", rows, " x ", heads, " x ", dim);
+    TORCH_CHECK_TYPE(t.scalar_type() == dtype, name, " has dtype ", t.scalar_type(), ", expected ", dtype);
+    same_device(name, t, like);
+    return r;
+}
+
+constexpr int kCacheArgs = 7, kPlanArgs = 3;
+
+// (k_codes, k_scales, v_codes, v_scales, k_scale, v_scale, format)
+nvfp4_kv_cache cache_of(PyObject* const* v, const at::Tensor*& codes) {
+    const at::Tensor& k = tensor(v[0], "k_codes");
+    TORCH_CHECK_VALUE(k.dim() == 4, "k_codes must be pages x kv_heads x page_size x head_dim / 2");
+    codes = &k;
+    nvfp4_kv_cache c = {};
+    c.format = small(v[6], "format");
+    c.pages = k.size(0);
+    c.kv_heads = (int32_t)std::min<int64_t>(k.size(1), INT32_MAX);
+    c.page_size = k.size(2);
+    c.head_dim = (int32_t)std::min<int64_t>(2 * k.size(3), INT32_MAX);
+    const int64_t per = c.format == NVFP4_KV_MXFP4 ? 32 : 16, slots = k.size(0) * k.size(1) * k.size(2);
+    c.k_codes = static_cast<uint8_t*>(flat("k_codes", k, slots * k.size(3), at::kByte, k));
+    c.v_codes = flat<uint8_t>(v[2], "v_codes", slots * k.size(3), at::kByte, k);
+    c.k_scales = flat<uint8_t>(v[1], "k_scales", slots * (2 * k.size(3) / per), at::kByte, k);
+    c.v_scales = flat<uint8_t>(v[3], "v_scales", slots * (2 * k.size(3) / per), at::kByte, k);
+    c.k_scale = flat<float>(v[4], "k_scale", k.size(1), at::kFloat, k);
+    c.v_scale = flat<float>(v[5], "v_scale", k.size(1), at::kFloat, k);
+    return c;
+}
+
+// (page_table, lengths, offsets or None) of a call on `rows` rows
+nvfp4_kv_plan plan_of(PyObject* const* v, int64_t rows, const at::Tensor& like) {
+    const at::Tensor& table = tensor(v[0], "page_table");
+    nvfp4_kv_plan p = {};
+    p.ld_table = matrix("page_table", table);
+    TORCH_CHECK_TYPE(table.scalar_type() == at::kInt, "page_table has dtype ", table.scalar_type(), ", expected ", at::kInt);
+    same_device("page_table", table, like);
+    p.page_table = static_cast<int32_t*>(table.data_ptr());
+    p.seqs = table.size(0);
+    p.width = table.size(1);
+    p.lengths = static_cast<int32_t*>(flat("lengths", tensor(v[1], "lengths"), p.seqs, at::kInt, like));
+    p.offsets = flat<int32_t>(v[2], "offsets", p.seqs + 1, at::kInt, like);
+    p.rows = rows;
+    TORCH_CHECK_VALUE(given(v[2]) || rows == p.seqs, "without offsets there must be one row a sequence, got ", rows,
+                      " rows of ", p.seqs);
+    return p;
+}
+
+// (k, v, cache, plan, rope or None, interleaved, q or None, out, stream) -> q_out
+PyObject* kv_append(PyObject*, PyObject* const* v, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    expect(n, 2 + kCacheArgs + kPlanArgs + 5);
+    const at::Tensor *codes, &k = tensor(v[0], "k"), &val = tensor(v[1], "v");
+    const nvfp4_kv_cache c = cache_of(v + 2, codes);
+    PyObject* const* rest = v + 2 + kCacheArgs;
+    const at::ScalarType dt = k.scalar_type();
+    const int32_t code = code_of(dt);
+    TORCH_CHECK_VALUE(k.dim() == 3, "k must be rows x kv_heads x head_dim");
+    const int64_t rows = k.size(0);
+    const nvfp4_kv_rows kr = heads_of("k", k, rows, c.kv_heads, c.head_dim, dt, *codes);
+    const nvfp4_kv_rows vr = heads_of("v", val, rows, c.kv_heads, c.head_dim, dt, *codes);
+    const nvfp4_kv_plan plan = plan_of(rest, rows, *codes);
+    rest += kPlanArgs;
+    nvfp4_kv_rope rope = {};
+    if (given(rest[0])) {
+        const at::Tensor& t = tensor(rest[0], "rope");
+        rope.ld = matrix("rope", t);
+        TORCH_CHECK_TYPE(t.scalar_type() == at::kFloat, "rope has dtype ", t.scalar_type(), ", expected ", at::kFloat);
+        same_device("rope", t, *codes);
+        TORCH_CHECK_VALUE(t.size(1) <= INT32_MAX, "rope is too wide");
+        rope.table = static_cast<float*>(t.data_ptr());
+        rope.positions = t.size(0);
+        rope.dim = (int32_t)t.size(1);
+        rope.interleaved = truth(rest[1]);
+    }
+    void* s = stream_of(*codes, rest[4]);
+    at::Tensor out;
+    nvfp4_kv_rows qr = {}, qo = {};
+    int32_t q_heads = 0;
+    if (given(rest[2])) {
+        const at::Tensor& q = tensor(rest[2], "q");
+        TORCH_CHECK_VALUE(q.dim() == 3 && q.size(1) <= INT32_MAX, "q must be rows x q_heads x head_dim");
+        q_heads = (int32_t)q.size(1);
+        qr = heads_of("q", q, rows, q_heads, c.head_dim, dt, *codes);
+        out = output(rest[3], "out", {rows, q_heads, c.head_dim}, dt, *codes);
+        qo = heads_of("out", out, rows, q_heads, c.head_dim, dt, *codes);
+    }
+    check("nvfp4_kv_append", nvfp4_kv_append(&kr, &vr, code, &c, &plan, given(rest[0]) ? &rope : nullptr,
+                                             q_heads ? &qr : nullptr, q_heads, q_heads ? &qo : nullptr, s));
+    return wrapped(out);
+    END_HANDLE_TH_ERRORS
+}
+
+// (cache, plan, rows, dtype code, k, v to fill, stream) -> (k, v)
+PyObject* kv_gather(PyObject*, PyObject* const* v, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    expect(n, kCacheArgs + kPlanArgs + 5);
+    const at::Tensor* codes;
+    const nvfp4_kv_cache c = cache_of(v, codes);
+    PyObject* const* rest = v + kCacheArgs + kPlanArgs;
+    const int64_t rows = integer(rest[0]);
+    TORCH_CHECK_VALUE(rows >= 0, "rows is negative");
+    const nvfp4_kv_plan plan = plan_of(v + kCacheArgs, rows, *codes);
+    const int32_t code = small(rest[1], "dtype");
+    const at::ScalarType dt = code == NVFP4_F32 ? at::kFloat : at::kBFloat16;
+    void* s = stream_of(*codes, rest[4]);
+    const at::Tensor out[2] = {output(rest[2], "out[0]", {rows, c.kv_heads, c.head_dim}, dt, *codes),
+                               output(rest[3], "out[1]", {rows, c.kv_heads, c.head_dim}, dt, *codes)};
+    nvfp4_kv_rows kr = heads_of("out[0]", out[0], rows, c.kv_heads, c.head_dim, dt, *codes);
+    nvfp4_kv_rows vr = heads_of("out[1]", out[1], rows, c.kv_heads, c.head_dim, dt, *codes);
+    check("nvfp4_kv_gather", nvfp4_kv_gather(&c, &plan, &kr, &vr, code, s));
+    return tuple(out);
+    END_HANDLE_TH_ERRORS
+}
+
+// (q, cache, plan, scale, window, lse, out, lse to fill, workspace, stream) -> (out, lse)
+PyObject* kv_attention(PyObject*, PyObject* const* v, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    expect(n, 1 + kCacheArgs + kPlanArgs + 7);
+    const at::Tensor *codes, &q = tensor(v[0], "q");
+    const nvfp4_kv_cache c = cache_of(v + 1, codes);
+    PyObject* const* rest = v + 1 + kCacheArgs;
+    const at::ScalarType dt = q.scalar_type();
+    const int32_t code = code_of(dt);
+    TORCH_CHECK_VALUE(q.dim() == 3 && q.size(1) <= INT32_MAX, "q must be rows x q_heads x head_dim");
+    const int64_t rows = q.size(0);
+    const int32_t heads = (int32_t)q.size(1);
+    const nvfp4_kv_rows qr = heads_of("q", q, rows, heads, c.head_dim, dt, *codes);
+    const nvfp4_kv_plan plan = plan_of(rest, rows, *codes);
+    rest += kPlanArgs;
+    const double scale = PyFloat_AsDouble(rest[0]);
+    if (scale == -1.0 && PyErr_Occurred()) throw Raised();
+    const int64_t window = integer(rest[1]);
+    void* s = stream_of(*codes, rest[6]);
+    at::Tensor out[2];
+    out[0] = output(rest[3], "out", {rows, heads, c.head_dim}, dt, *codes);
+    nvfp4_kv_rows o = heads_of("out", out[0], rows, heads, c.head_dim, dt, *codes);
+    float* lse = nullptr;
+    if (truth(rest[2])) {
+        out[1] = output(rest[4], "lse", {rows, heads}, at::kFloat, *codes);
+        lse = static_cast<float*>(flat("lse", out[1], rows * heads, at::kFloat, *codes));
+    }
+    const Workspace ws(rest[5], nvfp4_kv_attention_workspace_size(rows, heads, c.kv_heads, c.head_dim, code), *codes);
+    check("nvfp4_kv_attention",
+          nvfp4_kv_attention(&qr, code, heads, &c, &plan, (float)scale, window, &o, lse, ws.ptr, ws.bytes, s));
+    return tuple(out);
+    END_HANDLE_TH_ERRORS
+}
+
 // (NVFP4Error, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
 PyObject* setup(PyObject*, PyObject* const* v, Py_ssize_t n) {
     HANDLE_TH_ERRORS
@@ -430,7 +589,8 @@ PyObject* setup(PyObject*, PyObject* const* v, Py_ssize_t n) {
 #define NVFP4_ENTRY(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {NVFP4_ENTRY(setup),          NVFP4_ENTRY(rmsnorm), NVFP4_ENTRY(rmsnorm_backward),
                          NVFP4_ENTRY(route),          NVFP4_ENTRY(route_backward), NVFP4_ENTRY(gemv),
-                         NVFP4_ENTRY(mx_gemv),        NVFP4_ENTRY(expert_gemv),    {nullptr, nullptr, 0, nullptr}};
+                         NVFP4_ENTRY(mx_gemv),        NVFP4_ENTRY(expert_gemv), NVFP4_ENTRY(kv_append),
+                         NVFP4_ENTRY(kv_gather),      NVFP4_ENTRY(kv_attention), {nullptr, nullptr, 0, nullptr}};
 #undef NVFP4_ENTRY
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -205,4 +205,65 @@ hipError_t launch_gemv(const GemvArgs& p, bool swiglu, hipStream_t s);
 // way of ws (assignments x output columns floats).
 hipError_t launch_expert_gemv(GemvArgs p, bool swiglu, const float* weights, float* ws, hipStream_t s);
 
+// The paged 4-bit key/value cache (see nvfp4_kv_cache) and the plan of a call
+// (nvfp4_kv_plan).
+struct KvCache {
+    uint8_t* k_codes;
+    uint8_t* k_scales;
+    uint8_t* v_codes;
+    uint8_t* v_scales;
+    const float* k_scale;  // NULL: MX
+    const float* v_scale;
+    int pages, heads, dim;
+    bool mx;
+};
+struct KvPlan {
+    const int* table;
+    int64_t ld_table;
+    const int* lengths;
+    const int* offsets;  // NULL: one row a sequence
+    int width, page_shift, seqs, rows;
+};
+// Rows x heads of dim elements each, strides in elements.
+struct KvRows {
+    const void* data;
+    int64_t row, head;
+};
+constexpr int64_t kMaxKvSeqs = 65536;
+struct KvAppend {
+    KvCache cache;
+    KvPlan plan;
+    KvRows k, v, q;
+    struct { void* data; int64_t row, head; } q_out;
+    int q_heads;  // 0: no q
+    bool bf16, interleaved;
+    const float* rope;
+    int64_t rope_ld;
+    int rope_rows, rot;  // no rotation: INT32_MAX, 0
+};
+hipError_t launch_kv_append(const KvAppend& p, hipStream_t s);
+struct KvGather {
+    KvCache cache;
+    KvPlan plan;
+    KvRows k, v;
+    bool bf16;
+};
+hipError_t launch_kv_gather(const KvGather& p, hipStream_t s);
+
+// Attention over the cache (see nvfp4_kv_attention).
+struct KvAttention {
+    KvCache cache;
+    KvPlan plan;
+    KvRows q;
+    struct { void* data; int64_t row, head; } out;
+    float* lse;  // nullable, rows x q_heads
+    int q_heads, group;
+    int window;  // 0: none
+    float scale;
+    bool bf16;
+    float* ws;
+};
+size_t kv_attention_workspace_bytes(int64_t rows, int q_heads, int kv_heads, int dim, bool bf16);
+hipError_t launch_kv_attention(const KvAttention& p, hipStream_t s);
+
 }  // namespace nvfp4

@@ -621,6 +621,154 @@ nvfp4_status nvfp4_expert_gemv(const void* x, int32_t dt /* nvfp4_dtype */, int6
     return e == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
 }
 
+// ---------------------------------------------------------------- the 4-bit cache
+namespace {
+
+constexpr int64_t kMaxKvRows = (int64_t)1 << 30;
+
+nvfp4_status check_cache(const nvfp4_kv_cache* c, const nvfp4_kv_plan* p) {
+    if (!c || !p) return NVFP4_ERR_NULL;
+    if (c->format != NVFP4_KV_NVFP4 && c->format != NVFP4_KV_MXFP4) return NVFP4_ERR_ENUM;
+    if (c->pages < 0 || c->page_size < 1 || c->kv_heads < 1 || c->head_dim < 1) return NVFP4_ERR_SHAPE;
+    if (p->rows < 0 || p->seqs < 0 || p->width < 0 || p->ld_table < p->width) return NVFP4_ERR_SHAPE;
+    if (!p->offsets && p->rows != p->seqs) return NVFP4_ERR_SHAPE;
+    const bool mx = c->format == NVFP4_KV_MXFP4;
+    if (c->pages > 0 && (!c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales)) return NVFP4_ERR_NULL;
+    if (!mx && (!c->k_scale || !c->v_scale)) return NVFP4_ERR_NULL;
+    if (p->seqs > 0 && (!p->lengths || (p->width > 0 && !p->page_table))) return NVFP4_ERR_NULL;
+    if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4) ||
+        !aligned(p->page_table, 4) || !aligned(p->lengths, 4) || !aligned(p->offsets, 4))
+        return NVFP4_ERR_ALIGN;
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return NVFP4_ERR_UNSUPPORTED;
+    if (c->page_size < 16 || (c->page_size & (c->page_size - 1))) return NVFP4_ERR_UNSUPPORTED;
+    if (c->page_size > kMaxKvRows || p->width > kMaxKvRows / c->page_size || p->rows > kMaxKvRows ||
+        p->seqs > kMaxKvSeqs || c->pages > 0x7FFFFFFF)
+        return NVFP4_ERR_UNSUPPORTED;
+    return NVFP4_OK;
+}
+
+// Rows x heads of a call (written: heads that do not overlap).
+nvfp4_status check_heads(const nvfp4_kv_rows* r, int64_t rows, int64_t heads, int64_t dim, int32_t dt, bool written) {
+    if (!r) return NVFP4_ERR_NULL;
+    if (r->row_stride < 0 || r->head_stride < 0) return NVFP4_ERR_SHAPE;
+    if (rows > 0 && !r->data) return NVFP4_ERR_NULL;
+    if (written && rows > 0) {
+        const bool by_row = (heads == 1 || r->head_stride >= dim) && (rows == 1 || r->row_stride / heads >= (heads == 1 ? dim : r->head_stride));
+        const bool by_head = (rows == 1 || r->row_stride >= dim) && (heads == 1 || r->head_stride / rows >= (rows == 1 ? dim : r->row_stride));
+        if (!by_row && !by_head) return NVFP4_ERR_SHAPE;
+    }
+    return aligned(r->data, dtype_size(dt)) ? NVFP4_OK : NVFP4_ERR_ALIGN;
+}
+
+KvCache kv_cache_of(const nvfp4_kv_cache* c) {
+    const bool mx = c->format == NVFP4_KV_MXFP4;
+    return KvCache{c->k_codes, c->k_scales, c->v_codes, c->v_scales, mx ? nullptr : c->k_scale, mx ? nullptr : c->v_scale,
+                   (int)c->pages, c->kv_heads, c->head_dim, mx};
+}
+
+KvPlan kv_plan_of(const nvfp4_kv_cache* c, const nvfp4_kv_plan* p) {
+    return KvPlan{p->page_table, p->ld_table, p->lengths, p->offsets, (int)p->width, __builtin_ctzll(c->page_size),
+                  (int)p->seqs, (int)p->rows};
+}
+
+KvRows kv_rows_of(const nvfp4_kv_rows* r) { return KvRows{r->data, r->row_stride, r->head_stride}; }
+
+}  // namespace
+
+nvfp4_status nvfp4_kv_append(const nvfp4_kv_rows* k, const nvfp4_kv_rows* v, int32_t dt /* nvfp4_dtype */,
+                             const nvfp4_kv_cache* cache, const nvfp4_kv_plan* plan, const nvfp4_kv_rope* rope,
+                             const nvfp4_kv_rows* q, int32_t q_heads, nvfp4_kv_rows* q_out, void* stream) {
+    if (!valid_dtype(dt)) return NVFP4_ERR_ENUM;
+    nvfp4_status st = check_cache(cache, plan);
+    if (st != NVFP4_OK) return st;
+    const int64_t rows = plan->rows, dim = cache->head_dim;
+    if (q_heads < 0 || (q ? q_heads < 1 : q_heads > 0)) return NVFP4_ERR_SHAPE;
+    st = check_heads(k, rows, cache->kv_heads, dim, dt, false);
+    if (st == NVFP4_OK) st = check_heads(v, rows, cache->kv_heads, dim, dt, false);
+    if (st == NVFP4_OK && q) st = check_heads(q, rows, q_heads, dim, dt, false);
+    if (st == NVFP4_OK && q) st = check_heads(q_out, rows, q_heads, dim, dt, true);
+    if (st != NVFP4_OK) return st;
+    KvAppend a = {};
+    a.rope_rows = 0x7FFFFFFF;
+    if (rope) {
+        if (rope->positions < 0 || rope->dim < 1 || rope->ld < rope->dim) return NVFP4_ERR_SHAPE;
+        if (rope->positions > 0 && !rope->table) return NVFP4_ERR_NULL;
+        if (!aligned(rope->table, 4)) return NVFP4_ERR_ALIGN;
+        if (rope->dim < 32 || rope->dim > dim || (rope->dim & (rope->dim - 1))) return NVFP4_ERR_UNSUPPORTED;
+        a.rope = rope->table;
+        a.rope_ld = rope->ld;
+        a.rope_rows = (int)(rope->positions < 0x7FFFFFFF ? rope->positions : 0x7FFFFFFF);
+        a.rot = rope->dim;
+        a.interleaved = rope->interleaved != 0;
+    }
+    a.cache = kv_cache_of(cache);
+    a.plan = kv_plan_of(cache, plan);
+    a.k = kv_rows_of(k);
+    a.v = kv_rows_of(v);
+    if (q) {
+        a.q = kv_rows_of(q);
+        a.q_out = {q_out->data, q_out->row_stride, q_out->head_stride};
+        a.q_heads = q_heads;
+    }
+    a.bf16 = dt == NVFP4_BF16;
+    if (q_heads > 0x3FFFFFFF - 2 * (int64_t)cache->kv_heads) return NVFP4_ERR_UNSUPPORTED;
+    return launch_kv_append(a, static_cast<hipStream_t>(stream)) == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
+}
+
+nvfp4_status nvfp4_kv_gather(const nvfp4_kv_cache* cache, const nvfp4_kv_plan* plan, nvfp4_kv_rows* k,
+                             nvfp4_kv_rows* v, int32_t dt /* nvfp4_dtype */, void* stream) {
+    if (!valid_dtype(dt)) return NVFP4_ERR_ENUM;
+    nvfp4_status st = check_cache(cache, plan);
+    if (st == NVFP4_OK) st = check_heads(k, plan->rows, cache->kv_heads, cache->head_dim, dt, true);
+    if (st == NVFP4_OK) st = check_heads(v, plan->rows, cache->kv_heads, cache->head_dim, dt, true);
+    if (st != NVFP4_OK) return st;
+    if (cache->kv_heads > 0x1FFFFFFF) return NVFP4_ERR_UNSUPPORTED;
+    const KvGather g = {kv_cache_of(cache), kv_plan_of(cache, plan), kv_rows_of(k), kv_rows_of(v), dt == NVFP4_BF16};
+    return launch_kv_gather(g, static_cast<hipStream_t>(stream)) == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
+}
+
+size_t nvfp4_kv_attention_workspace_size(int64_t rows, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                         int32_t dt /* nvfp4_dtype */) {
+    if (rows < 0 || rows > kMaxKvRows || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads || !valid_dtype(dt)) return 0;
+    if (head_dim != 64 && head_dim != 128 && head_dim != 256) return 0;
+    if (rows > 0x7FFFFFFF / q_heads) return 0;
+    return kv_attention_workspace_bytes(rows, q_heads, kv_heads, head_dim, dt == NVFP4_BF16);
+}
+
+nvfp4_status nvfp4_kv_attention(const nvfp4_kv_rows* q, int32_t dt /* nvfp4_dtype */, int32_t q_heads,
+                                const nvfp4_kv_cache* cache, const nvfp4_kv_plan* plan, float scale, int64_t window,
+                                nvfp4_kv_rows* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+    if (!valid_dtype(dt)) return NVFP4_ERR_ENUM;
+    nvfp4_status st = check_cache(cache, plan);
+    if (st != NVFP4_OK) return st;
+    if (q_heads < 1 || q_heads % cache->kv_heads || window < 0) return NVFP4_ERR_SHAPE;
+    const int64_t rows = plan->rows, dim = cache->head_dim;
+    st = check_heads(q, rows, q_heads, dim, dt, false);
+    if (st == NVFP4_OK) st = check_heads(out, rows, q_heads, dim, dt, true);
+    if (st != NVFP4_OK) return st;
+    if (!aligned(lse, 4)) return NVFP4_ERR_ALIGN;
+    if (rows > 0x7FFFFFFF / q_heads) return NVFP4_ERR_UNSUPPORTED;
+    const size_t need = nvfp4_kv_attention_workspace_size(rows, q_heads, cache->kv_heads, cache->head_dim, dt);
+    if (need) {
+        if (!ws || ws_bytes < need) return NVFP4_ERR_WORKSPACE;
+        if (!aligned(ws, 16)) return NVFP4_ERR_ALIGN;
+    }
+    KvAttention a = {};
+    a.cache = kv_cache_of(cache);
+    a.plan = kv_plan_of(cache, plan);
+    a.q = kv_rows_of(q);
+    a.out = {out->data, out->row_stride, out->head_stride};
+    a.lse = lse;
+    a.q_heads = q_heads;
+    a.group = q_heads / cache->kv_heads;
+    // (a window as long as the longest sequence hides nothing)
+    a.window = window < plan->width * cache->page_size ? (int)window : 0;
+    a.scale = scale;
+    a.bf16 = dt == NVFP4_BF16;
+    a.ws = static_cast<float*>(ws);
+    return launch_kv_attention(a, static_cast<hipStream_t>(stream)) == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
+}
+
 const char* nvfp4_status_string(int32_t s /* nvfp4_status */) {
     switch (s) {
         case NVFP4_OK: return "ok";

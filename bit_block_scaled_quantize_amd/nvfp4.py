@@ -1,5 +1,6 @@
 """Thin binding of libnvfp4.so (include/nvfp4.h): ctypes, and for the operators
-of a mixture-of-experts block the compiled module _native.
+of a mixture-of-experts block and of the 4-bit key/value cache the compiled
+module _native.
 
 Argument marshalling only: every step of quantize / dequantize / GEMM runs in
 the HIP kernels behind the C ABI.  PyTorch supplies device memory (output
@@ -30,6 +31,7 @@ NVFP4_MX_E4M3, NVFP4_MX_E2M1 = 0, 1
 NVFP4_MX_ACC_NATIVE, NVFP4_MX_ACC_EXACT = 0, 1
 NVFP4_ROUTE_SOFTMAX, NVFP4_ROUTE_SIGMOID = 0, 1
 NVFP4_GROUP_MAX, NVFP4_GROUP_TOP2 = 0, 1
+NVFP4_KV_NVFP4, NVFP4_KV_MXFP4 = 0, 1
 
 EXPORTED = ["nvfp4_quantize_workspace_size", "nvfp4_quantize", "nvfp4_quantize_noalloc", "nvfp4_requantize",
             "nvfp4_dequantize",
@@ -38,6 +40,7 @@ EXPORTED = ["nvfp4_quantize_workspace_size", "nvfp4_quantize", "nvfp4_quantize_n
             "nvfp4_rmsnorm", "nvfp4_rmsnorm_backward", "nvfp4_rmsnorm_backward_workspace_size",
             "nvfp4_route", "nvfp4_route_workspace_size", "nvfp4_route_backward",
             "nvfp4_gemv", "nvfp4_mx_gemv", "nvfp4_expert_gemv", "nvfp4_expert_gemv_workspace_size",
+            "nvfp4_kv_append", "nvfp4_kv_gather", "nvfp4_kv_attention", "nvfp4_kv_attention_workspace_size",
             "nvfp4_status_string", "nvfp4_version"]
 
 
@@ -62,6 +65,28 @@ class CRouteOpts(ctypes.Structure):
     _fields_ = [("top_k", ctypes.c_int32), ("score", ctypes.c_int32), ("groups", ctypes.c_int32),
                 ("top_groups", ctypes.c_int32), ("group_score", ctypes.c_int32), ("renorm", ctypes.c_int32),
                 ("bias", ctypes.c_void_p)]
+
+
+class CKVCache(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("pages", ctypes.c_int64), ("page_size", ctypes.c_int64), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("format", ctypes.c_int32)]
+
+
+class CKVPlan(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("ld_table", ctypes.c_int64), ("width", ctypes.c_int64),
+                ("lengths", ctypes.c_void_p), ("offsets", ctypes.c_void_p), ("seqs", ctypes.c_int64),
+                ("rows", ctypes.c_int64)]
+
+
+class CKVRows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class CKVRope(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("positions", ctypes.c_int64), ("ld", ctypes.c_int64),
+                ("dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
 
 
 def _load():
@@ -121,6 +146,15 @@ def _load():
     L.nvfp4_expert_gemv.argtypes = [vp, i32, i64, i64, vp, i64, i32, ctypes.POINTER(CTensor), i32, vp, vp, i32, i64, i32,
                                     vp, sz, vp]
     L.nvfp4_expert_gemv.restype = i32
+    kv = [ctypes.POINTER(t) for t in (CKVRows, CKVCache, CKVPlan, CKVRope)]
+    L.nvfp4_kv_append.argtypes = [kv[0], kv[0], i32, kv[1], kv[2], kv[3], kv[0], i32, kv[0], vp]
+    L.nvfp4_kv_append.restype = i32
+    L.nvfp4_kv_gather.argtypes = [kv[1], kv[2], kv[0], kv[0], i32, vp]
+    L.nvfp4_kv_gather.restype = i32
+    L.nvfp4_kv_attention_workspace_size.argtypes = [i64, i32, i32, i32, i32]
+    L.nvfp4_kv_attention_workspace_size.restype = sz
+    L.nvfp4_kv_attention.argtypes = [kv[0], i32, i32, kv[1], kv[2], ctypes.c_float, i64, kv[0], vp, vp, sz, vp]
+    L.nvfp4_kv_attention.restype = i32
     L.nvfp4_status_string.argtypes = [i32]
     L.nvfp4_status_string.restype = ctypes.c_char_p
     L.nvfp4_version.argtypes = []
@@ -606,3 +640,82 @@ def nvfp4_expert_gemv(x, ids, w, experts, weights=None, epilogue=NVFP4_EPI_NONE,
     [tokens, top_k]): each token's weighted sum of its products."""
     return _native.expert_gemv(x, ids, w.codes, w.scales, w.tensor_scale, w.rows, w.cols, w.scale_mode, experts, weights,
                                epilogue, _code(out_dtype), out, workspace, _handle(stream))
+
+
+# ---------------------------------------------------------------- the 4-bit key/value cache
+@dataclass
+class NVFP4KVCache:
+    """Pages of keys and values: codes uint8 [pages, kv_heads, page_size,
+    head_dim/2] and scales uint8 [pages, kv_heads, page_size, head_dim/16]
+    (NVFP4; with k_scale and v_scale, float32 [kv_heads], as the heads' tensor
+    scales) or [..., head_dim/32] (MXFP4) -- contiguous device tensors."""
+    k_codes: torch.Tensor
+    k_scales: torch.Tensor
+    v_codes: torch.Tensor
+    v_scales: torch.Tensor
+    k_scale: torch.Tensor = None
+    v_scale: torch.Tensor = None
+    format: int = NVFP4_KV_NVFP4
+
+    def args(self):
+        return (self.k_codes, self.k_scales, self.v_codes, self.v_scales, self.k_scale, self.v_scale, self.format)
+
+    @staticmethod
+    def empty(pages, kv_heads, head_dim, page_size=64, format=NVFP4_KV_NVFP4, k_scale=1.0, v_scale=1.0, device="cuda"):
+        """A cache with nothing in it.  k_scale and v_scale (NVFP4): what every
+        head's values are divided by before their blocks' E4M3 scales (largest
+        2688 times that) are found; the largest magnitude expected / 2688, or 1
+        for values of ordinary size (block maxima from 2^-9 * 6 to 2688)."""
+        per = 32 if format == NVFP4_KV_MXFP4 else 16
+        new = [torch.empty((pages, kv_heads, page_size, w), dtype=torch.uint8, device=device)
+               for w in (head_dim // 2, head_dim // per) * 2]
+        s = [None] * 2 if per == 32 else [torch.full((kv_heads,), float(x), device=device) for x in (k_scale, v_scale)]
+        return NVFP4KVCache(*new, *s, format)
+
+
+@_launches_on_stream
+def nvfp4_kv_append(k, v, cache, page_table, lengths, offsets=None, q=None, rope=None, interleaved=False, out=None,
+                    stream=None):
+    """Append k and v (rows x kv_heads x head_dim, float32 or bfloat16, unit
+    stride in the last dimension) to an NVFP4KVCache, k rotated by its
+    position, and return q (rows x q_heads x head_dim, optional) rotated alike
+    (into `out`, which may be q).  page_table int32 [seqs, width]; lengths
+    int32 [seqs]: the sequences' positions with the new ones; offsets int32
+    [seqs + 1]: rows offsets[s] .. offsets[s+1]-1 are the last ones of sequence s
+    (None: one row a sequence).  rope float32 [positions, dim]: each position's
+    dim / 2 cosines, then sines; the first dim elements of a head are rotated
+    in halves, or interleaved in pairs."""
+    return _native.kv_append(k, v, *cache.args(), page_table, lengths, offsets, rope, interleaved, q, out,
+                             _handle(stream))
+
+
+@_launches_on_stream
+def nvfp4_kv_gather(cache, page_table, lengths, offsets=None, rows=None, dtype=torch.bfloat16, out=None, stream=None):
+    """(k, v), each rows x kv_heads x head_dim, of the cache's positions that
+    the plan names (as nvfp4_kv_append); rows: their number (one a sequence
+    unless given).  out: a pair of tensors to fill."""
+    if out is not None:
+        dtype = out[0].dtype
+    return _native.kv_gather(*cache.args(), page_table, lengths, offsets, page_table.shape[0] if rows is None else rows,
+                             _dtype_code(dtype), *((None, None) if out is None else out), _handle(stream))
+
+
+def nvfp4_kv_attention_workspace_size(rows, q_heads, kv_heads, head_dim, dtype=torch.bfloat16):
+    """Bytes of workspace of nvfp4_kv_attention."""
+    return int(lib.nvfp4_kv_attention_workspace_size(rows, q_heads, kv_heads, head_dim, _dtype_code(dtype)))
+
+
+@_launches_on_stream
+def nvfp4_kv_attention(q, cache, page_table, lengths, offsets=None, scale=None, window=0, lse=False, out=None,
+                       out_lse=None, workspace=None, stream=None):
+    """Attention of q (rows x q_heads x head_dim, float32 or bfloat16) over the
+    cache: a row at position p of its sequence (plan as for nvfp4_kv_append,
+    after the append) sees the positions up to p, with window > 0 the last
+    `window` of them.  scale: head_dim ** -0.5 unless given.  Returns a tensor
+    like q, with lse=True also the float32 logarithms of the softmax's sums
+    [rows, q_heads].  out, out_lse and workspace
+    (nvfp4_kv_attention_workspace_size) may be preallocated."""
+    o, l = _native.kv_attention(q, *cache.args(), page_table, lengths, offsets,
+                                q.shape[-1] ** -0.5 if scale is None else scale, window, lse, out, out_lse, workspace,
+                                _handle(stream))
+    return (o, l) if lse else o

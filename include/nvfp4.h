@@ -519,6 +519,130 @@ nvfp4_status nvfp4_expert_gemv(const void* x, int32_t dt /* nvfp4_dtype */, int6
                                int32_t experts, const float* weights, void* y, int32_t y_dt /* nvfp4_dtype */,
                                int64_t ldy, int32_t ep /* nvfp4_epilogue */, void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * A paged key/value cache held in 4 bits, and the attention that reads it.
+ *
+ * The cache has `pages` pages of page_size slots; a slot holds one position's
+ * key and value of every kv head.  For each of k and v:
+ *   codes   pages x kv_heads x page_size x head_dim/2 bytes: E2M1 elements, the
+ *           even one in bits 3:0;
+ *   scales  NVFP4: pages x kv_heads x page_size x head_dim/16 E4M3 bytes, times
+ *           the head's float of k_scale (v_scale), kv_heads floats, as a
+ *           tensor scale: positive and fixed while the cache is in use;
+ *           MXFP4: pages x kv_heads x page_size x head_dim/32 E8M0 bytes;
+ *           k_scale and v_scale are NULL.
+ * What a slot holds before it is appended to is never read as a number.
+ *
+ * The plan of a call says which rows it deals with.  Sequence s has the pages
+ * page_table[s * ld_table + i], i < width, of which the i-th holds its positions
+ * i * page_size and on, and lengths[s] positions in all, those of an append
+ * among them.  Its rows are offsets[s] .. offsets[s+1]-1 (offsets NULL: row s
+ * alone); the i-th of n rows has the position lengths[s] - n + i.
+ *   - a page index outside [0, pages) names no page: nothing is stored there and
+ *     nothing there is seen;
+ *   - a length counts as one between 0 and width * page_size;
+ *   - rows before offsets[0] and from offsets[seqs] on belong to no sequence:
+ *     they are neither read nor written.  Offsets out of order give unspecified
+ *     results but no access out of bounds (they are clamped to [0, rows]).
+ * Requirements (all calls): head_dim 64, 128 or 256, page_size a power of two
+ * of 16 and more (else UNSUPPORTED); width * page_size <= 2^30, seqs <= 65536,
+ * rows <= 2^30, pages < 2^31 (else UNSUPPORTED); codes 16-byte aligned.  Rows
+ * of heads need only their element's alignment.  rows == 0 is a no-op.
+ * ---------------------------------------------------------------------- */
+typedef enum { NVFP4_KV_NVFP4 = 0, NVFP4_KV_MXFP4 = 1 } nvfp4_kv_format;
+
+typedef struct {
+    uint8_t* k_codes;
+    uint8_t* k_scales;
+    uint8_t* v_codes;
+    uint8_t* v_scales;
+    const float* k_scale; /* NVFP4: DEVICE, kv_heads floats */
+    const float* v_scale;
+    int64_t pages;
+    int64_t page_size;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t format; /* nvfp4_kv_format */
+} nvfp4_kv_cache;
+
+typedef struct {
+    const int32_t* page_table; /* DEVICE, seqs rows of width, row stride ld_table */
+    int64_t ld_table;
+    int64_t width;
+    const int32_t* lengths;    /* DEVICE, seqs */
+    const int32_t* offsets;    /* nullable DEVICE, seqs + 1 (NULL: rows == seqs) */
+    int64_t seqs;
+    int64_t rows;
+} nvfp4_kv_plan;
+
+/* rows x heads of head_dim consecutive elements each; strides in elements, not
+ * negative.  Where it is written, heads must not overlap: head_stride >=
+ * head_dim and row_stride >= heads * head_stride, or the other way round. */
+typedef struct {
+    void* data;
+    int64_t row_stride;
+    int64_t head_stride;
+} nvfp4_kv_rows;
+
+/* The rotation of positions: row p of the table (stride ld >= dim) holds the
+ * cosines, then the sines of position p's dim / 2 angles.  The first dim
+ * elements of a head are rotated, element i with element i + dim / 2, or
+ * (interleaved) element 2i with 2i + 1, by angle i:
+ *   (a, b) -> (a cos - b sin, b cos + a sin), each product and sum rounded to
+ *   binary32.
+ * dim: a power of two from 32 to head_dim (else UNSUPPORTED). */
+typedef struct {
+    const float* table; /* DEVICE */
+    int64_t positions;
+    int64_t ld;
+    int32_t dim;
+    int32_t interleaved;
+} nvfp4_kv_rope;
+
+/* Append the plan's rows of k and v (rows x kv_heads x head_dim, dtype dt) to
+ * the cache at their positions: k rotated (rope NULL: as it is), both then
+ * quantized to nearest even from binary32, by the rules of nvfp4_quantize with
+ * the head's float as s_t, or of nvfp4_mx_quantize.  q (nullable, rows x q_heads
+ * x head_dim) is rotated alike into q_out (rounded once to dt), which may be q
+ * itself.  A row whose position is negative or past the table of angles is not
+ * stored, and its row of q_out is zero.  Within one call no slot may have two
+ * rows (a page that is written to belongs to one sequence): such a slot's
+ * contents are unspecified. */
+nvfp4_status nvfp4_kv_append(const nvfp4_kv_rows* k, const nvfp4_kv_rows* v, int32_t dt /* nvfp4_dtype */,
+                             const nvfp4_kv_cache* cache, const nvfp4_kv_plan* plan, const nvfp4_kv_rope* rope,
+                             const nvfp4_kv_rows* q, int32_t q_heads, nvfp4_kv_rows* q_out, void* stream);
+
+/* Read the plan's rows back: k and v (rows x kv_heads x head_dim, dtype dt), as
+ * nvfp4_dequantize and nvfp4_mx_dequantize round; a row without a page is
+ * zero. */
+nvfp4_status nvfp4_kv_gather(const nvfp4_kv_cache* cache, const nvfp4_kv_plan* plan, nvfp4_kv_rows* k,
+                             nvfp4_kv_rows* v, int32_t dt /* nvfp4_dtype */, void* stream);
+
+/* Bytes of workspace nvfp4_kv_attention needs (0 for invalid sizes). */
+size_t nvfp4_kv_attention_workspace_size(int64_t rows, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                         int32_t dt /* nvfp4_dtype */);
+
+/* Attention of the plan's rows of q (rows x q_heads x head_dim, dtype dt) over
+ * their sequences' slots:
+ *   out[t][h] = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale * <q[t][h], k_j>),
+ * over the positions j <= the row's own, and with window > 0 only the last
+ * `window` of them; kv head h / (q_heads / kv_heads).  Rounded once to dt (out:
+ * may be q itself); lse (nullable, rows x q_heads floats) receives
+ * log(sum_j w_j).  A row that sees no position has zeros and an lse of -inf.
+ * Products are exact (of binary32 q: of its two FP16 parts for NVFP4, 22
+ * bits, or three BF16 parts for MXFP4), sums and the softmax's statistics
+ * binary32; the weights w_j go into the second product rounded to FP16 for
+ * BF16 q over NVFP4 (2^-12), as two BF16 parts over MXFP4 (2^-17), and as two
+ * FP16 or three BF16 parts for binary32 q.  Scores must stay in binary32's range.  A
+ * row of q that is not finite gives unspecified results, the other rows theirs.
+ * ws 16-byte aligned, ws_bytes >= nvfp4_kv_attention_workspace_size(...); it is
+ * scratch for this call only: calls that overlap must not share it.
+ * q_heads % kv_heads == 0; rows * q_heads < 2^31 (else UNSUPPORTED).  Results
+ * repeat bit for bit. */
+nvfp4_status nvfp4_kv_attention(const nvfp4_kv_rows* q, int32_t dt /* nvfp4_dtype */, int32_t q_heads,
+                                const nvfp4_kv_cache* cache, const nvfp4_kv_plan* plan, float scale, int64_t window,
+                                nvfp4_kv_rows* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* nvfp4_status_string(int32_t s /* nvfp4_status */);
 
