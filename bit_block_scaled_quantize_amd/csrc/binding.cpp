@@ -565,7 +565,7 @@ PyObject* kv_attention(PyObject*, PyObject* const* v, Py_ssize_t n) {
         out[1] = output(rest[4], "lse", {rows, heads}, at::kFloat, *codes);
         lse = static_cast<float*>(flat("lse", out[1], rows * heads, at::kFloat, *codes));
     }
-    const Workspace ws(rest[5], nvfp4_kv_attention_workspace_size(rows, heads, c.kv_heads, c.head_dim, code), *codes);
+    const Workspace ws(rest[5], nvfp4_kv_attention_workspace_size(rows, plan.seqs, heads, c.kv_heads, c.head_dim, code), *codes);
     check("nvfp4_kv_attention",
           nvfp4_kv_attention(&qr, code, heads, &c, &plan, (float)scale, window, &o, lse, ws.ptr, ws.bytes, s));
     return tuple(out);

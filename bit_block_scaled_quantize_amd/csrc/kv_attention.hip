@@ -51,9 +51,13 @@ constexpr int kCols = 16;     // columns (rows of q x heads of a group) of a seg
 constexpr int kTile = 64;     // keys of a unit of work
 constexpr int kShares = 512;  // workgroups: two on each of 256 compute units
 constexpr float kLowest = -3.402823466e38f;
-// weights are taken times 2^kBias, near FP16's largest: half a step of its
-// subnormal numbers is then 2^-40 of the largest weight
-constexpr float kBias = 15.0f;
+// Weights are taken over a maximum that may lie up to kSlack (in powers of two)
+// below the true one, so that the sums are rescaled seldom, and times 2^kBias,
+// so that they reach FP16's largest: half a step of its subnormal numbers is
+// then 2^-36 of the largest weight.
+constexpr float kBias = 11.0f, kSlack = 4.0f;
+// Sequences of more columns than this for a kv head are k_kv_prefill's (BF16 q).
+constexpr int kFewColumns = 64;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // One format's operand type: FP16 for NVFP4, BF16 (whose exponents hold every
@@ -144,7 +148,8 @@ __device__ __forceinline__ Seq seq_of(const KvAttention& p, int s) {
     Seq q;
     kv_rows(p.plan, s, q.row, q.rows);
     q.length = kv_length(p.plan, s);
-    q.columns = (int)(((int64_t)q.rows * p.group + kCols - 1) / kCols);
+    const int64_t cols = (int64_t)q.rows * p.group;
+    q.columns = p.bf16 && cols > kFewColumns ? 0 : (int)((cols + kCols - 1) / kCols);
     const int64_t low = p.window ? (int64_t)q.length - q.rows - p.window + 1 : 0;
     q.first_tile = low > 0 ? (int)(low / kTile) : 0;
     q.tiles = max(1, (q.length + kTile - 1) / kTile - q.first_tile);
@@ -431,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv_attention(const KvAttention 
                     half_pair(fmaxf(a, b), a, b);
                     top = fmaxf(a, b);
                 }
-                if (__any(top > m)) {
+                if (__any(top > m + kSlack)) {
                     const float next = fmaxf(m, top), f = __builtin_amdgcn_exp2f(m - next);
                     m = next;
                     l *= f;
@@ -562,6 +567,408 @@ __global__ void __launch_bounds__(kThreads) k_kv_join(const KvAttention p) {
     }
 }
 
+// ---------------------------------------------------------------- many rows
+// k_kv_prefill: a workgroup has 32 columns to a wave and goes over 64 keys at a
+// time, converted once for all of them into LDS (two buffers; codes are loaded
+// two tiles ahead, their pages three).  S^T = K Q^T and O^T = V^T P^T by
+// 32x32x16 MFMA; as in k_kv_attention the first product's sums are the second's
+// operand as they lie.
+template <int D>
+constexpr int kPreWaves = D == 256 ? 4 : 8;
+template <int D>
+constexpr int kPreCols = 32 * kPreWaves<D>;
+// K rows: 16 bytes after each put 16 rows' pieces of a 16-byte read in
+// different banks; V rows: 64 bytes put 4 rows' 64-byte pieces there.
+template <int D>
+constexpr int kPreK = 2 * D + 16;
+template <int D>
+constexpr int kPreV = 2 * D + 64;
+template <int D>
+constexpr int kPreBytes = kTile * (kPreK<D> + kPreV<D>) + 16;
+
+typedef float v16f_t __attribute__((ext_vector_type(16)));
+
+__device__ __forceinline__ v16f_t mfma32(v8h_t a, v8h_t b, v16f_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ v16f_t mfma32(v8b_t a, v8b_t b, v16f_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+// Blocks of kPreCols columns of sequence s for a kv head.
+template <int D>
+__device__ __forceinline__ int pre_blocks(const KvAttention& p, int s) {
+    int row, rows;
+    kv_rows(p.plan, s, row, rows);
+    const int64_t cols = (int64_t)rows * p.group;
+    return cols > kFewColumns ? (int)((cols + kPreCols<D> - 1) / kPreCols<D>) : 0;
+}
+
+// Block `index` of all, the last ones first (they see the most keys): its
+// sequence and number there; false past the end.
+template <int D>
+__device__ __forceinline__ bool pre_find(const KvAttention& p, int64_t index, int& s, int& block) {
+    const int lane = threadIdx.x & 63;
+    int64_t all = 0;
+    for (int b = 0; b < p.plan.seqs; b += 64) all += shfl64(scan64(b + lane < p.plan.seqs ? pre_blocks<D>(p, b + lane) : 0), 63);
+    if (index >= all) return false;
+    index = all - 1 - index;
+    for (int b = 0;; b += 64) {
+        const int64_t own = b + lane < p.plan.seqs ? pre_blocks<D>(p, b + lane) : 0;
+        const int64_t upto = scan64(own), sum = shfl64(upto, 63);
+        if (index < sum) {
+            const int l = __builtin_ctzll(__ballot(index < upto));
+            s = __builtin_amdgcn_readfirstlane(b + l);
+            block = __builtin_amdgcn_readfirstlane((int)(index - shfl64(upto - own, l)));
+            return true;
+        }
+        index -= sum;
+    }
+}
+
+// What workgroup `id` of k_kv_prefill does: columns of a kv head (neighbouring
+// workgroups have different heads, so that with 8 of them one head's keys stay
+// in one XCD's L2) and the split-th part of its tiles.
+struct PreWork {
+    Seq q;
+    Segment g;  // (begin, end: tiles of keys)
+    int s, split;
+    int64_t slot;  // of the workspace
+};
+
+template <int D>
+__device__ __forceinline__ bool pre_work(const KvAttention& p, int64_t id, PreWork& w) {
+    w.slot = id;
+    w.g.head = (int)(id % p.cache.heads);
+    id /= p.cache.heads;
+    w.split = (int)(id % p.splits);
+    int block;
+    if (!pre_find<D>(p, id / p.splits, w.s, block)) return false;
+    kv_rows(p.plan, w.s, w.q.row, w.q.rows);
+    w.q.length = kv_length(p.plan, w.s);
+    w.g.first = block * kPreCols<D>;
+    w.g.count = (int)min((int64_t)kPreCols<D>, (int64_t)w.q.rows * p.group - w.g.first);
+    const int pos0 = w.q.length - w.q.rows;
+    const int first = pos0 + w.g.first / p.group, last = pos0 + (w.g.first + w.g.count - 1) / p.group;
+    const int low = p.window ? max(0, first - p.window + 1) / kTile : 0;
+    const int tiles = last >= 0 ? last / kTile + 1 - low : 0;
+    const int each = (tiles + p.splits - 1) / p.splits;
+    w.g.begin = low + min(tiles, w.split * each);
+    w.g.end = low + min(tiles, (w.split + 1) * each);
+    return true;
+}
+
+// A slot: [columns][D] of O, then the columns' maxima and sums.
+template <int D>
+constexpr int64_t kPreSlotFloats = (int64_t)kPreCols<D> * (D + 2);
+
+template <bool MX, int D>
+__global__ void __launch_bounds__(64 * kPreWaves<D>, kPreWaves<D> / 4) k_kv_prefill(const KvAttention p) {
+    typedef Form<MX> F;
+    typedef typename F::v8 v8;
+    constexpr int W = kPreWaves<D>, PP = kPParts<MX, false>, EPT = D / W, KS = D / 16, DB = D / 32;
+    constexpr int per = MX ? 32 : 16;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int col = lane & 31, h = lane >> 5;
+    PreWork work;
+    if (!pre_work<D>(p, blockIdx.x, work)) return;
+    const Seq& q = work.q;
+    const Segment& g = work.g;
+    const int pos0 = q.length - q.rows;
+    // the lane's column, and the positions of its wave's
+    const int wfirst = g.first + 32 * wave, wlast = min(wfirst + 31, g.first + g.count - 1);
+    const bool idle = wfirst > wlast;
+    const int c = min(wfirst + col, g.first + g.count - 1);
+    const int qrow = c / p.group, qhead = g.head * p.group + c % p.group;
+    const int pos = pos0 + qrow, low = p.window ? max(0, pos - p.window + 1) : 0;
+    const int wpos_first = pos0 + wfirst / p.group, wpos_last = idle ? -1 : pos0 + wlast / p.group;
+    const int wlow_first = p.window ? max(0, wpos_first - p.window + 1) : 0;
+    const int wlow_last = p.window ? max(0, wpos_last - p.window + 1) : 0;
+
+    v8 qf[KS];
+    float factor = fabsf(p.scale) * kLog2e;
+    if constexpr (!MX) factor *= p.cache.k_scale[g.head];
+    {
+        float v[KS][8];
+        const uint16_t* src = static_cast<const uint16_t*>(p.q.data) + (q.row + qrow) * p.q.row + qhead * p.q.head + 8 * h;
+#pragma unroll
+        for (int i = 0; i < KS; ++i) load_upto8(src + 16 * i, 8, v[i]);
+        int e = 15;
+        if constexpr (!MX) {
+            float top = 0.0f, a, b;
+#pragma unroll
+            for (int i = 0; i < KS; ++i)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(v[i][k]));
+            half_pair(top, a, b);
+            e = __builtin_amdgcn_frexp_expf(fmaxf(a, b));
+            factor = ldexpf(factor, e - 15);
+        }
+        // (the scale's sign goes with q, so that larger sums are larger scores)
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if constexpr (!MX) v[i][k] = ldexpf(v[i][k], 15 - e);
+                if (p.scale < 0.0f) v[i][k] = -v[i][k];
+            }
+            split8<MX, 1>(v[i], &qf[i]);
+        }
+        factor = fmaxf(factor, 1e-37f);  // (0 times a hidden score's -inf is no number)
+    }
+
+    // what a thread loads of a tile: EPT elements of a key
+    const int lkey = threadIdx.x / W, part = threadIdx.x % W;
+    struct Raw {
+        uint32_t w[EPT / 8], s;
+    } rk, rv;
+    int page_next;
+    const int slot_mask = (1 << p.plan.page_shift) - 1;
+    const int j0 = (int)g.begin, j1 = (int)g.end;
+    const auto find_page = [&](int j) {
+        const int key = j * kTile + lkey;
+        return j < j1 && key < q.length ? kv_page(p.plan, p.cache.pages, work.s, key) : -1;
+    };
+    bool hole;  // of the codes loaded
+    const auto load = [&](int j, int page) {
+        const int key = j * kTile + lkey;
+        hole = j < j1 && key < q.length && page < 0;
+#pragma unroll
+        for (int i = 0; i < EPT / 8; ++i) rk.w[i] = rv.w[i] = 0;
+        rk.s = rv.s = 0;
+        if (page < 0) return;
+        const int64_t slot = (((int64_t)page * p.cache.heads + g.head) << p.plan.page_shift) + (key & slot_mask);
+        const uint8_t* kc = p.cache.k_codes + slot * (D / 2) + part * (EPT / 2);
+        const uint8_t* vc = p.cache.v_codes + slot * (D / 2) + part * (EPT / 2);
+        if constexpr (EPT == 8) {
+            rk.w[0] = *reinterpret_cast<const uint32_t*>(kc);
+            rv.w[0] = *reinterpret_cast<const uint32_t*>(vc);
+        } else if constexpr (EPT == 16) {
+            const uint2 a = *reinterpret_cast<const uint2*>(kc), b = *reinterpret_cast<const uint2*>(vc);
+            rk.w[0] = a.x, rk.w[1] = a.y;
+            rv.w[0] = b.x, rv.w[1] = b.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < EPT / 32; ++i) {
+                const u4_t a = *reinterpret_cast<const u4_t*>(kc + 16 * i), b = *reinterpret_cast<const u4_t*>(vc + 16 * i);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    rk.w[4 * i + k] = a[k];
+                    rv.w[4 * i + k] = b[k];
+                }
+            }
+        }
+        const int64_t at = slot * (D / per) + part * EPT / per;
+        constexpr int n = EPT / per;
+        if constexpr (n <= 1) {
+            rk.s = p.cache.k_scales[at];
+            rv.s = p.cache.v_scales[at];
+        } else if constexpr (n == 2) {
+            rk.s = *reinterpret_cast<const h_align1*>(p.cache.k_scales + at);
+            rv.s = *reinterpret_cast<const h_align1*>(p.cache.v_scales + at);
+        } else {
+            rk.s = *reinterpret_cast<const w_align1*>(p.cache.k_scales + at);
+            rv.s = *reinterpret_cast<const w_align1*>(p.cache.v_scales + at);
+        }
+    };
+    // converts what is loaded into buffer b; word i of its last 16 bytes: whether
+    // its keys 16 i and on have no page
+    const auto stage = [&](int b) {
+        char* k = kv_lds + b * kPreBytes<D>;
+        char* v = k + kTile * kPreK<D>;
+#pragma unroll
+        for (int i = 0; i < EPT / 8; ++i) {
+            *reinterpret_cast<v8*>(k + lkey * kPreK<D> + part * (2 * EPT) + 16 * i) =
+                F::values(rk.w[i], (rk.s >> (8 * (8 * i / per))) & 0xFFu);
+            *reinterpret_cast<v8*>(v + lkey * kPreV<D> + part * (2 * EPT) + 16 * i) =
+                F::values(rv.w[i], (rv.s >> (8 * (8 * i / per))) & 0xFFu);
+        }
+        if (part == 0 && (lkey & 15) == 0) *reinterpret_cast<int*>(v + kTile * kPreV<D> + lkey / 4) = hole;
+    };
+
+    float m = kLowest, l = 0.0f;
+    v16f_t o[DB];
+#pragma unroll
+    for (int i = 0; i < DB; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[i][r] = 0.0f;
+
+    if (j0 < j1) {
+        load(j0, find_page(j0));
+        page_next = find_page(j0 + 1);
+        stage(0);
+        load(j0 + 1, page_next);
+        page_next = find_page(j0 + 2);
+    }
+    for (int j = j0; j < j1; ++j) {
+        lds_barrier();
+        const int b = (j - j0) & 1;
+        if (j + 1 < j1) {
+            stage(b ^ 1);
+            load(j + 2, page_next);
+            page_next = find_page(j + 3);
+        }
+        const int key0 = j * kTile;
+        if (key0 > wpos_last || key0 + kTile <= wlow_first) continue;
+        const char* kt = kv_lds + b * kPreBytes<D>;
+        const char* vt = kt + kTile * kPreK<D>;
+        v16f_t sc[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) sc[t][r] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < KS; ++i)
+                sc[t] = mfma32(*reinterpret_cast<const v8*>(kt + (32 * t + col) * kPreK<D> + 32 * i + 16 * h), qf[i], sc[t]);
+        }
+        const u4_t holes = *reinterpret_cast<const u4_t*>(vt + kTile * kPreV<D>);
+        const bool none = (holes[0] | holes[1] | holes[2] | holes[3]) != 0;
+        if (none || key0 + kTile - 1 > wpos_first || key0 < wlow_last) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int key = key0 + 32 * t + 8 * (r >> 2) + 4 * h + (r & 3);
+                    const bool seen = key <= pos && key >= low && !holes[2 * t + (r >> 3)];
+                    sc[t][r] = seen ? sc[t][r] : -INFINITY;
+                }
+        }
+        float top = -INFINITY, a0, a1;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) top = fmaxf(top, sc[t][r]);
+        half_pair(top, a0, a1);
+        top = fmaxf(a0, a1) * factor;
+        if (__any(top > m + kSlack)) {
+            const float next = fmaxf(m, top), f = __builtin_amdgcn_exp2f(m - next);
+            m = next;
+            l *= f;
+#pragma unroll
+            for (int i = 0; i < DB; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) o[i][r] *= f;
+        }
+        const float base = m - kBias;
+        v8 pf[4][PP];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            float w[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                w[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[u >> 1][8 * (u & 1) + r], factor, -base));
+                l += w[r];
+            }
+            split8<MX, PP>(w, pf[u]);
+        }
+#pragma unroll
+        for (int i = 0; i < DB; ++i)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                typedef __attribute__((address_space(3))) v4s_t lds_v4s;
+                typedef short v8s_t __attribute__((ext_vector_type(8)));
+                const char* at = vt + (16 * u + 4 * h + ((lane & 15) >> 2)) * kPreV<D> + 64 * i + 32 * ((lane >> 4) & 1) + 8 * (lane & 3);
+                const v4s_t x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)at);
+                const v4s_t y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(at + 8 * kPreV<D>));
+                const v8s_t z = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+#pragma unroll
+                for (int k = PP - 1; k >= 0; --k) o[i] = mfma32(__builtin_bit_cast(v8, z), pf[u][k], o[i]);
+            }
+    }
+    {
+        float a, b;
+        half_pair(l, a, b);
+        l = a + b;
+    }
+    const int lc = 32 * wave + col;  // column of the block
+    if (lc >= g.count) return;
+    if (p.splits > 1) {
+        float* slot = p.pre_ws + work.slot * kPreSlotFloats<D>;
+        if (j0 < j1)
+#pragma unroll
+            for (int i = 0; i < DB; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    *reinterpret_cast<v4f_t*>(slot + lc * D + 32 * i + 8 * r + 4 * h) =
+                        v4f_t{o[i][4 * r], o[i][4 * r + 1], o[i][4 * r + 2], o[i][4 * r + 3]};
+        if (h == 0) {
+            slot[kPreCols<D> * D + lc] = m;
+            slot[kPreCols<D> * (D + 1) + lc] = l;
+        }
+        return;
+    }
+    const float f = l > 0.0f ? (MX ? 1.0f : p.cache.v_scale[g.head]) / l : 0.0f;
+#pragma unroll
+    for (int i = 0; i < DB; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            store_out<false>(p, q, g, lc, 32 * i + 8 * r + 4 * h,
+                             v4f_t{o[i][4 * r] * f, o[i][4 * r + 1] * f, o[i][4 * r + 2] * f, o[i][4 * r + 3] * f});
+    if (p.lse && h == 0) store_lse(p, q, g, lc, m, l);
+}
+
+// The parts of a block, joined in order: kJoinCols of its columns.
+constexpr int kJoinCols = 32;
+template <bool MX, int D>
+__global__ void __launch_bounds__(kThreads) k_kv_prefill_join(const KvAttention p) {
+    constexpr int pieces = kPreCols<D> / kJoinCols;
+    PreWork work;
+    const int64_t id = blockIdx.x / pieces, first = id / p.cache.heads * p.splits * p.cache.heads + id % p.cache.heads;
+    if (!pre_work<D>(p, first, work)) return;
+    const float v_scale = MX ? 1.0f : p.cache.v_scale[work.g.head];
+    const int c0 = (int)(blockIdx.x % pieces) * kJoinCols;
+    for (int i = threadIdx.x; i < kJoinCols * (D / 4); i += kThreads) {
+        const int cc = c0 + i / (D / 4), d = 4 * (i % (D / 4));
+        if (cc >= work.g.count) return;
+        float top = kLowest, total = 0.0f;
+        v4f_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int k = 0; k < p.splits; ++k) {
+            const float* slot = p.pre_ws + (first + (int64_t)k * p.cache.heads) * kPreSlotFloats<D>;
+            const float l = slot[kPreCols<D> * (D + 1) + cc];
+            if (!(l > 0.0f)) continue;  // (an empty part has written no sums)
+            const float m = slot[kPreCols<D> * D + cc], next = fmaxf(top, m);
+            const float f = __builtin_amdgcn_exp2f(top - next), e = __builtin_amdgcn_exp2f(m - next);
+            const v4f_t x = *reinterpret_cast<const v4f_t*>(slot + cc * D + d);
+            total = total * f + l * e;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sum[r] = sum[r] * f + x[r] * e;
+            top = next;
+        }
+        const float f = total > 0.0f ? v_scale / total : 0.0f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sum[r] *= f;
+        store_out<false>(p, work.q, work.g, cc, d, sum);
+        if (p.lse && d == 0) store_lse(p, work.q, work.g, cc, top, total);
+    }
+}
+
+// Blocks of one kv head at most, and the parts of each: with fewer than 512
+// workgroups (two for each compute unit) each block's keys are split.
+int64_t pre_blocks_most(int64_t rows, int64_t seqs, int group, int dim) {
+    const int64_t cols = dim == 256 ? kPreCols<256> : kPreCols<128>;
+    return rows * group / cols + std::min(seqs, rows * group / (kFewColumns + 1));
+}
+
+int pre_splits(int64_t rows, int64_t seqs, int group, int heads, int dim) {
+    const int64_t blocks = pre_blocks_most(rows, seqs, group, dim) * heads;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(16, 512 / std::max<int64_t>(1, blocks)));
+}
+
+template <bool MX, int D>
+hipError_t run_prefill(KvAttention p, hipStream_t s) {
+    constexpr int bytes = 2 * kPreBytes<D>;
+    const int64_t blocks = pre_blocks_most(p.plan.rows, p.plan.seqs, p.group, D) * p.cache.heads;
+    p.splits = pre_splits(p.plan.rows, p.plan.seqs, p.group, p.cache.heads, D);
+    p.pre_ws = p.ws + 2 * kShares * kSlotFloats<D>;
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_kv_prefill<MX, D>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((k_kv_prefill<MX, D>), dim3((uint32_t)(blocks * p.splits)), dim3(64 * kPreWaves<D>), bytes, s, p);
+    if (p.splits > 1)
+        hipLaunchKernelGGL((k_kv_prefill_join<MX, D>), dim3((uint32_t)(blocks * (kPreCols<D> / kJoinCols))), dim3(kThreads), 0, s, p);
+    return hipGetLastError();
+}
+
 template <bool MX, bool F32, int D>
 hipError_t run(const KvAttention& p, hipStream_t s) {
     constexpr int bytes = kWaves * kWaveBytes<D>;
@@ -573,16 +980,26 @@ hipError_t run(const KvAttention& p, hipStream_t s) {
     }
     hipLaunchKernelGGL((k_kv_attention<MX, F32, D>), dim3(kShares), dim3(kThreads), bytes, s, p);
     hipLaunchKernelGGL((k_kv_join<MX, F32, D>), dim3(kShares - 1), dim3(kThreads), 0, s, p);
+    if constexpr (!F32) {
+        // (offsets may give all rows to one sequence)
+        const int64_t most = p.plan.offsets ? (int64_t)p.plan.rows * p.group : p.group;
+        if (most > kFewColumns) return run_prefill<MX, D>(p, s);
+    }
     return hipGetLastError();
 }
 
 }  // namespace
 
-size_t kv_attention_workspace_bytes(int64_t rows, int q_heads, int kv_heads, int dim, bool bf16) {
-    (void)q_heads;
-    (void)kv_heads;
-    (void)bf16;
-    return rows > 0 ? (size_t)2 * kShares * (kCols * dim + 2 * kCols) * sizeof(float) : 0;
+size_t kv_attention_workspace_bytes(int64_t rows, int64_t seqs, int q_heads, int kv_heads, int dim, bool bf16) {
+    if (rows == 0) return 0;
+    int64_t floats = 2 * kShares * (kCols * dim + 2 * kCols);
+    const int group = q_heads / kv_heads;
+    if (bf16 && rows * group > kFewColumns) {
+        const int64_t cols = dim == 256 ? kPreCols<256> : kPreCols<128>;
+        const int splits = pre_splits(rows, seqs, group, kv_heads, dim);
+        if (splits > 1) floats += pre_blocks_most(rows, seqs, group, dim) * kv_heads * splits * cols * (dim + 2);
+    }
+    return (size_t)floats * sizeof(float);
 }
 
 hipError_t launch_kv_attention(const KvAttention& p, hipStream_t s) {

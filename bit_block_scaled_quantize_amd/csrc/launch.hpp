@@ -230,6 +230,9 @@ struct KvRows {
     int64_t row, head;
 };
 constexpr int64_t kMaxKvSeqs = 65536;
+// Rows x heads of q of one call (its workgroups, at most one for 64 of them and
+// one for 128, then fit a grid).
+constexpr int64_t kMaxKvQueries = (int64_t)1 << 28;
 struct KvAppend {
     KvCache cache;
     KvPlan plan;
@@ -262,8 +265,10 @@ struct KvAttention {
     float scale;
     bool bf16;
     float* ws;
+    int splits;     // of the keys of many rows; set by the launcher, as
+    float* pre_ws;  // its part of ws
 };
-size_t kv_attention_workspace_bytes(int64_t rows, int q_heads, int kv_heads, int dim, bool bf16);
+size_t kv_attention_workspace_bytes(int64_t rows, int64_t seqs, int q_heads, int kv_heads, int dim, bool bf16);
 hipError_t launch_kv_attention(const KvAttention& p, hipStream_t s);
 
 }  // namespace nvfp4

@@ -727,12 +727,12 @@ nvfp4_status nvfp4_kv_gather(const nvfp4_kv_cache* cache, const nvfp4_kv_plan* p
     return launch_kv_gather(g, static_cast<hipStream_t>(stream)) == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
 }
 
-size_t nvfp4_kv_attention_workspace_size(int64_t rows, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+size_t nvfp4_kv_attention_workspace_size(int64_t rows, int64_t seqs, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                                          int32_t dt /* nvfp4_dtype */) {
-    if (rows < 0 || rows > kMaxKvRows || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads || !valid_dtype(dt)) return 0;
+    if (rows < 0 || seqs < 0 || seqs > kMaxKvSeqs || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads || !valid_dtype(dt)) return 0;
     if (head_dim != 64 && head_dim != 128 && head_dim != 256) return 0;
-    if (rows > 0x7FFFFFFF / q_heads) return 0;
-    return kv_attention_workspace_bytes(rows, q_heads, kv_heads, head_dim, dt == NVFP4_BF16);
+    if (rows > kMaxKvQueries / q_heads) return 0;
+    return kv_attention_workspace_bytes(rows, seqs, q_heads, kv_heads, head_dim, dt == NVFP4_BF16);
 }
 
 nvfp4_status nvfp4_kv_attention(const nvfp4_kv_rows* q, int32_t dt /* nvfp4_dtype */, int32_t q_heads,
@@ -747,8 +747,8 @@ nvfp4_status nvfp4_kv_attention(const nvfp4_kv_rows* q, int32_t dt /* nvfp4_dtyp
     if (st == NVFP4_OK) st = check_heads(out, rows, q_heads, dim, dt, true);
     if (st != NVFP4_OK) return st;
     if (!aligned(lse, 4)) return NVFP4_ERR_ALIGN;
-    if (rows > 0x7FFFFFFF / q_heads) return NVFP4_ERR_UNSUPPORTED;
-    const size_t need = nvfp4_kv_attention_workspace_size(rows, q_heads, cache->kv_heads, cache->head_dim, dt);
+    if (rows > kMaxKvQueries / q_heads) return NVFP4_ERR_UNSUPPORTED;
+    const size_t need = nvfp4_kv_attention_workspace_size(rows, plan->seqs, q_heads, cache->kv_heads, cache->head_dim, dt);
     if (need) {
         if (!ws || ws_bytes < need) return NVFP4_ERR_WORKSPACE;
         if (!aligned(ws, 16)) return NVFP4_ERR_ALIGN;

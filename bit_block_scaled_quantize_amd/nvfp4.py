@@ -151,7 +151,7 @@ def _load():
     L.nvfp4_kv_append.restype = i32
     L.nvfp4_kv_gather.argtypes = [kv[1], kv[2], kv[0], kv[0], i32, vp]
     L.nvfp4_kv_gather.restype = i32
-    L.nvfp4_kv_attention_workspace_size.argtypes = [i64, i32, i32, i32, i32]
+    L.nvfp4_kv_attention_workspace_size.argtypes = [i64, i64, i32, i32, i32, i32]
     L.nvfp4_kv_attention_workspace_size.restype = sz
     L.nvfp4_kv_attention.argtypes = [kv[0], i32, i32, kv[1], kv[2], ctypes.c_float, i64, kv[0], vp, vp, sz, vp]
     L.nvfp4_kv_attention.restype = i32
@@ -700,9 +700,9 @@ def nvfp4_kv_gather(cache, page_table, lengths, offsets=None, rows=None, dtype=t
                              _dtype_code(dtype), *((None, None) if out is None else out), _handle(stream))
 
 
-def nvfp4_kv_attention_workspace_size(rows, q_heads, kv_heads, head_dim, dtype=torch.bfloat16):
-    """Bytes of workspace of nvfp4_kv_attention."""
-    return int(lib.nvfp4_kv_attention_workspace_size(rows, q_heads, kv_heads, head_dim, _dtype_code(dtype)))
+def nvfp4_kv_attention_workspace_size(rows, seqs, q_heads, kv_heads, head_dim, dtype=torch.bfloat16):
+    """Bytes of workspace of nvfp4_kv_attention for rows of q in seqs sequences."""
+    return int(lib.nvfp4_kv_attention_workspace_size(rows, seqs, q_heads, kv_heads, head_dim, _dtype_code(dtype)))
 
 
 @_launches_on_stream

@@ -618,8 +618,9 @@ nvfp4_status nvfp4_kv_append(const nvfp4_kv_rows* k, const nvfp4_kv_rows* v, int
 nvfp4_status nvfp4_kv_gather(const nvfp4_kv_cache* cache, const nvfp4_kv_plan* plan, nvfp4_kv_rows* k,
                              nvfp4_kv_rows* v, int32_t dt /* nvfp4_dtype */, void* stream);
 
-/* Bytes of workspace nvfp4_kv_attention needs (0 for invalid sizes). */
-size_t nvfp4_kv_attention_workspace_size(int64_t rows, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+/* Bytes of workspace nvfp4_kv_attention needs for a plan of that many rows and
+ * sequences (0 for invalid sizes). */
+size_t nvfp4_kv_attention_workspace_size(int64_t rows, int64_t seqs, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                                          int32_t dt /* nvfp4_dtype */);
 
 /* Attention of the plan's rows of q (rows x q_heads x head_dim, dtype dt) over
@@ -632,12 +633,13 @@ size_t nvfp4_kv_attention_workspace_size(int64_t rows, int32_t q_heads, int32_t 
  * Products are exact (of binary32 q: of its two FP16 parts for NVFP4, 22
  * bits, or three BF16 parts for MXFP4), sums and the softmax's statistics
  * binary32; the weights w_j go into the second product rounded to FP16 for
- * BF16 q over NVFP4 (2^-12), as two BF16 parts over MXFP4 (2^-17), and as two
- * FP16 or three BF16 parts for binary32 q.  Scores must stay in binary32's range.  A
+ * BF16 q over NVFP4 (2^-12, and 2^-36 of the row's largest weight for those far below it), as two
+ * BF16 parts over MXFP4 (2^-17), and as two FP16 or three BF16 parts for
+ * binary32 q.  Scores must stay in binary32's range.  A
  * row of q that is not finite gives unspecified results, the other rows theirs.
  * ws 16-byte aligned, ws_bytes >= nvfp4_kv_attention_workspace_size(...); it is
  * scratch for this call only: calls that overlap must not share it.
- * q_heads % kv_heads == 0; rows * q_heads < 2^31 (else UNSUPPORTED).  Results
+ * q_heads % kv_heads == 0; rows * q_heads <= 2^28 (else UNSUPPORTED).  Results
  * repeat bit for bit. */
 nvfp4_status nvfp4_kv_attention(const nvfp4_kv_rows* q, int32_t dt /* nvfp4_dtype */, int32_t q_heads,
                                 const nvfp4_kv_cache* cache, const nvfp4_kv_plan* plan, float scale, int64_t window,

@@ -114,21 +114,21 @@ def attention(q, cache, table, lengths, offsets, scale, window, pages, page_size
             mean_abs[first:first + n, h] = w @ v[h // group].abs()
             lse[first:first + n, h] = z
             eps[first:first + n, h, 0] = e
-            lost[first:first + n, h, 0] = 2.0 ** -40 * seen.sum(dim=1) * v[h // group].abs().max()
+            lost[first:first + n, h, 0] = 2.0 ** -36 * seen.sum(dim=1) * v[h // group].abs().max()
     weight = 2.0 * eps + 2.0 ** -19
     return out, lse, mean_abs, weight, lost
 
 
-#: relative error of a weight as it goes into the second product
+#: relative error of a weight as it goes into the second product (half a step of each part)
 WEIGHT = {("bf16", False): 2.0 ** -12, ("bf16", True): 2.0 ** -17, ("f32", False): 2.0 ** -22, ("f32", True): 2.0 ** -24}
 
 
 def check_attention(got, got_lse, want, dtype, mx, rows=None):
     out, lse, mean_abs, weight, lost = want
     half = torch.finfo(DT[dtype]).eps / 2
-    # FP16 weights in [0, 2^15]: below 2^-14 a rounding is off by up to 2^-25, which is 2^-40 of the largest weight (in the
-    # running maximum's scale it is smaller still), so of the result by up to 2^-40 max |v| for each key: `lost`.  It counts
-    # where the keys of the large weights hold zeros, as E2M1 values often are.
+    # FP16 weights are taken times 2^11 over a maximum that is at most the row's own: below 2^-14 a rounding is off by up to
+    # 2^-25, which is 2^-36 of the largest weight or less, so of the result by up to 2^-36 max |v| for each key: `lost`.  It
+    # counts where the keys of the large weights hold zeros, as E2M1 values often are.
     tol = (weight + WEIGHT[dtype, mx] + 1e-5) * mean_abs + half * out.abs() + (0.0 if mx else 1.0) * lost + 1e-37
     tol = tol * (1.0 + 2.0 ** -7)
     keep = slice(None) if rows is None else rows

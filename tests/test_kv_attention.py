@@ -86,6 +86,32 @@ def test_many_rows(nv, dtype):
     run_and_check(nv, [1100], [1030], 1, 5, 64, 16, True, dtype, window=500, seed=6)
 
 
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_blocks_of_many_columns(nv, dim, mx):
+    """Sequences of over 64 columns beside ones of few, whole and split by keys."""
+    run_and_check(nv, [65, 10, 700, 33], [65, 1, 300, 0], 2, 3, dim, 16, mx, "bf16", seed=20)
+    run_and_check(nv, [40, 1000], [50, 17], 1, 8, dim, 32, mx, "bf16", seed=21)  # ten rows before the first position
+    run_and_check(nv, [2100, 900], [257, 128], 1, 4, dim, 64, mx, "bf16", window=200, seed=22)
+    run_and_check(nv, [300], [100], 1, 5, dim, 64, mx, "bf16", scale=-0.7, seed=23)
+    run_and_check(nv, [300], [100], 1, 5, dim, 64, mx, "bf16", scale=0.0, seed=24)
+    run_and_check(nv, [500, 20], None, 1, 70, dim, 64, mx, "bf16", seed=25)  # one row of 70 heads to a kv head
+    new = [1 + (13 * i) % 30 for i in range(40)]
+    run_and_check(nv, [n + (97 * i) % 250 for i, n in enumerate(new)], new, 8, 6, dim, 16, mx, "bf16", seed=26)
+
+
+def test_holes_under_many_rows(nv):
+    cache, table, L, O, offsets, q = case(nv, [400, 200], [150, 100], 2, 4, 128, 16, False, "bf16", seed=27)
+    table[0, 3] = -1
+    table[0, 20] = cache.k_codes.shape[0]
+    table[1, :] = -5
+    for window in (0, 40):
+        o, lse = nv.nvfp4_kv_attention(q, cache, table, L, O, lse=True, window=window)
+        want = P.attention(q, cache, table, [400, 200], offsets, 128 ** -0.5, window, cache.k_codes.shape[0], 16)
+        P.check_attention(o, lse, want, "bf16", False)
+        assert bool((o[150:] == 0).all()) and bool(torch.isinf(lse[150:]).all())
+
+
 @pytest.mark.parametrize("seqs", [65, 200, 1030])
 def test_many_sequences(nv, seqs):
     lengths = [(37 * i * i + 11 * i) % 90 for i in range(seqs)]
@@ -198,7 +224,7 @@ def test_another_stream_and_a_given_workspace(nv):
     ref = nv.nvfp4_kv_attention(q, cache, table, L)
     torch.cuda.synchronize()
     side = torch.cuda.Stream()
-    ws = torch.empty(nv.nvfp4_kv_attention_workspace_size(2, 8, 2, 128), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(nv.nvfp4_kv_attention_workspace_size(2, 2, 8, 2, 128), dtype=torch.uint8, device="cuda")
     ws.fill_(255)
     torch.cuda.synchronize()
     got = [nv.nvfp4_kv_attention(q, cache, table, L, stream=side, workspace=ws) for _ in range(3)]
@@ -226,7 +252,7 @@ def test_a_captured_step_follows_its_inputs(nv):
     rope = torch.cat([a.cos(), a.sin()], dim=1).float().cuda()
     q, k, v = (torch.zeros((3, h, dim), device="cuda").bfloat16() for h in (heads * group, heads, heads))
     L = torch.tensor(start, dtype=torch.int32).cuda() + 1
-    ws = torch.empty(nv.nvfp4_kv_attention_workspace_size(3, heads * group, heads, dim), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(nv.nvfp4_kv_attention_workspace_size(3, 3, heads * group, heads, dim), dtype=torch.uint8, device="cuda")
 
     def step(cache, table, workspace=None):
         r = nv.nvfp4_kv_append(k, v, cache, table, L, q=q, rope=rope)

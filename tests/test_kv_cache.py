@@ -112,10 +112,11 @@ def test_gather_and_attention_reject_bad_arguments(nv):
                      ("ALIGN", dict(lse=65538)), ("WS", dict(ws=None)), ("WS", dict(ws_bytes=1000)),
                      ("ALIGN", dict(ws=65544))]:
         assert attention(c, p, **kw) == E[want], (want, kw)
-    assert attention(c, _plan(nv, rows=1 << 30), hq=4, q=_rows(nv, row=0), out=_rows(nv, row=512)) == E["UNSUP"]
+    assert attention(c, _plan(nv, rows=(1 << 26) + 1), hq=4, q=_rows(nv, row=0), out=_rows(nv, row=512)) == E["UNSUP"]
     size = nv.nvfp4_kv_attention_workspace_size
-    assert size(5, 4, 2, 128) > 0 and size(0, 4, 2, 128) == 0
-    assert size(5, 3, 2, 128) == 0 and size(5, 4, 2, 96) == 0 and size(-1, 4, 2, 128) == 0
+    assert size(5, 3, 4, 2, 128) > 0 and size(0, 3, 4, 2, 128) == 0
+    assert size(5, 3, 3, 2, 128) == 0 and size(5, 3, 4, 2, 96) == 0 and size(-1, 3, 4, 2, 128) == 0
+    assert size(5, -1, 4, 2, 128) == 0 and size(1 << 27, 3, 4, 2, 128) == 0
 
 
 def test_the_binding_checks_shapes_and_types(nv):
