@@ -48,8 +48,8 @@ typedef uint32_t w_align1 __attribute__((aligned(1)));
 
 constexpr int kThreads = 256, kWaves = 4;
 constexpr int kCols = 16;     // columns (rows of q x heads of a group) of a segment
-constexpr int kTile = 64;     // keys of a unit of work
-constexpr int kShares = 512;  // workgroups: two on each of 256 compute units
+constexpr int kStep = 32;     // keys of a unit of work
+constexpr int kTile = 64;     // keys of a tile of k_kv_prefill
 constexpr float kLowest = -3.402823466e38f;
 // Weights are taken over a maximum that may lie up to kSlack (in powers of two)
 // below the true one, so that the sums are rescaled seldom, and times 2^kBias,
@@ -151,8 +151,8 @@ __device__ __forceinline__ Seq seq_of(const KvAttention& p, int s) {
     const int64_t cols = (int64_t)q.rows * p.group;
     q.columns = p.bf16 && cols > kFewColumns ? 0 : (int)((cols + kCols - 1) / kCols);
     const int64_t low = p.window ? (int64_t)q.length - q.rows - p.window + 1 : 0;
-    q.first_tile = low > 0 ? (int)(low / kTile) : 0;
-    q.tiles = max(1, (q.length + kTile - 1) / kTile - q.first_tile);
+    q.first_tile = low > 0 ? (int)(low / kStep) : 0;
+    q.tiles = max(1, (q.length + kStep - 1) / kStep - q.first_tile);
     return q;
 }
 
@@ -160,48 +160,80 @@ __device__ __forceinline__ int64_t units_of(const KvAttention& p, const Seq& q) 
     return (int64_t)q.columns * q.tiles * p.cache.heads;
 }
 
-__device__ __forceinline__ int64_t shfl64(int64_t v, int from) {
-    return (int64_t)((uint64_t)(uint32_t)__shfl((int)(v >> 32), from) << 32 | (uint32_t)__shfl((int)v, from));
+// A lane's value in every lane.
+__device__ __forceinline__ int64_t from_lane(int64_t v, int lane) {
+    return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 |
+                     (uint32_t)__builtin_amdgcn_readlane((int)v, lane));
 }
 
-// Inclusive sum over the lanes.
+// v of the lane SHIFT places below within its row of 16, 0 where there is none.
+template <int SHIFT>
+__device__ __forceinline__ int64_t row_below(int64_t v) {
+    const int lo = __builtin_amdgcn_update_dpp(0, (int)v, 0x110 + SHIFT, 0xF, 0xF, true);
+    const int hi = __builtin_amdgcn_update_dpp(0, (int)(v >> 32), 0x110 + SHIFT, 0xF, 0xF, true);
+    return (int64_t)((uint64_t)(uint32_t)hi << 32 | (uint32_t)lo);
+}
+
+// Inclusive sum over the lanes (all active): rows of 16, then the rows below.
 __device__ __forceinline__ int64_t scan64(int64_t v) {
-    const int lane = threadIdx.x & 63;
-    for (int d = 1; d < 64; d <<= 1) {
-        const int64_t o = shfl64(v, lane >= d ? lane - d : lane);
-        if (lane >= d) v += o;
+    v += row_below<1>(v);
+    v += row_below<2>(v);
+    v += row_below<4>(v);
+    v += row_below<8>(v);
+    const int row = (threadIdx.x & 63) >> 4;
+    const int64_t a = from_lane(v, 15), b = a + from_lane(v, 31), c = b + from_lane(v, 47);
+    return v + (row == 0 ? 0 : row == 1 ? a : row == 2 ? b : c);
+}
+
+// A list of entries by sequence, `count(s)` of sequence s: the sum of all, and
+// the sequence of entry u (< sum) with the first entry of that sequence.  64
+// sequences at a time; the first 64 are counted once.
+template <typename Count>
+struct List {
+    Count count;
+    int seqs;
+    int64_t own0, upto0, sum;
+    __device__ __forceinline__ List(int seqs_, Count c) : count(c), seqs(seqs_) {
+        own0 = lane_count(0);
+        upto0 = scan64(own0);
+        sum = from_lane(upto0, 63);
+        for (int b = 64; b < seqs; b += 64) sum += from_lane(scan64(lane_count(b)), 63);
     }
-    return v;
-}
-
-// Units of sequences 64 b and on, by lane.
-__device__ __forceinline__ int64_t lane_units(const KvAttention& p, int b) {
-    const int s = b + (threadIdx.x & 63);
-    return s < p.plan.seqs ? units_of(p, seq_of(p, s)) : 0;
-}
-
-__device__ __forceinline__ int64_t all_units(const KvAttention& p) {
-    int64_t sum = 0;
-    for (int b = 0; b < p.plan.seqs; b += 64) sum += shfl64(scan64(lane_units(p, b)), 63);
-    return sum;
-}
-
-// Sequence of unit u (< all_units) and the first unit of that sequence.
-__device__ __forceinline__ int find_seq(const KvAttention& p, int64_t u, int64_t& first) {
-    int64_t before = 0;
-    for (int b = 0;; b += 64) {
-        const int64_t own = lane_units(p, b), upto = scan64(own), all = shfl64(upto, 63);
-        if (u < before + all) {
-            const int l = __builtin_ctzll(__ballot(u < before + upto));
-            first = before + shfl64(upto - own, l);
-            return b + l;
+    __device__ __forceinline__ int64_t lane_count(int b) const {
+        const int s = b + (threadIdx.x & 63);
+        return s < seqs ? count(s) : 0;
+    }
+    __device__ __forceinline__ int find(int64_t u, int64_t& first) const {
+        int64_t before = 0, own = own0, upto = upto0;
+        for (int b = 0;;) {
+            const int64_t all = from_lane(upto, 63);
+            if (u < before + all) {
+                const int l = __builtin_ctzll(__ballot(u < before + upto));
+                first = before + from_lane(upto - own, l);
+                return b + l;
+            }
+            before += all;
+            b += 64;
+            own = lane_count(b);
+            upto = scan64(own);
         }
-        before += all;
     }
+};
+template <typename Count>
+__device__ __forceinline__ List<Count> list_of(int seqs, Count c) {
+    return List<Count>(seqs, c);
 }
 
-// Workgroups that take a share: one for 4 tiles (its waves) at least.
-__device__ __forceinline__ int64_t shares_of(int64_t units) { return max((int64_t)1, min((int64_t)kShares, units / kWaves)); }
+// Workgroups that take a share (three on each of 256 compute units, as many as
+// LDS holds of D 256): one for kLeast units at least.
+template <int D>
+constexpr int kShares = D == 256 ? 512 : 1024;
+constexpr int kLeast = 2 * kWaves;
+
+template <int D>
+__device__ __forceinline__ int64_t shares_of(int64_t units) {
+    return max((int64_t)1, min((int64_t)kShares<D>, units / kLeast));
+}
 
 __device__ __forceinline__ int64_t share_begin(int64_t w, int64_t shares, int64_t units) {
     const int64_t each = units / shares, rest = units % shares;
@@ -279,7 +311,8 @@ template <int D>
 constexpr int kMergeStride = D + 4;
 
 template <int D, bool MX>
-__device__ __forceinline__ void load_codes(const uint8_t* codes, const uint8_t* scales, Codes<D>& c) {
+__device__ __forceinline__ Codes<D> load_codes(const uint8_t* codes, const uint8_t* scales) {
+    Codes<D> c;
     if constexpr (D == 64) {
         const uint2 q = *reinterpret_cast<const uint2*>(codes);
         c.w[0] = q.x;
@@ -296,6 +329,7 @@ __device__ __forceinline__ void load_codes(const uint8_t* codes, const uint8_t* 
     if constexpr (n <= 1) c.s = *scales;
     else if constexpr (n == 2) c.s = *reinterpret_cast<const h_align1*>(scales);
     else c.s = *reinterpret_cast<const w_align1*>(scales);
+    return c;
 }
 
 // The j-th 8 of the lane's elements.
@@ -304,8 +338,14 @@ __device__ __forceinline__ typename Form<MX>::v8 values8(const Codes<D>& c, int 
     return Form<MX>::values(c.w[j], (c.s >> (8 * (8 * j / (MX ? 32 : 16)))) & 0xFFu);
 }
 
+// What a lane holds of 32 keys: of sub-tile t key 16 t + lane % 16.
+template <int D>
+struct Step {
+    Codes<D> k[2], v[2];
+};
+
 template <bool MX, bool F32, int D>
-__global__ void __launch_bounds__(kThreads, 2) k_kv_attention(const KvAttention p) {
+__global__ void __launch_bounds__(kThreads, kShares<D> / 256) k_kv_attention(const KvAttention p) {
     typedef Form<MX> F;
     typedef typename F::v8 v8;
     constexpr int QP = kQParts<MX, F32>, PP = kPParts<MX, F32>, KD = D / 32;
@@ -315,13 +355,13 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv_attention(const KvAttention 
     char* lds = kv_lds + wave * kWaveBytes<D>;
     __shared__ float stats[2][kWaves][kCols];
 
-    const int64_t units = all_units(p);
-    const int64_t shares = shares_of(units), me = blockIdx.x;
+    const auto list = list_of(p.plan.seqs, [&](int i) { return units_of(p, seq_of(p, i)); });
+    const int64_t units = list.sum, shares = shares_of<D>(units), me = blockIdx.x;
     if (units == 0 || me >= shares) return;
     int64_t u = share_begin(me, shares, units);
     const int64_t u_end = share_begin(me + 1, shares, units);
     int64_t seq_first;
-    int s = find_seq(p, u, seq_first);
+    int s = __builtin_amdgcn_readfirstlane(list.find(u, seq_first));
     Seq q = seq_of(p, s);
     const int slot_mask = (1 << p.plan.page_shift) - 1;
 
@@ -340,38 +380,72 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv_attention(const KvAttention 
         // of the segment's first and last column
         const int pos_first = q.length - q.rows + g.first / p.group;
         const int pos_last = q.length - q.rows + (g.first + g.count - 1) / p.group;
-        const int seg_low = p.window ? max(0, pos_first - p.window + 1) : 0;
+        const int low_first = p.window ? max(0, pos_first - p.window + 1) : 0;
+        const int low_last = p.window ? max(0, pos_last - p.window + 1) : 0;
+
+        // steps of 32 keys that some column sees
+        const int j1 = min(q.first_tile + (int)(stop - g.begin), pos_last < 0 ? 0 : pos_last / kStep + 1);
+        int j = max(q.first_tile + (int)(u - g.begin), low_first / kStep) + wave;
+
+        const auto find_page = [&](int at, int t) {
+            const int k16 = at * kStep + 16 * t;
+            return at < j1 && k16 < q.length ? kv_page(p.plan, p.cache.pages, s, k16) : -1;
+        };
+        const auto load = [&](int at, int t, int page, const uint8_t* codes, const uint8_t* scales) {
+            Codes<D> c = {};
+            if (page >= 0) {
+                const int64_t first = (((int64_t)page * p.cache.heads + g.head) << p.plan.page_shift) + ((at * kStep + 16 * t) & slot_mask);
+                c = load_codes<D, MX>(codes + first * (D / 2) + (col * (D / 2) + g4 * (D / 8)),
+                                      scales + first * (D / per) + (col * (D / per) + g4 * (D / 4) / per));
+            }
+            return c;
+        };
+        Step<D> st;  // the step at j
+        int page[2], next[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            page[t] = __builtin_amdgcn_readfirstlane(find_page(j, t));
+            st.k[t] = load(j, t, page[t], p.cache.k_codes, p.cache.k_scales);
+            st.v[t] = load(j, t, page[t], p.cache.v_codes, p.cache.v_scales);
+            next[t] = find_page(j + kWaves, t);
+        }
 
         // q, its row scaled into FP16's range
         v8 qf[KD][QP];
-        float factor = p.scale * kLog2e;
+        float factor = fabsf(p.scale) * kLog2e;
         if constexpr (!MX) factor *= p.cache.k_scale[g.head];
         {
             float v[KD][8];
             const int64_t at = (q.row + qrow) * p.q.row + qhead * p.q.head + g4 * (D / 4);
 #pragma unroll
-            for (int j = 0; j < KD; ++j) {
-                if constexpr (F32) load_upto8(static_cast<const float*>(p.q.data) + at + 8 * j, 8, v[j]);
-                else load_upto8(static_cast<const uint16_t*>(p.q.data) + at + 8 * j, 8, v[j]);
+            for (int i = 0; i < KD; ++i) {
+                if constexpr (F32) load_upto8(static_cast<const float*>(p.q.data) + at + 8 * i, 8, v[i]);
+                else load_upto8(static_cast<const uint16_t*>(p.q.data) + at + 8 * i, 8, v[i]);
             }
+            int e = 15;
             if constexpr (!MX) {
                 float top = 0.0f;
 #pragma unroll
-                for (int j = 0; j < KD; ++j)
+                for (int i = 0; i < KD; ++i)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[j][i]));
+                    for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(v[i][k]));
                 float a, b;
                 row_pair(top, a, b);
                 half_pair(fmaxf(a, b), a, b);
-                const int e = __builtin_amdgcn_frexp_expf(fmaxf(a, b));  // 0 for 0
-#pragma unroll
-                for (int j = 0; j < KD; ++j)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[j][i] = ldexpf(v[j][i], 15 - e);
+                e = __builtin_amdgcn_frexp_expf(fmaxf(a, b));  // 0 for 0
                 factor = ldexpf(factor, e - 15);
             }
+            // (the scale's sign goes with q, so that larger sums are larger scores)
 #pragma unroll
-            for (int j = 0; j < KD; ++j) split8<MX, QP>(v[j], qf[j]);
+            for (int i = 0; i < KD; ++i) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    if constexpr (!MX) v[i][k] = ldexpf(v[i][k], 15 - e);
+                    if (p.scale < 0.0f) v[i][k] = -v[i][k];
+                }
+                split8<MX, QP>(v[i], qf[i]);
+            }
+            factor = fmaxf(factor, 1e-37f);  // (0 times a hidden score's -inf is no number)
         }
 
         float m = kLowest, l = 0.0f;
@@ -379,102 +453,97 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv_attention(const KvAttention 
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) o[i] = v4f_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-        const int j0 = q.first_tile + (int)(u - g.begin), j1 = q.first_tile + (int)(stop - g.begin);
-        for (int j = j0 + wave; j < j1; j += kWaves) {
-            const int key0 = j * kTile;
-            if (key0 > pos_last || key0 + kTile <= seg_low) continue;
-#pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
-                const int k32 = key0 + 32 * half;
-                if (k32 > pos_last) break;
-                // pages of the two sub-tiles of 16 keys (-1: none)
-                int page[2];
-                Codes<D> kc[2], vc[2];
+        // Codes are loaded again as soon as they are converted: the next step's
+        // are under way while one is multiplied, and the pages of the one after.
+        for (; j < j1; j += kWaves) {
+            const int k32 = j * kStep;
+            const bool holes[2] = {page[0] < 0, page[1] < 0};
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const int k16 = k32 + 16 * t;
-                    page[t] = -1;
-                    if (k16 < q.length)
-                        page[t] = __builtin_amdgcn_readfirstlane(kv_page(p.plan, p.cache.pages, s, k16));
-                    if (page[t] >= 0) {
-                        const int64_t slot = (((int64_t)page[t] * p.cache.heads + g.head) << p.plan.page_shift) + (k16 & slot_mask) + col;
-                        const int64_t sc = slot * (D / per) + g4 * (D / 4) / per;
-                        load_codes<D, MX>(p.cache.k_codes + slot * (D / 2) + g4 * (D / 8), p.cache.k_scales + sc, kc[t]);
-                        load_codes<D, MX>(p.cache.v_codes + slot * (D / 2) + g4 * (D / 8), p.cache.v_scales + sc, vc[t]);
-                        if (k16 + col >= q.length) kc[t].s = vc[t].s = 0;  // what lies behind the end is no number
-                    } else {
+            for (int t = 0; t < 2; ++t) {
+                const uint32_t there = k32 + 16 * t + col < q.length ? ~0u : 0u;  // (behind the end is no number)
+                st.k[t].s &= there;
+                st.v[t].s &= there;
+                page[t] = __builtin_amdgcn_readfirstlane(next[t]);
+            }
+            // scores: register r of sub-tile t is key 16 t + 4 g4 + r of the column
+            v4f_t sc[2];
 #pragma unroll
-                        for (int i = 0; i < KD; ++i) kc[t].w[i] = vc[t].w[i] = 0;
-                        kc[t].s = vc[t].s = 0;
-                    }
+            for (int t = 0; t < 2; ++t) {
+                sc[t] = v4f_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int i = 0; i < KD; ++i) {
+                    const v8 a = values8<D, MX>(st.k[t], i);
+#pragma unroll
+                    for (int x = QP - 1; x >= 0; --x) sc[t] = F::mfma(a, qf[i][x], sc[t]);
                 }
-                // scores: register r of sub-tile t is key 16 t + 4 g4 + r of the column
-                v4f_t sc[2];
+            }
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    sc[t] = v4f_t{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int t = 0; t < 2; ++t) st.k[t] = load(j + kWaves, t, page[t], p.cache.k_codes, p.cache.k_scales);
+            // V to LDS
 #pragma unroll
-                    for (int i = 0; i < KD; ++i) {
-                        const v8 a = values8<D, MX>(kc[t], i);
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
-                        for (int x = QP - 1; x >= 0; --x) sc[t] = F::mfma(a, qf[i][x], sc[t]);
-                    }
-                }
-                float top = kLowest;
+                for (int i = 0; i < KD; ++i)
+                    *reinterpret_cast<v8*>(lds + (16 * t + col) * kRowBytes<D> + g4 * (D / 2) + 16 * i) = values8<D, MX>(st.v[t], i);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                st.v[t] = load(j + kWaves, t, page[t], p.cache.v_codes, p.cache.v_scales);
+                next[t] = find_page(j + 2 * kWaves, t);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            if (k32 + kStep - 1 > pos_first || k32 < low_last || holes[0] || holes[1]) {
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const int key = k32 + 16 * t + 4 * g4 + r;
-                        const bool seen = page[t] >= 0 && key <= pos && key >= low && key < q.length;
-                        sc[t][r] = seen ? sc[t][r] * factor : -INFINITY;
-                        top = fmaxf(top, sc[t][r]);
+                        sc[t][r] = key <= pos && key >= low && !holes[t] ? sc[t][r] : -INFINITY;
                     }
-                {
-                    float a, b;
-                    row_pair(top, a, b);
-                    half_pair(fmaxf(a, b), a, b);
-                    top = fmaxf(a, b);
-                }
-                if (__any(top > m + kSlack)) {
-                    const float next = fmaxf(m, top), f = __builtin_amdgcn_exp2f(m - next);
-                    m = next;
-                    l *= f;
-#pragma unroll
-                    for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) o[i][r] *= f;
-                }
-                float w[8];
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        w[4 * t + r] = __builtin_amdgcn_exp2f(sc[t][r] - m + kBias);
-                        l += w[4 * t + r];
-                    }
-                v8 pf[PP];
-                split8<MX, PP>(w, pf);
-                // V through LDS
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int i = 0; i < KD; ++i)
-                        *reinterpret_cast<v8*>(lds + (16 * t + col) * kRowBytes<D> + g4 * (D / 2) + 16 * i) = values8<D, MX>(vc[t], i);
-                asm volatile("" ::: "memory");
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    typedef __attribute__((address_space(3))) v4s_t lds_v4s;
-                    char* at = lds + (4 * g4 + (col >> 2)) * kRowBytes<D> + 32 * i + 8 * (col & 3);
-                    const v4s_t x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)at);
-                    const v4s_t y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(at + 16 * kRowBytes<D>));
-                    typedef short v8s_t __attribute__((ext_vector_type(8)));
-                    const v8s_t z = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-#pragma unroll
-                    for (int k = PP - 1; k >= 0; --k) o[i] = F::mfma(__builtin_bit_cast(v8, z), pf[k], o[i]);
-                }
-                asm volatile("" ::: "memory");
             }
+            float top = -INFINITY;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) top = fmaxf(top, sc[t][r]);
+            {
+                float a, b;
+                row_pair(top, a, b);
+                half_pair(fmaxf(a, b), a, b);
+                top = fmaxf(a, b) * factor;
+            }
+            if (__any(top > m + kSlack)) {
+                const float next = fmaxf(m, top), f = __builtin_amdgcn_exp2f(m - next);
+                m = next;
+                l *= f;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) o[i][r] *= f;
+            }
+            const float base = m - kBias;
+            float w[8];
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    w[4 * t + r] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][r], factor, -base));
+                    l += w[4 * t + r];
+                }
+            v8 pf[PP];
+            split8<MX, PP>(w, pf);
+            asm volatile("" ::: "memory");
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                typedef __attribute__((address_space(3))) v4s_t lds_v4s;
+                typedef short v8s_t __attribute__((ext_vector_type(8)));
+                char* from = lds + (4 * g4 + (col >> 2)) * kRowBytes<D> + 32 * i + 8 * (col & 3);
+                const v4s_t x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)from);
+                const v4s_t y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(from + 16 * kRowBytes<D>));
+                const v8s_t z = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+#pragma unroll
+                for (int k = PP - 1; k >= 0; --k) o[i] = F::mfma(__builtin_bit_cast(v8, z), pf[k], o[i]);
+            }
+            asm volatile("" ::: "memory");
         }
 
         // the waves' sums, joined in order
@@ -531,40 +600,84 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv_attention(const KvAttention 
     }
 }
 
-// Share w joins the segment that its first unit lies inside of, where it is the
-// first share that does.
+// Workgroup (w - 1, y) joins columns 4 y and on of the segment that share w
+// begins inside of, where it is the first share that does.  The weights of up
+// to 64 shares are found by lane, a column to a wave; then D / 4 threads have a
+// column's elements, 256 / D of them a part of the shares each.
+constexpr int kJoinColumns = 4;
 template <bool MX, bool F32, int D>
 __global__ void __launch_bounds__(kThreads) k_kv_join(const KvAttention p) {
-    const int64_t units = all_units(p);
-    const int64_t shares = shares_of(units), w = blockIdx.x + 1;
+    constexpr int parts = 256 / D;
+    __shared__ float weight[kJoinColumns][64];
+    __shared__ v4f_t sums[kThreads];
+    const auto list = list_of(p.plan.seqs, [&](int i) { return units_of(p, seq_of(p, i)); });
+    const int64_t units = list.sum, shares = shares_of<D>(units), w = blockIdx.x + 1;
     if (units == 0 || w >= shares) return;
     const int64_t u = share_begin(w, shares, units);
     int64_t seq_first;
-    const int s = find_seq(p, u, seq_first);
-    const Seq q = seq_of(p, s);
+    const Seq q = seq_of(p, list.find(u, seq_first));
     const Segment g = segment_at(p, q, seq_first, u);
-    if (u == g.begin || share_begin(w - 1, shares, units) > g.begin) return;
-    const float v_scale = MX ? 1.0f : p.cache.v_scale[g.head];
-    for (int i = threadIdx.x; i < g.count * (D / 4); i += kThreads) {
-        const int cc = i / (D / 4), d = 4 * (i % (D / 4));
-        float top = kLowest, total = 0.0f;
-        v4f_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int64_t k = w - 1; k < shares && share_begin(k, shares, units) < g.end; ++k) {
-            const float* slot = slot_of<D>(p, k, k == w - 1 ? 1 : 0);
-            const float m = slot[kCols * D + cc], next = fmaxf(top, m);
-            const float f = __builtin_amdgcn_exp2f(top - next), h = __builtin_amdgcn_exp2f(m - next);
-            const v4f_t x = *reinterpret_cast<const v4f_t*>(slot + cc * D + d);
-            total = total * f + slot[kCols * D + kCols + cc] * h;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) sum[r] = sum[r] * f + x[r] * h;
-            top = next;
+    const int c0 = blockIdx.y * kJoinColumns;
+    if (u == g.begin || share_begin(w - 1, shares, units) > g.begin || c0 >= g.count) return;
+    // shares w - 1 .. last have a part
+    int64_t last = w;
+    while (last + 1 < shares && share_begin(last + 1, shares, units) < g.end) ++last;
+    const int n = (int)(last - w + 2);
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int cc = c0 + threadIdx.x / (parts * (D / 4)), part = threadIdx.x / (D / 4) % parts, d = 4 * (threadIdx.x % (D / 4));
+    float top = kLowest, total = 0.0f;  // of the wave's column
+    v4f_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int b = 0; b < n; b += 64) {
+        const int most = min(64, n - b);
+        float m = kLowest, l = 0.0f;
+        if (lane < most) {
+            const float* slot = slot_of<D>(p, w - 1 + b + lane, b + lane == 0 ? 1 : 0) + kCols * D + min(c0 + wave, g.count - 1);
+            m = slot[0];
+            l = slot[kCols];
         }
-        const float f = total > 0.0f ? v_scale / total : 0.0f;
+        const float next = fmaxf(top, reduce64(m, MaxOp())), f = __builtin_amdgcn_exp2f(top - next);
+        const float e = __builtin_amdgcn_exp2f(m - next);
+        total = total * f + reduce64(l * e, AddOp());
+        top = next;
+        if (b) {  // what is summed so far, to the new maximum
+            if (lane == 0) weight[wave][0] = f;
+            __syncthreads();
+            const float mine = weight[cc - c0][0];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) sum[r] *= f;
-        store_out<F32>(p, q, g, cc, d, sum);
-        if (p.lse && d == 0) store_lse(p, q, g, cc, top, total);
+            for (int r = 0; r < 4; ++r) sum[r] *= mine;
+            __syncthreads();
+        }
+        weight[wave][lane] = e;
+        __syncthreads();
+#pragma unroll 8
+        for (int k = part; k < most; k += parts) {
+            const float x = weight[cc - c0][k];
+            const v4f_t y = *reinterpret_cast<const v4f_t*>(slot_of<D>(p, w - 1 + b + k, b + k == 0 ? 1 : 0) +
+                                                            min(cc, g.count - 1) * D + d);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sum[r] += x * y[r];
+        }
+        __syncthreads();
     }
+    if (lane == 0) {
+        weight[wave][0] = total;
+        weight[wave][1] = top;
+    }
+    sums[threadIdx.x] = sum;
+    __syncthreads();
+    if (part || cc >= g.count) return;
+#pragma unroll
+    for (int i = 1; i < parts; ++i) {
+        const v4f_t y = sums[threadIdx.x + i * (D / 4)];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sum[r] += y[r];
+    }
+    total = weight[cc - c0][0];
+    const float f = total > 0.0f ? (MX ? 1.0f : p.cache.v_scale[g.head]) / total : 0.0f;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) sum[r] *= f;
+    store_out<F32>(p, q, g, cc, d, sum);
+    if (p.lse && d == 0) store_lse(p, q, g, cc, weight[cc - c0][1], total);
 }
 
 // ---------------------------------------------------------------- many rows
@@ -608,22 +721,13 @@ __device__ __forceinline__ int pre_blocks(const KvAttention& p, int s) {
 // sequence and number there; false past the end.
 template <int D>
 __device__ __forceinline__ bool pre_find(const KvAttention& p, int64_t index, int& s, int& block) {
-    const int lane = threadIdx.x & 63;
-    int64_t all = 0;
-    for (int b = 0; b < p.plan.seqs; b += 64) all += shfl64(scan64(b + lane < p.plan.seqs ? pre_blocks<D>(p, b + lane) : 0), 63);
-    if (index >= all) return false;
-    index = all - 1 - index;
-    for (int b = 0;; b += 64) {
-        const int64_t own = b + lane < p.plan.seqs ? pre_blocks<D>(p, b + lane) : 0;
-        const int64_t upto = scan64(own), sum = shfl64(upto, 63);
-        if (index < sum) {
-            const int l = __builtin_ctzll(__ballot(index < upto));
-            s = __builtin_amdgcn_readfirstlane(b + l);
-            block = __builtin_amdgcn_readfirstlane((int)(index - shfl64(upto - own, l)));
-            return true;
-        }
-        index -= sum;
-    }
+    const auto list = list_of(p.plan.seqs, [&](int i) { return (int64_t)pre_blocks<D>(p, i); });
+    if (index >= list.sum) return false;
+    index = list.sum - 1 - index;
+    int64_t first;
+    s = __builtin_amdgcn_readfirstlane(list.find(index, first));
+    block = __builtin_amdgcn_readfirstlane((int)(index - first));
+    return true;
 }
 
 // What workgroup `id` of k_kv_prefill does: columns of a kv head (neighbouring
@@ -959,7 +1063,7 @@ hipError_t run_prefill(KvAttention p, hipStream_t s) {
     constexpr int bytes = 2 * kPreBytes<D>;
     const int64_t blocks = pre_blocks_most(p.plan.rows, p.plan.seqs, p.group, D) * p.cache.heads;
     p.splits = pre_splits(p.plan.rows, p.plan.seqs, p.group, p.cache.heads, D);
-    p.pre_ws = p.ws + 2 * kShares * kSlotFloats<D>;
+    p.pre_ws = p.ws + 2 * kShares<D> * kSlotFloats<D>;
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_kv_prefill<MX, D>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != hipSuccess) return e;
@@ -978,8 +1082,8 @@ hipError_t run(const KvAttention& p, hipStream_t s) {
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((k_kv_attention<MX, F32, D>), dim3(kShares), dim3(kThreads), bytes, s, p);
-    hipLaunchKernelGGL((k_kv_join<MX, F32, D>), dim3(kShares - 1), dim3(kThreads), 0, s, p);
+    hipLaunchKernelGGL((k_kv_attention<MX, F32, D>), dim3(kShares<D>), dim3(kThreads), bytes, s, p);
+    hipLaunchKernelGGL((k_kv_join<MX, F32, D>), dim3(kShares<D> - 1, kCols / kJoinColumns), dim3(kThreads), 0, s, p);
     if constexpr (!F32) {
         // (offsets may give all rows to one sequence)
         const int64_t most = p.plan.offsets ? (int64_t)p.plan.rows * p.group : p.group;
@@ -992,7 +1096,7 @@ hipError_t run(const KvAttention& p, hipStream_t s) {
 
 size_t kv_attention_workspace_bytes(int64_t rows, int64_t seqs, int q_heads, int kv_heads, int dim, bool bf16) {
     if (rows == 0) return 0;
-    int64_t floats = 2 * kShares * (kCols * dim + 2 * kCols);
+    int64_t floats = 2 * (dim == 256 ? kShares<256> : kShares<128>) * (kCols * dim + 2 * kCols);
     const int group = q_heads / kv_heads;
     if (bf16 && rows * group > kFewColumns) {
         const int64_t cols = dim == 256 ? kPreCols<256> : kPreCols<128>;
