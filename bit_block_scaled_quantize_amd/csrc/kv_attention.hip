@@ -137,11 +137,17 @@ __device__ __forceinline__ void split8(const float v[8], typename Form<MX>::v8 o
 }
 
 // ---------------------------------------------------------------- the list of work
-// Sequence s has `columns` blocks of 16 columns and `tiles` tiles of keys from
-// first_tile (one at least, so that rows that see no key have a place where
-// they are written).
+// Sequence s has `columns` blocks of 16 columns for each kv head: segments of
+// `real` steps of keys from first_step (one at least, so that rows that see no
+// key have a place where they are written).  A segment counts kExtra units more
+// than that, about what its beginning and end cost, so that shares of many short
+// ones are no longer than those of a long one.
+// Where none has more than kShort steps and there are kManySegments of them at
+// least, each wave has whole segments of its own instead of a share.
+constexpr int kExtra = 4, kShort = 16, kManySegments = 512;
 struct Seq {
-    int row, rows, length, columns, first_tile, tiles;
+    int row, rows, length, columns, first_step, real;
+    __device__ __forceinline__ int64_t units() const { return (int64_t)real + kExtra; }
 };
 
 __device__ __forceinline__ Seq seq_of(const KvAttention& p, int s) {
@@ -151,13 +157,27 @@ __device__ __forceinline__ Seq seq_of(const KvAttention& p, int s) {
     const int64_t cols = (int64_t)q.rows * p.group;
     q.columns = p.bf16 && cols > kFewColumns ? 0 : (int)((cols + kCols - 1) / kCols);
     const int64_t low = p.window ? (int64_t)q.length - q.rows - p.window + 1 : 0;
-    q.first_tile = low > 0 ? (int)(low / kStep) : 0;
-    q.tiles = max(1, (q.length + kStep - 1) / kStep - q.first_tile);
+    q.first_step = low > 0 ? (int)(low / kStep) : 0;
+    q.real = max(1, (q.length + kStep - 1) / kStep - q.first_step);
     return q;
 }
 
 __device__ __forceinline__ int64_t units_of(const KvAttention& p, const Seq& q) {
-    return (int64_t)q.columns * q.tiles * p.cache.heads;
+    return q.columns * q.units() * p.cache.heads;
+}
+
+// The same, and whether any segment has more than kShort steps.
+__device__ __forceinline__ int64_t units_of(const KvAttention& p, const Seq& q, bool& longer) {
+    longer |= q.columns > 0 && q.real > kShort;
+    return units_of(p, q);
+}
+
+__device__ __forceinline__ int64_t segments_of(const KvAttention& p, const Seq& q) { return (int64_t)q.columns * p.cache.heads; }
+
+// a / b of numbers that are not negative (a 64-bit division takes some hundred
+// instructions).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
 // A lane's value in every lane.
@@ -186,36 +206,52 @@ __device__ __forceinline__ int64_t scan64(int64_t v) {
 }
 
 // A list of entries by sequence, `count(s)` of sequence s: the sum of all, and
-// the sequence of entry u (< sum) with the first entry of that sequence.  64
-// sequences at a time; the first 64 are counted once.
+// the sequence of entry u (< sum) with the first entry of that sequence.  A lane
+// counts 4 consecutive ones of 256, whose loads are under way together; the
+// first 256 are counted once.
 template <typename Count>
 struct List {
     Count count;
     int seqs;
-    int64_t own0, upto0, sum;
+    int64_t own0[4], upto0, sum;
     __device__ __forceinline__ List(int seqs_, Count c) : count(c), seqs(seqs_) {
-        own0 = lane_count(0);
-        upto0 = scan64(own0);
+        upto0 = scan64(lane_count(0, own0));
         sum = from_lane(upto0, 63);
-        for (int b = 64; b < seqs; b += 64) sum += from_lane(scan64(lane_count(b)), 63);
+        for (int b = 256; b < seqs; b += 256) {
+            int64_t own[4];
+            sum += from_lane(scan64(lane_count(b, own)), 63);
+        }
     }
-    __device__ __forceinline__ int64_t lane_count(int b) const {
-        const int s = b + (threadIdx.x & 63);
-        return s < seqs ? count(s) : 0;
+    __device__ __forceinline__ int64_t lane_count(int b, int64_t own[4]) const {
+        const int s = b + 4 * (threadIdx.x & 63);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // (counted without a branch: the last one's again past the end)
+            const int64_t n = count(min(s + i, seqs - 1));
+            own[i] = s + i < seqs ? n : 0;
+        }
+        return own[0] + own[1] + own[2] + own[3];
     }
     __device__ __forceinline__ int find(int64_t u, int64_t& first) const {
-        int64_t before = 0, own = own0, upto = upto0;
+        int64_t before = 0, upto = upto0, own[4] = {own0[0], own0[1], own0[2], own0[3]};
         for (int b = 0;;) {
             const int64_t all = from_lane(upto, 63);
             if (u < before + all) {
                 const int l = __builtin_ctzll(__ballot(u < before + upto));
-                first = before + from_lane(upto - own, l);
-                return b + l;
+                int s = b + 4 * l;
+                first = before + from_lane(upto - (own[0] + own[1] + own[2] + own[3]), l);
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                    const int64_t n = from_lane(own[i], l);
+                    if (s == b + 4 * l + i && u >= first + n) {
+                        first += n;
+                        ++s;
+                    }
+                }
+                return s;
             }
             before += all;
-            b += 64;
-            own = lane_count(b);
-            upto = scan64(own);
+            b += 256;
+            upto = scan64(lane_count(b, own));
         }
     }
 };
@@ -224,21 +260,26 @@ __device__ __forceinline__ List<Count> list_of(int seqs, Count c) {
     return List<Count>(seqs, c);
 }
 
-// Workgroups that take a share (three on each of 256 compute units, as many as
-// LDS holds of D 256): one for kLeast units at least.
-template <int D>
-constexpr int kShares = D == 256 ? 512 : 1024;
+// Workgroups that take a share (as many as 256 compute units hold at once by
+// their registers and LDS): one for kLeast units at least.
+template <bool F32, int D>
+constexpr int kShares = D == 256 ? 512 : F32 && D == 128 ? 768 : 1024;
 constexpr int kLeast = 2 * kWaves;
 
-template <int D>
-__device__ __forceinline__ int64_t shares_of(int64_t units) {
-    return max((int64_t)1, min((int64_t)kShares<D>, units / kLeast));
-}
-
-__device__ __forceinline__ int64_t share_begin(int64_t w, int64_t shares, int64_t units) {
-    const int64_t each = units / shares, rest = units % shares;
-    return w * each + min(w, rest);
-}
+// Where each share begins: the first `rest` of them have a unit more.
+struct Shares {
+    int64_t count, each, rest;
+    __device__ __forceinline__ Shares(int64_t units, int most) {
+        count = max((int64_t)1, min((int64_t)most, units / kLeast));
+        each = quotient(units, count);
+        rest = units - each * count;
+    }
+    __device__ __forceinline__ int64_t begin(int64_t w) const { return w * each + min(w, rest); }
+    __device__ __forceinline__ int64_t of(int64_t u) const {
+        const int64_t split = rest * (each + 1);
+        return u < split ? quotient(u, each + 1) : rest + quotient(u - split, each);
+    }
+};
 
 // Columns [first, first + count) of a segment are rows and heads of q: column c
 // is row c / group, head c % group of the kv head's.
@@ -247,14 +288,20 @@ struct Segment {
     int64_t begin, end;  // units
 };
 
-__device__ __forceinline__ Segment segment_at(const KvAttention& p, const Seq& q, int64_t seq_first, int64_t u) {
-    const int64_t at = (u - seq_first) / q.tiles;
+// Segment `index` of sequence q's.
+__device__ __forceinline__ Segment segment_of(const KvAttention& p, const Seq& q, int64_t index) {
     Segment g;
-    g.head = (int)(at / q.columns);
-    g.first = (int)(at % q.columns) * kCols;
+    g.head = (int)quotient(index, q.columns);
+    g.first = (int)(index - (int64_t)g.head * q.columns) * kCols;
     g.count = (int)min((int64_t)kCols, (int64_t)q.rows * p.group - g.first);
-    g.begin = seq_first + at * q.tiles;
-    g.end = g.begin + q.tiles;
+    return g;
+}
+
+__device__ __forceinline__ Segment segment_at(const KvAttention& p, const Seq& q, int64_t seq_first, int64_t u) {
+    const int64_t at = quotient(u - seq_first, q.units());
+    Segment g = segment_of(p, q, at);
+    g.begin = seq_first + at * q.units();
+    g.end = g.begin + q.units();
     return g;
 }
 
@@ -345,7 +392,7 @@ struct Step {
 };
 
 template <bool MX, bool F32, int D>
-__global__ void __launch_bounds__(kThreads, kShares<D> / 256) k_kv_attention(const KvAttention p) {
+__global__ void __launch_bounds__(kThreads, (kShares<F32, D> / 256)) k_kv_attention(const KvAttention p) {
     typedef Form<MX> F;
     typedef typename F::v8 v8;
     constexpr int QP = kQParts<MX, F32>, PP = kPParts<MX, F32>, KD = D / 32;
@@ -355,23 +402,51 @@ __global__ void __launch_bounds__(kThreads, kShares<D> / 256) k_kv_attention(con
     char* lds = kv_lds + wave * kWaveBytes<D>;
     __shared__ float stats[2][kWaves][kCols];
 
-    const auto list = list_of(p.plan.seqs, [&](int i) { return units_of(p, seq_of(p, i)); });
-    const int64_t units = list.sum, shares = shares_of<D>(units), me = blockIdx.x;
-    if (units == 0 || me >= shares) return;
-    int64_t u = share_begin(me, shares, units);
-    const int64_t u_end = share_begin(me + 1, shares, units);
-    int64_t seq_first;
-    int s = __builtin_amdgcn_readfirstlane(list.find(u, seq_first));
-    Seq q = seq_of(p, s);
+    bool longer = false;
+    const auto list = list_of(p.plan.seqs, [&](int i) { return units_of(p, seq_of(p, i), longer); });
+    if (list.sum == 0) return;
+    // units, or segments where each wave has its own
+    int64_t u = (int64_t)blockIdx.x * kWaves + wave, u_end = 0, seq_first = 0;
+    int s = -1;
+    Seq q;
+    const Shares shares(list.sum, kShares<F32, D>);
+    if (!__any(longer)) {
+        const auto segments = list_of(p.plan.seqs, [&](int i) { return segments_of(p, seq_of(p, i)); });
+        if (segments.sum >= kManySegments) {
+            u_end = segments.sum;
+            if (u < u_end) s = __builtin_amdgcn_readfirstlane(segments.find(u, seq_first));
+        }
+    }
+    const bool by_wave = u_end > 0;
+    if (!by_wave) {
+        if (blockIdx.x >= shares.count) return;
+        u = shares.begin(blockIdx.x);
+        u_end = shares.begin(blockIdx.x + 1);
+        s = __builtin_amdgcn_readfirstlane(list.find(u, seq_first));
+    }
+    if (u >= u_end) return;
+    q = seq_of(p, s);
     const int slot_mask = (1 << p.plan.page_shift) - 1;
+    const int stride = by_wave ? 1 : kWaves;
 
     while (u < u_end) {
-        while (u >= seq_first + units_of(p, q)) {
-            seq_first += units_of(p, q);
+        for (;;) {
+            const int64_t n = by_wave ? segments_of(p, q) : units_of(p, q);
+            if (u < seq_first + n) break;
+            seq_first += n;
             q = seq_of(p, ++s);
         }
-        const Segment g = segment_at(p, q, seq_first, u);
-        const int64_t stop = min(g.end, u_end);
+        const Segment g = by_wave ? segment_of(p, q, u - seq_first) : segment_at(p, q, seq_first, u);
+        // steps [from, to) of the segment's
+        int from = 0, to = q.real;
+        if (!by_wave) {
+            from = (int)min(u - g.begin, (int64_t)q.real);
+            to = (int)min(u_end - g.begin, (int64_t)q.real);
+            if (from > 0 && from >= to) {  // (an end that counts but has no steps)
+                u = g.end;
+                continue;
+            }
+        }
         // the lane's column
         const int c = g.first + min(col, g.count - 1);
         const int qrow = c / p.group, qhead = g.head * p.group + c % p.group;
@@ -384,8 +459,8 @@ __global__ void __launch_bounds__(kThreads, kShares<D> / 256) k_kv_attention(con
         const int low_last = p.window ? max(0, pos_last - p.window + 1) : 0;
 
         // steps of 32 keys that some column sees
-        const int j1 = min(q.first_tile + (int)(stop - g.begin), pos_last < 0 ? 0 : pos_last / kStep + 1);
-        int j = max(q.first_tile + (int)(u - g.begin), low_first / kStep) + wave;
+        const int j1 = min(q.first_step + to, pos_last < 0 ? 0 : pos_last / kStep + 1);
+        int j = max(q.first_step + from, low_first / kStep) + (by_wave ? 0 : wave);
 
         const auto find_page = [&](int at, int t) {
             const int k16 = at * kStep + 16 * t;
@@ -407,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, kShares<D> / 256) k_kv_attention(con
             page[t] = __builtin_amdgcn_readfirstlane(find_page(j, t));
             st.k[t] = load(j, t, page[t], p.cache.k_codes, p.cache.k_scales);
             st.v[t] = load(j, t, page[t], p.cache.v_codes, p.cache.v_scales);
-            next[t] = find_page(j + kWaves, t);
+            next[t] = find_page(j + stride, t);
         }
 
         // q, its row scaled into FP16's range
@@ -455,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, kShares<D> / 256) k_kv_attention(con
 
         // Codes are loaded again as soon as they are converted: the next step's
         // are under way while one is multiplied, and the pages of the one after.
-        for (; j < j1; j += kWaves) {
+        for (; j < j1; j += stride) {
             const int k32 = j * kStep;
             const bool holes[2] = {page[0] < 0, page[1] < 0};
 #pragma unroll
@@ -478,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, kShares<D> / 256) k_kv_attention(con
                 }
             }
 #pragma unroll
-            for (int t = 0; t < 2; ++t) st.k[t] = load(j + kWaves, t, page[t], p.cache.k_codes, p.cache.k_scales);
+            for (int t = 0; t < 2; ++t) st.k[t] = load(j + stride, t, page[t], p.cache.k_codes, p.cache.k_scales);
             // V to LDS
 #pragma unroll
             for (int t = 0; t < 2; ++t)
@@ -487,8 +562,8 @@ __global__ void __launch_bounds__(kThreads, kShares<D> / 256) k_kv_attention(con
                     *reinterpret_cast<v8*>(lds + (16 * t + col) * kRowBytes<D> + g4 * (D / 2) + 16 * i) = values8<D, MX>(st.v[t], i);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                st.v[t] = load(j + kWaves, t, page[t], p.cache.v_codes, p.cache.v_scales);
-                next[t] = find_page(j + 2 * kWaves, t);
+                st.v[t] = load(j + stride, t, page[t], p.cache.v_codes, p.cache.v_scales);
+                next[t] = find_page(j + 2 * stride, t);
             }
             __builtin_amdgcn_sched_barrier(0);
             if (k32 + kStep - 1 > pos_first || k32 < low_last || holes[0] || holes[1]) {
@@ -546,13 +621,25 @@ __global__ void __launch_bounds__(kThreads, kShares<D> / 256) k_kv_attention(con
             asm volatile("" ::: "memory");
         }
 
-        // the waves' sums, joined in order
         {
             float a, b;
             row_pair(l, a, b);
             half_pair(a + b, a, b);
             l = a + b;
         }
+        const float v_scale = MX ? 1.0f : p.cache.v_scale[g.head];
+        if (by_wave) {
+            if (col < g.count) {
+                const float f = l > 0.0f ? v_scale / l : 0.0f;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+                    store_out<F32>(p, q, g, col, 16 * i + 4 * g4, v4f_t{o[i][0] * f, o[i][1] * f, o[i][2] * f, o[i][3] * f});
+                if (p.lse && g4 == 0) store_lse(p, q, g, col, m, l);
+            }
+            u += (int64_t)gridDim.x * kWaves;
+            continue;
+        }
+        // the waves' sums, joined in order
         float* mine = reinterpret_cast<float*>(lds);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
@@ -562,9 +649,8 @@ __global__ void __launch_bounds__(kThreads, kShares<D> / 256) k_kv_attention(con
             stats[1][wave][col] = l;
         }
         __syncthreads();
-        const bool whole = u == g.begin && stop == g.end;
-        float* slot = slot_of<D>(p, me, u == g.begin ? 1 : 0);
-        const float v_scale = MX ? 1.0f : p.cache.v_scale[g.head];
+        const bool whole = from == 0 && to == q.real;
+        float* slot = slot_of<D>(p, blockIdx.x, from == 0 ? 1 : 0);
         for (int i = threadIdx.x; i < g.count * (D / 4); i += kThreads) {
             const int cc = i / (D / 4), d = 4 * (i % (D / 4));
             float top = kLowest;
@@ -596,88 +682,85 @@ __global__ void __launch_bounds__(kThreads, kShares<D> / 256) k_kv_attention(con
             }
         }
         __syncthreads();
-        u = stop;
+        u = g.end;
     }
 }
 
-// Workgroup (w - 1, y) joins columns 4 y and on of the segment that share w
-// begins inside of, where it is the first share that does.  The weights of up
-// to 64 shares are found by lane, a column to a wave; then D / 4 threads have a
-// column's elements, 256 / D of them a part of the shares each.
-constexpr int kJoinColumns = 4;
+// Workgroup w - 1 joins, of the segment whose steps share w begins among, an equal
+// part: as many workgroups do as the segment has such shares.  Of up to 16 parts a
+// thread adds an element's four by four, in order; of more a wave does, a part to
+// a lane.
 template <bool MX, bool F32, int D>
 __global__ void __launch_bounds__(kThreads) k_kv_join(const KvAttention p) {
-    constexpr int parts = 256 / D;
-    __shared__ float weight[kJoinColumns][64];
-    __shared__ v4f_t sums[kThreads];
-    const auto list = list_of(p.plan.seqs, [&](int i) { return units_of(p, seq_of(p, i)); });
-    const int64_t units = list.sum, shares = shares_of<D>(units), w = blockIdx.x + 1;
-    if (units == 0 || w >= shares) return;
-    const int64_t u = share_begin(w, shares, units);
+    bool longer = false;
+    const auto list = list_of(p.plan.seqs, [&](int i) { return units_of(p, seq_of(p, i), longer); });
+    if (list.sum == 0) return;
+    const Shares shares(list.sum, kShares<F32, D>);
+    const int64_t w = blockIdx.x + 1;
+    if (w >= shares.count) return;
+    if (!__any(longer) &&
+        list_of(p.plan.seqs, [&](int i) { return segments_of(p, seq_of(p, i)); }).sum >= kManySegments)
+        return;  // (none is split)
+    const int64_t u = shares.begin(w);
     int64_t seq_first;
     const Seq q = seq_of(p, list.find(u, seq_first));
     const Segment g = segment_at(p, q, seq_first, u);
-    const int c0 = blockIdx.y * kJoinColumns;
-    if (u == g.begin || share_begin(w - 1, shares, units) > g.begin || c0 >= g.count) return;
-    // shares w - 1 .. last have a part
-    int64_t last = w;
-    while (last + 1 < shares && share_begin(last + 1, shares, units) < g.end) ++last;
-    const int n = (int)(last - w + 2);
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int cc = c0 + threadIdx.x / (parts * (D / 4)), part = threadIdx.x / (D / 4) % parts, d = 4 * (threadIdx.x % (D / 4));
-    float top = kLowest, total = 0.0f;  // of the wave's column
-    v4f_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int b = 0; b < n; b += 64) {
-        const int most = min(64, n - b);
-        float m = kLowest, l = 0.0f;
-        if (lane < most) {
-            const float* slot = slot_of<D>(p, w - 1 + b + lane, b + lane == 0 ? 1 : 0) + kCols * D + min(c0 + wave, g.count - 1);
-            m = slot[0];
-            l = slot[kCols];
+    if (u == g.begin || u >= g.begin + q.real) return;
+    // shares first .. first + n - 1 have a part
+    const int64_t first = shares.of(g.begin);
+    const int n = (int)(shares.of(g.begin + q.real - 1) - first) + 1;
+    const auto part = [&](int k) { return slot_of<D>(p, first + k, k == 0 ? 1 : 0); };
+    const float v_scale = MX ? 1.0f : p.cache.v_scale[g.head];
+    const int items = g.count * (D / 4), rank = (int)(w - first - 1);
+    const int i0 = (int)((int64_t)items * rank / (n - 1)), i1 = (int)((int64_t)items * (rank + 1) / (n - 1));
+    if (n <= 16) {
+        for (int i = i0 + threadIdx.x; i < i1; i += kThreads) {
+            const int c = i / (D / 4), d = 4 * (i % (D / 4));
+            float top = kLowest, total = 0.0f;
+#pragma unroll 4
+            for (int k = 0; k < n; ++k) top = fmaxf(top, part(k)[kCols * D + c]);
+            v4f_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+            for (int k = 0; k < n; ++k) {
+                const float* x = part(k);
+                const float e = __builtin_amdgcn_exp2f(x[kCols * D + c] - top);
+                const v4f_t y = *reinterpret_cast<const v4f_t*>(x + c * D + d);
+                total += e * x[kCols * D + kCols + c];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) sum[r] += e * y[r];
+            }
+            const float f = total > 0.0f ? v_scale / total : 0.0f;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sum[r] *= f;
+            store_out<F32>(p, q, g, c, d, sum);
+            if (p.lse && d == 0) store_lse(p, q, g, c, top, total);
         }
-        const float next = fmaxf(top, reduce64(m, MaxOp())), f = __builtin_amdgcn_exp2f(top - next);
-        const float e = __builtin_amdgcn_exp2f(m - next);
-        total = total * f + reduce64(l * e, AddOp());
-        top = next;
-        if (b) {  // what is summed so far, to the new maximum
-            if (lane == 0) weight[wave][0] = f;
-            __syncthreads();
-            const float mine = weight[cc - c0][0];
+        return;
+    }
+    const int lane = threadIdx.x & 63;
+    for (int i = i0 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); i < i1; i += kWaves) {
+        const int c = i / (D / 4), d = 4 * (i % (D / 4));
+        float top = kLowest, total = 0.0f;
+        v4f_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int k = lane; k < n; k += 64) top = fmaxf(top, part(k)[kCols * D + c]);
+        top = reduce64(top, MaxOp());
+        for (int k = lane; k < n; k += 64) {
+            const float* x = part(k);
+            const float e = __builtin_amdgcn_exp2f(x[kCols * D + c] - top);
+            const v4f_t y = *reinterpret_cast<const v4f_t*>(x + c * D + d);
+            total += e * x[kCols * D + kCols + c];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) sum[r] *= mine;
-            __syncthreads();
+            for (int r = 0; r < 4; ++r) sum[r] += e * y[r];
         }
-        weight[wave][lane] = e;
-        __syncthreads();
-#pragma unroll 8
-        for (int k = part; k < most; k += parts) {
-            const float x = weight[cc - c0][k];
-            const v4f_t y = *reinterpret_cast<const v4f_t*>(slot_of<D>(p, w - 1 + b + k, b + k == 0 ? 1 : 0) +
-                                                            min(cc, g.count - 1) * D + d);
+        total = reduce64(total, AddOp());
+        const float f = total > 0.0f ? v_scale / total : 0.0f;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) sum[r] += x * y[r];
+        for (int r = 0; r < 4; ++r) sum[r] = reduce64(sum[r], AddOp()) * f;
+        if (lane == 0) {
+            store_out<F32>(p, q, g, c, d, sum);
+            if (p.lse && d == 0) store_lse(p, q, g, c, top, total);
         }
-        __syncthreads();
     }
-    if (lane == 0) {
-        weight[wave][0] = total;
-        weight[wave][1] = top;
-    }
-    sums[threadIdx.x] = sum;
-    __syncthreads();
-    if (part || cc >= g.count) return;
-#pragma unroll
-    for (int i = 1; i < parts; ++i) {
-        const v4f_t y = sums[threadIdx.x + i * (D / 4)];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) sum[r] += y[r];
-    }
-    total = weight[cc - c0][0];
-    const float f = total > 0.0f ? (MX ? 1.0f : p.cache.v_scale[g.head]) / total : 0.0f;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) sum[r] *= f;
-    store_out<F32>(p, q, g, cc, d, sum);
-    if (p.lse && d == 0) store_lse(p, q, g, cc, weight[cc - c0][1], total);
 }
 
 // ---------------------------------------------------------------- many rows
@@ -1063,7 +1146,7 @@ hipError_t run_prefill(KvAttention p, hipStream_t s) {
     constexpr int bytes = 2 * kPreBytes<D>;
     const int64_t blocks = pre_blocks_most(p.plan.rows, p.plan.seqs, p.group, D) * p.cache.heads;
     p.splits = pre_splits(p.plan.rows, p.plan.seqs, p.group, p.cache.heads, D);
-    p.pre_ws = p.ws + 2 * kShares<D> * kSlotFloats<D>;
+    p.pre_ws = p.ws + 2 * kShares<false, D> * kSlotFloats<D>;
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_kv_prefill<MX, D>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != hipSuccess) return e;
@@ -1082,8 +1165,8 @@ hipError_t run(const KvAttention& p, hipStream_t s) {
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((k_kv_attention<MX, F32, D>), dim3(kShares<D>), dim3(kThreads), bytes, s, p);
-    hipLaunchKernelGGL((k_kv_join<MX, F32, D>), dim3(kShares<D> - 1, kCols / kJoinColumns), dim3(kThreads), 0, s, p);
+    hipLaunchKernelGGL((k_kv_attention<MX, F32, D>), dim3(kShares<F32, D>), dim3(kThreads), bytes, s, p);
+    hipLaunchKernelGGL((k_kv_join<MX, F32, D>), dim3(kShares<F32, D> - 1), dim3(kThreads), 0, s, p);
     if constexpr (!F32) {
         // (offsets may give all rows to one sequence)
         const int64_t most = p.plan.offsets ? (int64_t)p.plan.rows * p.group : p.group;
@@ -1096,7 +1179,7 @@ hipError_t run(const KvAttention& p, hipStream_t s) {
 
 size_t kv_attention_workspace_bytes(int64_t rows, int64_t seqs, int q_heads, int kv_heads, int dim, bool bf16) {
     if (rows == 0) return 0;
-    int64_t floats = 2 * (dim == 256 ? kShares<256> : kShares<128>) * (kCols * dim + 2 * kCols);
+    int64_t floats = 2 * (dim == 256 ? kShares<false, 256> : dim == 128 && !bf16 ? kShares<true, 128> : kShares<false, 128>) * (kCols * dim + 2 * kCols);
     const int group = q_heads / kv_heads;
     if (bf16 && rows * group > kFewColumns) {
         const int64_t cols = dim == 256 ? kPreCols<256> : kPreCols<128>;
