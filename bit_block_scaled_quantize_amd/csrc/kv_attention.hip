@@ -139,15 +139,9 @@ __device__ __forceinline__ void split8(const float v[8], typename Form<MX>::v8 o
 // ---------------------------------------------------------------- the list of work
 // Sequence s has `columns` blocks of 16 columns for each kv head: segments of
 // `real` steps of keys from first_step (one at least, so that rows that see no
-// key have a place where they are written).  A segment counts kExtra units more
-// than that, about what its beginning and end cost, so that shares of many short
-// ones are no longer than those of a long one.
-// Where none has more than kShort steps and there are kManySegments of them at
-// least, each wave has whole segments of its own instead of a share.
-constexpr int kExtra = 4, kShort = 16, kManySegments = 512;
+// key have a place where they are written).
 struct Seq {
     int row, rows, length, columns, first_step, real;
-    __device__ __forceinline__ int64_t units() const { return (int64_t)real + kExtra; }
 };
 
 __device__ __forceinline__ Seq seq_of(const KvAttention& p, int s) {
@@ -161,18 +155,6 @@ __device__ __forceinline__ Seq seq_of(const KvAttention& p, int s) {
     q.real = max(1, (q.length + kStep - 1) / kStep - q.first_step);
     return q;
 }
-
-__device__ __forceinline__ int64_t units_of(const KvAttention& p, const Seq& q) {
-    return q.columns * q.units() * p.cache.heads;
-}
-
-// The same, and whether any segment has more than kShort steps.
-__device__ __forceinline__ int64_t units_of(const KvAttention& p, const Seq& q, bool& longer) {
-    longer |= q.columns > 0 && q.real > kShort;
-    return units_of(p, q);
-}
-
-__device__ __forceinline__ int64_t segments_of(const KvAttention& p, const Seq& q) { return (int64_t)q.columns * p.cache.heads; }
 
 // a / b of numbers that are not negative (a 64-bit division takes some hundred
 // instructions).
@@ -205,103 +187,168 @@ __device__ __forceinline__ int64_t scan64(int64_t v) {
     return v + (row == 0 ? 0 : row == 1 ? a : row == 2 ? b : c);
 }
 
-// A list of entries by sequence, `count(s)` of sequence s: the sum of all, and
-// the sequence of entry u (< sum) with the first entry of that sequence.  A lane
-// counts 4 consecutive ones of 256, whose loads are under way together; the
-// first 256 are counted once.
-template <typename Count>
-struct List {
-    Count count;
-    int seqs;
-    int64_t own0[4], upto0, sum;
-    __device__ __forceinline__ List(int seqs_, Count c) : count(c), seqs(seqs_) {
-        upto0 = scan64(lane_count(0, own0));
-        sum = from_lane(upto0, 63);
-        for (int b = 256; b < seqs; b += 256) {
-            int64_t own[4];
-            sum += from_lane(scan64(lane_count(b, own)), 63);
-        }
-    }
-    __device__ __forceinline__ int64_t lane_count(int b, int64_t own[4]) const {
+// Sum over the lanes.
+__device__ __forceinline__ int64_t sum64(int64_t v) {
+    v += row_below<1>(v);
+    v += row_below<2>(v);
+    v += row_below<4>(v);
+    v += row_below<8>(v);
+    return from_lane(v, 15) + from_lane(v, 31) + from_lane(v, 47) + from_lane(v, 63);
+}
+
+// Steps and segments of 256 sequences, 4 consecutive ones to a lane, whose loads
+// are under way together.
+struct Quad {
+    int real[4], segs[4];
+    __device__ __forceinline__ Quad(const KvAttention& p, int b) {
         const int s = b + 4 * (threadIdx.x & 63);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {  // (counted without a branch: the last one's again past the end)
-            const int64_t n = count(min(s + i, seqs - 1));
-            own[i] = s + i < seqs ? n : 0;
+        for (int i = 0; i < 4; ++i) {  // (without a branch: past the end the last one's again)
+            const Seq q = seq_of(p, min(s + i, p.plan.seqs - 1));
+            real[i] = q.real;
+            segs[i] = s + i < p.plan.seqs ? q.columns * p.cache.heads : 0;
         }
-        return own[0] + own[1] + own[2] + own[3];
+    }
+};
+
+// The list of entries by sequence, count(real, segs) of each: the sum of all, and
+// the sequence of entry u (< sum) with the first entry of that sequence.  The first
+// 256 sequences are loaded once.
+template <typename Count>
+struct List {
+    const KvAttention& p;
+    const Quad& first256;
+    Count count;
+    int64_t upto0, sum;
+    __device__ __forceinline__ List(const KvAttention& p_, const Quad& q, Count c) : p(p_), first256(q), count(c) {
+        upto0 = scan64(all_of(q));
+        sum = from_lane(upto0, 63);
+        for (int b = 256; b < p.plan.seqs; b += 256) sum += from_lane(scan64(all_of(Quad(p, b))), 63);
+    }
+    __device__ __forceinline__ int64_t all_of(const Quad& q) const {
+        return count(q.real[0], q.segs[0]) + count(q.real[1], q.segs[1]) + count(q.real[2], q.segs[2]) +
+               count(q.real[3], q.segs[3]);
     }
     __device__ __forceinline__ int find(int64_t u, int64_t& first) const {
-        int64_t before = 0, upto = upto0, own[4] = {own0[0], own0[1], own0[2], own0[3]};
+        int64_t before = 0, upto = upto0;
+        Quad q = first256;
         for (int b = 0;;) {
             const int64_t all = from_lane(upto, 63);
             if (u < before + all) {
                 const int l = __builtin_ctzll(__ballot(u < before + upto));
                 int s = b + 4 * l;
-                first = before + from_lane(upto - (own[0] + own[1] + own[2] + own[3]), l);
+                first = before + from_lane(upto - all_of(q), l);
 #pragma unroll
                 for (int i = 0; i < 3; ++i) {
-                    const int64_t n = from_lane(own[i], l);
+                    const int64_t n = from_lane(count(q.real[i], q.segs[i]), l);
                     if (s == b + 4 * l + i && u >= first + n) {
                         first += n;
                         ++s;
                     }
                 }
-                return s;
+                return __builtin_amdgcn_readfirstlane(s);
             }
             before += all;
             b += 256;
-            upto = scan64(lane_count(b, own));
+            q = Quad(p, b);
+            upto = scan64(all_of(q));
         }
     }
 };
 template <typename Count>
-__device__ __forceinline__ List<Count> list_of(int seqs, Count c) {
-    return List<Count>(seqs, c);
+__device__ __forceinline__ List<Count> list_of(const KvAttention& p, const Quad& q, Count c) {
+    return List<Count>(p, q, c);
 }
 
-// Workgroups that take a share (as many as 256 compute units hold at once by
-// their registers and LDS): one for kLeast units at least.
+// Workgroups (as many as 256 compute units hold at once by their registers and
+// LDS).
 template <bool F32, int D>
 constexpr int kShares = D == 256 ? 512 : F32 && D == 128 ? 768 : 1024;
-constexpr int kLeast = 2 * kWaves;
 
-// Where each share begins: the first `rest` of them have a unit more.
-struct Shares {
-    int64_t count, each, rest;
-    __device__ __forceinline__ Shares(int64_t units, int most) {
-        count = max((int64_t)1, min((int64_t)most, units / kLeast));
-        each = quotient(units, count);
-        rest = units - each * count;
-    }
+// How the segments are divided, by what they are on the device:
+//   by wave    no segment has more than kShort steps, and there are kManySegments
+//              at least: each wave has whole segments of its own;
+//   in parts   of `part` steps (kLeast at least), as many as there are workgroups
+//              or fewer, if that takes no more than kMostPart steps: a workgroup
+//              has one part;
+//   in shares  else: every workgroup has an equal share of the list of all steps,
+//              whose first and last may lie inside segments.  A segment counts
+//              kExtra steps more than it has, about what its beginning and end
+//              cost.
+// (Parts end with their segment where shares would have a second one to begin,
+// which costs some 5 us; many steps are better divided evenly.)
+constexpr int kShort = 16, kManySegments = 512, kLeast = 2 * kWaves, kMostPart = 32, kExtra = 4;
+struct Division {
+    bool by_wave;
+    int part;           // 0: in shares
+    int64_t sum;        // segments, parts or units of the list
+    int64_t each, rest; // shares: the first `rest` have a unit more
+    int64_t shares;
     __device__ __forceinline__ int64_t begin(int64_t w) const { return w * each + min(w, rest); }
-    __device__ __forceinline__ int64_t of(int64_t u) const {
+    __device__ __forceinline__ int64_t share_of(int64_t u) const {
         const int64_t split = rest * (each + 1);
         return u < split ? quotient(u, each + 1) : rest + quotient(u - split, each);
     }
+    // entries of a sequence
+    __device__ __forceinline__ int64_t operator()(int real, int segs) const {
+        return by_wave ? segs : part ? (int64_t)segs * ((uint32_t)(real + part - 1) / (uint32_t)part)
+                                     : segs * ((int64_t)real + kExtra);
+    }
 };
 
-// Columns [first, first + count) of a segment are rows and heads of q: column c
-// is row c / group, head c % group of the kv head's.
-struct Segment {
-    int head, first, count;
-    int64_t begin, end;  // units
-};
-
-// Segment `index` of sequence q's.
-__device__ __forceinline__ Segment segment_of(const KvAttention& p, const Seq& q, int64_t index) {
-    Segment g;
-    g.head = (int)quotient(index, q.columns);
-    g.first = (int)(index - (int64_t)g.head * q.columns) * kCols;
-    g.count = (int)min((int64_t)kCols, (int64_t)q.rows * p.group - g.first);
-    return g;
+__device__ __forceinline__ Division divide(const KvAttention& p, const Quad& first256, int most) {
+    bool longer = false;
+    int64_t steps = 0, segments = 0;
+    for (int b = 0; b < p.plan.seqs; b += 256) {
+        const Quad q = b ? Quad(p, b) : first256;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            longer |= q.segs[i] > 0 && q.real[i] > kShort;
+            steps += (int64_t)q.real[i] * q.segs[i];
+            segments += q.segs[i];
+        }
+    }
+    steps = sum64(steps);
+    segments = sum64(segments);
+    Division d = {};
+    d.by_wave = !__any(longer) && segments >= kManySegments;
+    if (d.by_wave || segments == 0) {
+        d.sum = segments;
+        return d;
+    }
+    if (segments <= most) {
+        int64_t part = max((int64_t)kLeast, quotient(steps + most - 1, most));
+        for (; part <= kMostPart; part += part / 4) {
+            d.part = (int)part;
+            d.sum = list_of(p, first256, d).sum;
+            if (d.sum <= most) return d;
+        }
+        d.part = 0;
+    }
+    d.sum = steps + kExtra * segments;
+    d.shares = max((int64_t)1, min((int64_t)most, quotient(d.sum, kLeast)));
+    d.each = quotient(d.sum, d.shares);
+    d.rest = d.sum - d.each * d.shares;
+    return d;
 }
 
-__device__ __forceinline__ Segment segment_at(const KvAttention& p, const Seq& q, int64_t seq_first, int64_t u) {
-    const int64_t at = quotient(u - seq_first, q.units());
-    Segment g = segment_of(p, q, at);
-    g.begin = seq_first + at * q.units();
-    g.end = g.begin + q.units();
+// Columns [first, first + count) of a segment are rows and heads of q: column c
+// is row c / group, head c % group of the kv head's.  Its entries of the list are
+// `begin` and on.
+struct Segment {
+    int head, first, count;
+    int64_t begin, entries;
+};
+
+__device__ __forceinline__ Segment segment_at(const KvAttention& p, const Division& d, const Seq& q, int64_t seq_first,
+                                              int64_t u) {
+    Segment g;
+    g.entries = d(q.real, 1);
+    const int64_t at = quotient(u - seq_first, g.entries);
+    g.begin = seq_first + at * g.entries;
+    g.head = (int)quotient(at, q.columns);
+    g.first = (int)(at - (int64_t)g.head * q.columns) * kCols;
+    g.count = (int)min((int64_t)kCols, (int64_t)q.rows * p.group - g.first);
     return g;
 }
 
@@ -311,8 +358,8 @@ __device__ __forceinline__ Segment segment_at(const KvAttention& p, const Seq& q
 template <int D>
 constexpr int kSlotFloats = kCols * D + 2 * kCols;
 
-// The two slots of share w: of a segment that an earlier share began (0), and
-// of one that it begins and does not end (1).
+// Two slots for a workgroup: of a segment that an earlier one began (0), and of one
+// that it begins and does not end (1).
 template <int D>
 __device__ __forceinline__ float* slot_of(const KvAttention& p, int64_t w, int which) {
     return p.ws + (2 * w + which) * kSlotFloats<D>;
@@ -402,48 +449,40 @@ __global__ void __launch_bounds__(kThreads, (kShares<F32, D> / 256)) k_kv_attent
     char* lds = kv_lds + wave * kWaveBytes<D>;
     __shared__ float stats[2][kWaves][kCols];
 
-    bool longer = false;
-    const auto list = list_of(p.plan.seqs, [&](int i) { return units_of(p, seq_of(p, i), longer); });
-    if (list.sum == 0) return;
-    // units, or segments where each wave has its own
-    int64_t u = (int64_t)blockIdx.x * kWaves + wave, u_end = 0, seq_first = 0;
-    int s = -1;
-    Seq q;
-    const Shares shares(list.sum, kShares<F32, D>);
-    if (!__any(longer)) {
-        const auto segments = list_of(p.plan.seqs, [&](int i) { return segments_of(p, seq_of(p, i)); });
-        if (segments.sum >= kManySegments) {
-            u_end = segments.sum;
-            if (u < u_end) s = __builtin_amdgcn_readfirstlane(segments.find(u, seq_first));
-        }
-    }
-    const bool by_wave = u_end > 0;
-    if (!by_wave) {
-        if (blockIdx.x >= shares.count) return;
-        u = shares.begin(blockIdx.x);
-        u_end = shares.begin(blockIdx.x + 1);
-        s = __builtin_amdgcn_readfirstlane(list.find(u, seq_first));
+    const Quad first256(p, 0);
+    const Division d = divide(p, first256, kShares<F32, D>);
+    int64_t u = d.by_wave ? (int64_t)blockIdx.x * kWaves + wave : blockIdx.x, u_end = d.sum;
+    if (!d.by_wave && !d.part) {
+        if (u >= d.shares) return;
+        u_end = d.begin(u + 1);
+        u = d.begin(u);
     }
     if (u >= u_end) return;
-    q = seq_of(p, s);
+    int64_t seq_first;
+    int s = list_of(p, first256, d).find(u, seq_first);
+    Seq q = seq_of(p, s);
     const int slot_mask = (1 << p.plan.page_shift) - 1;
-    const int stride = by_wave ? 1 : kWaves;
+    const int stride = d.by_wave ? 1 : kWaves;
 
     while (u < u_end) {
         for (;;) {
-            const int64_t n = by_wave ? segments_of(p, q) : units_of(p, q);
+            const int64_t n = d(q.real, q.columns * p.cache.heads);
             if (u < seq_first + n) break;
             seq_first += n;
             q = seq_of(p, ++s);
         }
-        const Segment g = by_wave ? segment_of(p, q, u - seq_first) : segment_at(p, q, seq_first, u);
+        const Segment g = segment_at(p, d, q, seq_first, u);
         // steps [from, to) of the segment's
         int from = 0, to = q.real;
-        if (!by_wave) {
+        if (d.part) {
+            from = (int)(u - g.begin) * d.part;
+            to = min(q.real, from + d.part);
+            u_end = 0;
+        } else if (!d.by_wave) {
             from = (int)min(u - g.begin, (int64_t)q.real);
             to = (int)min(u_end - g.begin, (int64_t)q.real);
             if (from > 0 && from >= to) {  // (an end that counts but has no steps)
-                u = g.end;
+                u = g.begin + g.entries;
                 continue;
             }
         }
@@ -460,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, (kShares<F32, D> / 256)) k_kv_attent
 
         // steps of 32 keys that some column sees
         const int j1 = min(q.first_step + to, pos_last < 0 ? 0 : pos_last / kStep + 1);
-        int j = max(q.first_step + from, low_first / kStep) + (by_wave ? 0 : wave);
+        int j = max(q.first_step + from, low_first / kStep) + (d.by_wave ? 0 : wave);
 
         const auto find_page = [&](int at, int t) {
             const int k16 = at * kStep + 16 * t;
@@ -628,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, (kShares<F32, D> / 256)) k_kv_attent
             l = a + b;
         }
         const float v_scale = MX ? 1.0f : p.cache.v_scale[g.head];
-        if (by_wave) {
+        if (d.by_wave) {
             if (col < g.count) {
                 const float f = l > 0.0f ? v_scale / l : 0.0f;
 #pragma unroll
@@ -682,85 +721,77 @@ __global__ void __launch_bounds__(kThreads, (kShares<F32, D> / 256)) k_kv_attent
             }
         }
         __syncthreads();
-        u = g.end;
+        u = g.begin + g.entries;
     }
 }
 
-// Workgroup w - 1 joins, of the segment whose steps share w begins among, an equal
-// part: as many workgroups do as the segment has such shares.  Of up to 16 parts a
-// thread adds an element's four by four, in order; of more a wave does, a part to
-// a lane.
+// LANES lanes add four elements of the n parts, a part in turn to a lane; items
+// [i0, i1) of a segment's count x D / 4.
+template <int LANES, typename Op>
+__device__ __forceinline__ float reduce_lanes(float x, Op op) {
+    if constexpr (LANES == 64) return reduce64(x, op);
+    if constexpr (LANES == 16) return reduce16(x, op);
+    if constexpr (LANES >= 2) x = op(x, lane_xor1(x));
+    if constexpr (LANES == 4) x = op(x, lane_xor2(x));
+    return x;
+}
+
+template <bool F32, int D, int LANES, typename Part>
+__device__ __forceinline__ void join_items(const KvAttention& p, const Seq& q, const Segment& g, float v_scale, int i0, int i1,
+                                           int n, Part part) {
+    const int at = threadIdx.x / LANES, k0 = threadIdx.x % LANES;
+    for (int b = i0; b < i1; b += kThreads / LANES) {  // (the same in all lanes)
+        const int i = min(b + at, i1 - 1), c = i / (D / 4), d = 4 * (i % (D / 4));
+        float top = kLowest, total = 0.0f;
+        v4f_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+        for (int k = k0; k < n; k += LANES) {
+            const float* x = part(k);
+            const float m = x[kCols * D + c], l = x[kCols * D + kCols + c];
+            const v4f_t y = *reinterpret_cast<const v4f_t*>(x + c * D + d);
+            const float next = fmaxf(top, m), f = __builtin_amdgcn_exp2f(top - next), e = __builtin_amdgcn_exp2f(m - next);
+            total = total * f + l * e;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sum[r] = sum[r] * f + y[r] * e;
+            top = next;
+        }
+        const float most = reduce_lanes<LANES>(top, MaxOp()), e = __builtin_amdgcn_exp2f(top - most);
+        total = reduce_lanes<LANES>(total * e, AddOp());
+        const float f = total > 0.0f ? v_scale / total : 0.0f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sum[r] = reduce_lanes<LANES>(sum[r] * e, AddOp()) * f;
+        if (k0 == 0 && b + at < i1) {
+            store_out<F32>(p, q, g, c, d, sum);
+            if (p.lse && d == 0) store_lse(p, q, g, c, most, total);
+        }
+    }
+}
+
+// Workgroup w - 1 joins an equal part of the segment that workgroup w of
+// k_kv_attention has a later part of: as many do as have one.
 template <bool MX, bool F32, int D>
 __global__ void __launch_bounds__(kThreads) k_kv_join(const KvAttention p) {
-    bool longer = false;
-    const auto list = list_of(p.plan.seqs, [&](int i) { return units_of(p, seq_of(p, i), longer); });
-    if (list.sum == 0) return;
-    const Shares shares(list.sum, kShares<F32, D>);
+    const Quad first256(p, 0);
+    const Division d = divide(p, first256, kShares<F32, D>);
     const int64_t w = blockIdx.x + 1;
-    if (w >= shares.count) return;
-    if (!__any(longer) &&
-        list_of(p.plan.seqs, [&](int i) { return segments_of(p, seq_of(p, i)); }).sum >= kManySegments)
-        return;  // (none is split)
-    const int64_t u = shares.begin(w);
+    if (d.by_wave || w >= (d.part ? d.sum : d.shares)) return;
+    const int64_t u = d.part ? w : d.begin(w);
     int64_t seq_first;
-    const Seq q = seq_of(p, list.find(u, seq_first));
-    const Segment g = segment_at(p, q, seq_first, u);
-    if (u == g.begin || u >= g.begin + q.real) return;
-    // shares first .. first + n - 1 have a part
-    const int64_t first = shares.of(g.begin);
-    const int n = (int)(shares.of(g.begin + q.real - 1) - first) + 1;
+    const Seq q = seq_of(p, list_of(p, first256, d).find(u, seq_first));
+    const Segment g = segment_at(p, d, q, seq_first, u);
+    if (u == g.begin || (!d.part && u >= g.begin + q.real)) return;
+    // workgroups first .. first + n - 1 have a part
+    const int64_t first = d.part ? g.begin : d.share_of(g.begin);
+    const int n = d.part ? (int)g.entries : (int)(d.share_of(g.begin + q.real - 1) - first) + 1;
     const auto part = [&](int k) { return slot_of<D>(p, first + k, k == 0 ? 1 : 0); };
     const float v_scale = MX ? 1.0f : p.cache.v_scale[g.head];
     const int items = g.count * (D / 4), rank = (int)(w - first - 1);
     const int i0 = (int)((int64_t)items * rank / (n - 1)), i1 = (int)((int64_t)items * (rank + 1) / (n - 1));
-    if (n <= 16) {
-        for (int i = i0 + threadIdx.x; i < i1; i += kThreads) {
-            const int c = i / (D / 4), d = 4 * (i % (D / 4));
-            float top = kLowest, total = 0.0f;
-#pragma unroll 4
-            for (int k = 0; k < n; ++k) top = fmaxf(top, part(k)[kCols * D + c]);
-            v4f_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-            for (int k = 0; k < n; ++k) {
-                const float* x = part(k);
-                const float e = __builtin_amdgcn_exp2f(x[kCols * D + c] - top);
-                const v4f_t y = *reinterpret_cast<const v4f_t*>(x + c * D + d);
-                total += e * x[kCols * D + kCols + c];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) sum[r] += e * y[r];
-            }
-            const float f = total > 0.0f ? v_scale / total : 0.0f;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) sum[r] *= f;
-            store_out<F32>(p, q, g, c, d, sum);
-            if (p.lse && d == 0) store_lse(p, q, g, c, top, total);
-        }
-        return;
-    }
-    const int lane = threadIdx.x & 63;
-    for (int i = i0 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); i < i1; i += kWaves) {
-        const int c = i / (D / 4), d = 4 * (i % (D / 4));
-        float top = kLowest, total = 0.0f;
-        v4f_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int k = lane; k < n; k += 64) top = fmaxf(top, part(k)[kCols * D + c]);
-        top = reduce64(top, MaxOp());
-        for (int k = lane; k < n; k += 64) {
-            const float* x = part(k);
-            const float e = __builtin_amdgcn_exp2f(x[kCols * D + c] - top);
-            const v4f_t y = *reinterpret_cast<const v4f_t*>(x + c * D + d);
-            total += e * x[kCols * D + kCols + c];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) sum[r] += e * y[r];
-        }
-        total = reduce64(total, AddOp());
-        const float f = total > 0.0f ? v_scale / total : 0.0f;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) sum[r] = reduce64(sum[r], AddOp()) * f;
-        if (lane == 0) {
-            store_out<F32>(p, q, g, c, d, sum);
-            if (p.lse && d == 0) store_lse(p, q, g, c, top, total);
-        }
-    }
+    // (lanes for all items at once, but no more than have a part)
+    if (n < 4 || i1 - i0 > 128) join_items<F32, D, 1>(p, q, g, v_scale, i0, i1, n, part);
+    else if (n < 16 || i1 - i0 > 32) join_items<F32, D, 4>(p, q, g, v_scale, i0, i1, n, part);
+    else if (n < 64 || i1 - i0 > 8) join_items<F32, D, 16>(p, q, g, v_scale, i0, i1, n, part);
+    else join_items<F32, D, 64>(p, q, g, v_scale, i0, i1, n, part);
 }
 
 // ---------------------------------------------------------------- many rows
@@ -804,13 +835,22 @@ __device__ __forceinline__ int pre_blocks(const KvAttention& p, int s) {
 // sequence and number there; false past the end.
 template <int D>
 __device__ __forceinline__ bool pre_find(const KvAttention& p, int64_t index, int& s, int& block) {
-    const auto list = list_of(p.plan.seqs, [&](int i) { return (int64_t)pre_blocks<D>(p, i); });
-    if (index >= list.sum) return false;
-    index = list.sum - 1 - index;
-    int64_t first;
-    s = __builtin_amdgcn_readfirstlane(list.find(index, first));
-    block = __builtin_amdgcn_readfirstlane((int)(index - first));
-    return true;
+    const int lane = threadIdx.x & 63;
+    const auto blocks = [&](int b) { return b + lane < p.plan.seqs ? (int64_t)pre_blocks<D>(p, b + lane) : 0; };
+    int64_t all = 0;
+    for (int b = 0; b < p.plan.seqs; b += 64) all += from_lane(scan64(blocks(b)), 63);
+    if (index >= all) return false;
+    index = all - 1 - index;
+    for (int b = 0;; b += 64) {
+        const int64_t own = blocks(b), upto = scan64(own), sum = from_lane(upto, 63);
+        if (index < sum) {
+            const int l = __builtin_ctzll(__ballot(index < upto));
+            s = __builtin_amdgcn_readfirstlane(b + l);
+            block = __builtin_amdgcn_readfirstlane((int)(index - from_lane(upto - own, l)));
+            return true;
+        }
+        index -= sum;
+    }
 }
 
 // What workgroup `id` of k_kv_prefill does: columns of a kv head (neighbouring
@@ -818,8 +858,8 @@ __device__ __forceinline__ bool pre_find(const KvAttention& p, int64_t index, in
 // in one XCD's L2) and the split-th part of its tiles.
 struct PreWork {
     Seq q;
-    Segment g;  // (begin, end: tiles of keys)
-    int s, split;
+    Segment g;
+    int s, split, from, to;  // tiles of keys
     int64_t slot;  // of the workspace
 };
 
@@ -840,8 +880,8 @@ __device__ __forceinline__ bool pre_work(const KvAttention& p, int64_t id, PreWo
     const int low = p.window ? max(0, first - p.window + 1) / kTile : 0;
     const int tiles = last >= 0 ? last / kTile + 1 - low : 0;
     const int each = (tiles + p.splits - 1) / p.splits;
-    w.g.begin = low + min(tiles, w.split * each);
-    w.g.end = low + min(tiles, (w.split + 1) * each);
+    w.from = low + min(tiles, w.split * each);
+    w.to = low + min(tiles, (w.split + 1) * each);
     return true;
 }
 
@@ -911,7 +951,7 @@ __global__ void __launch_bounds__(64 * kPreWaves<D>, kPreWaves<D> / 4) k_kv_pref
     } rk, rv;
     int page_next;
     const int slot_mask = (1 << p.plan.page_shift) - 1;
-    const int j0 = (int)g.begin, j1 = (int)g.end;
+    const int j0 = work.from, j1 = work.to;
     const auto find_page = [&](int j) {
         const int key = j * kTile + lkey;
         return j < j1 && key < q.length ? kv_page(p.plan, p.cache.pages, work.s, key) : -1;
