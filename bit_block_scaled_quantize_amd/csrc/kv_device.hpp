@@ -35,29 +35,42 @@ __device__ __forceinline__ int kv_page(const KvPlan& p, int pages, int s, int po
     return (uint32_t)page < (uint32_t)pages ? page : -1;
 }
 
-// Sequence and position of row t (the same in every lane of the wave); false for
-// a row that belongs to no sequence.  64 offsets are compared at a time: the
-// sequence is the number of offsets[1 ...] that are <= t.
-__device__ __forceinline__ bool kv_place(const KvPlan& p, int t, int& s, int& pos) {
-    if (!p.offsets) {
-        s = t;
-    } else {
-        if (t < p.offsets[0]) return false;
-        const int lane = threadIdx.x & 63;
+// Where rows t0 .. t0 + n - 1 (n <= 64) lie: lane r has row t0 + r's position and
+// page.
+struct KvPlaces {
+    int pos;   // kNoRow: a row that belongs to no sequence
+    int page;  // -1: none
+};
+constexpr int kNoRow = -0x7FFFFFFF - 1;
+
+// A row's sequence is the number of offsets[1 ...] that are <= it; 64 offsets are
+// compared at a time.
+__device__ __forceinline__ KvPlaces kv_places(const KvPlan& p, int pages, int t0, int n) {
+    const int lane = threadIdx.x & 63, t = t0 + lane;
+    KvPlaces w = {kNoRow, -1};
+    int s = t;
+    if (p.offsets) {
         s = 0;
         for (int b = 0; b < p.seqs; b += 64) {
-            const int c = __popcll(__ballot(b + lane < p.seqs && p.offsets[b + lane + 1] <= t));
-            s += c;
-            if (c < 64) break;
+            const int end = b + lane < p.seqs ? p.offsets[b + lane + 1] : 0x7FFFFFFF;
+            int more = 0;
+            for (int r = 0; r < n; ++r) {
+                const int c = __popcll(__ballot(end <= t0 + r));
+                if (lane == r) s += c;
+                more = c;  // (of the last row)
+            }
+            if (more < 64) break;
         }
-        s = __builtin_amdgcn_readfirstlane(s);
-        if (s >= p.seqs) return false;
     }
-    int first, n;
-    kv_rows(p, s, first, n);
-    if (t < first || t - first >= n) return false;  // (offsets out of order)
-    pos = kv_length(p, s) - n + (t - first);
-    return true;
+    if (lane < n && s < p.seqs && (!p.offsets || t >= p.offsets[0])) {
+        int first, count;
+        kv_rows(p, s, first, count);
+        if (t >= first && t - first < count) {  // (not so where offsets are out of order)
+            w.pos = kv_length(p, s) - count + (t - first);
+            if (w.pos >= 0) w.page = kv_page(p, pages, s, w.pos);
+        }
+    }
+    return w;
 }
 
 // E8M0 byte as binary32: 2^(b - 127) (b = 0: a subnormal number).

@@ -243,15 +243,17 @@ struct KvAppend {
     const float* rope;
     int64_t rope_ld;
     int rope_rows, rot;  // no rotation: INT32_MAX, 0
+    int rows_each, chunks_each;  // of a wave; set by the launcher
 };
-hipError_t launch_kv_append(const KvAppend& p, hipStream_t s);
+hipError_t launch_kv_append(KvAppend p, hipStream_t s);
 struct KvGather {
     KvCache cache;
     KvPlan plan;
     KvRows k, v;
     bool bf16;
+    int rows_each, chunks_each;  // of a wave; set by the launcher
 };
-hipError_t launch_kv_gather(const KvGather& p, hipStream_t s);
+hipError_t launch_kv_gather(KvGather p, hipStream_t s);
 
 // Attention over the cache (see nvfp4_kv_attention).
 struct KvAttention {

@@ -723,7 +723,7 @@ nvfp4_status nvfp4_kv_gather(const nvfp4_kv_cache* cache, const nvfp4_kv_plan* p
     if (st == NVFP4_OK) st = check_heads(v, plan->rows, cache->kv_heads, cache->head_dim, dt, true);
     if (st != NVFP4_OK) return st;
     if (cache->kv_heads > 0x1FFFFFFF) return NVFP4_ERR_UNSUPPORTED;
-    const KvGather g = {kv_cache_of(cache), kv_plan_of(cache, plan), kv_rows_of(k), kv_rows_of(v), dt == NVFP4_BF16};
+    const KvGather g = {kv_cache_of(cache), kv_plan_of(cache, plan), kv_rows_of(k), kv_rows_of(v), dt == NVFP4_BF16, 0, 0};
     return launch_kv_gather(g, static_cast<hipStream_t>(stream)) == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
 }
 
