@@ -106,6 +106,17 @@ __device__ __forceinline__ bool share_of_wave(int rows, int chunks, int rows_eac
     return true;
 }
 
+// A row and a chunk of a wave's share, in order.
+struct Cursor {
+    int r, c;
+    __device__ __forceinline__ void next(const Share& w) {
+        if (++c == w.c1) {
+            c = w.c0;
+            ++r;
+        }
+    }
+};
+
 // A lane has the 8 elements from a and the 8 from b of its head: consecutive
 // ones, but in the part of a head that is rotated in halves, pairs that lie
 // rot / 2 apart.  A block's largest magnitude is then that of the lane's own
@@ -149,6 +160,7 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(const KvAppend p) {
             float x[8], y[8];
             unpack_raw(now, 0, x);
             unpack_raw(now, 1, y);
+            // (two ahead, 15047 rows of 72 heads took 119 us instead of 114)
             if (c + 1 < w.c1) now = load(r, c + 1);
             else if (r + 1 < w.n) now = load(r + 1, w.c0);
             if (pos == kNoRow) continue;
@@ -220,9 +232,12 @@ __global__ void __launch_bounds__(kThreads) k_kv_gather(const KvGather p) {
         uint2 w;
         uint32_t byte;
     };
-    const auto load = [&](int r, int c) {
+    Cursor ahead = {0, w.c0};
+    const auto load = [&]() {
         Held v = {{0u, 0u}, 0u};
+        const int r = min(ahead.r, 63), c = ahead.c;  // (lanes past the last row have no page)
         const int pos = __builtin_amdgcn_readlane(places.pos, r), page = __builtin_amdgcn_readlane(places.page, r);
+        ahead.next(w);
         if (page >= 0) {
             const int hd = min(c * kHeads + lane / kLanes, heads - 1);
             const bool is_k = hd < p.cache.heads;
@@ -234,24 +249,29 @@ __global__ void __launch_bounds__(kThreads) k_kv_gather(const KvGather p) {
         }
         return v;
     };
-    Held now = load(0, w.c0);
-    for (int r = 0; r < w.n; ++r) {
-        const int t = w.t0 + r, pos = __builtin_amdgcn_readlane(places.pos, r), page = __builtin_amdgcn_readlane(places.page, r);
-        for (int c = w.c0; c < w.c1; ++c) {
-            const Held held = now;
-            if (c + 1 < w.c1) now = load(r, c + 1);
-            else if (r + 1 < w.n) now = load(r + 1, w.c0);
+    constexpr int kAhead = 4;
+    Held held[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) held[i] = load();
+    for (Cursor at = {0, w.c0}; at.r < w.n;) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const Held now = held[i];
+            held[i] = load();
+            const int r = min(at.r, 63), c = at.c, t = w.t0 + r;
+            const int pos = __builtin_amdgcn_readlane(places.pos, r), page = __builtin_amdgcn_readlane(places.page, r);
+            at.next(w);
             const int hd = c * kHeads + lane / kLanes;
             if (pos == kNoRow || hd >= heads) continue;
             const bool is_k = hd < p.cache.heads;
             const int h = is_k ? hd : hd - p.cache.heads;
             float v[16] = {};
             if (page >= 0) {
-                const float f = MX ? e8m0_value(held.byte) : e4m3_value(held.byte);
+                const float f = MX ? e8m0_value(now.byte) : e4m3_value(now.byte);
                 const float hs = MX ? 1.0f : (is_k ? p.cache.k_scale : p.cache.v_scale)[h];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float2 u = e2m1x2_unpack(j < 4 ? held.w.x : held.w.y, j & 3);
+                    const float2 u = e2m1x2_unpack(j < 4 ? now.w.x : now.w.y, j & 3);
                     v[2 * j] = u.x * f * hs;
                     v[2 * j + 1] = u.y * f * hs;
                 }
@@ -264,15 +284,18 @@ __global__ void __launch_bounds__(kThreads) k_kv_gather(const KvGather p) {
     }
 }
 
-// Rows and chunks of heads for a wave: one of each while there are no more than
-// 16384 waves to have them (64 on each of 256 compute units), then more chunks, then
-// up to 8 rows (64 of over 2^26, so that a grid holds them).
+// Chunks of heads and rows for a wave: more chunks than one where there are over 8192
+// waves to have them (32 on each of 256 compute units), and then more rows, up to
+// 8, where there are over 32768 (64 rows of over 2^26, so that a grid holds them).
+// 15047 rows of 72 heads to append, 16 to gather: from 4096 on 127 and 21.9 us, from
+// 8192 119 and 21.6, from 32768 141 and 27.8; 79926 rows to gather, more rows from
+// 8192 on 134 us, from 32768 109.
 template <typename P>
 int divide_rows(P& p, int heads) {
     const int per = 64 / (p.cache.dim / 16), chunks = (heads + per - 1) / per;
-    const int64_t each = (int64_t)p.plan.rows * chunks / 16384;
-    p.chunks_each = (int)std::max<int64_t>(1, std::min<int64_t>(chunks, each));
-    p.rows_each = (int)std::max<int64_t>(1, std::min<int64_t>(p.plan.rows > (1 << 26) ? 64 : 8, each / chunks));
+    const int64_t items = (int64_t)p.plan.rows * chunks;
+    p.chunks_each = (int)std::max<int64_t>(1, std::min<int64_t>(chunks, items / 8192));
+    p.rows_each = (int)std::max<int64_t>(1, std::min<int64_t>(p.plan.rows > (1 << 26) ? 64 : 8, items / chunks / 32768));
     const int64_t waves = (int64_t)((p.plan.rows + p.rows_each - 1) / p.rows_each) * ((chunks + p.chunks_each - 1) / p.chunks_each);
     return (int)((waves + kWaves - 1) / kWaves);
 }
