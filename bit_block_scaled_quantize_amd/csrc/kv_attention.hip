@@ -197,17 +197,24 @@ __device__ __forceinline__ int64_t sum64(int64_t v) {
 }
 
 // Steps and segments of 256 sequences, 4 consecutive ones to a lane, whose loads
-// are under way together.
+// are under way together; where there are 64 in all or fewer, one to a lane.
 struct Quad {
     int real[4], segs[4];
+    static __device__ __forceinline__ int each(const KvAttention& p) { return p.plan.seqs <= 64 ? 1 : 4; }
     __device__ __forceinline__ Quad(const KvAttention& p, int b) {
-        const int s = b + 4 * (threadIdx.x & 63);
+        const int s = b + each(p) * (threadIdx.x & 63);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {  // (without a branch: past the end the last one's again)
-            const Seq q = seq_of(p, min(s + i, p.plan.seqs - 1));
-            real[i] = q.real;
-            segs[i] = s + i < p.plan.seqs ? q.columns * p.cache.heads : 0;
+        for (int i = 0; i < 4; ++i) real[i] = segs[i] = 0;
+        count(p, s, 0);
+        if (each(p) == 4) {
+#pragma unroll
+            for (int i = 1; i < 4; ++i) count(p, s + i, i);
         }
+    }
+    __device__ __forceinline__ void count(const KvAttention& p, int s, int i) {
+        const Seq q = seq_of(p, min(s, p.plan.seqs - 1));  // (past the end the last one's again, without a branch)
+        real[i] = q.real;
+        segs[i] = s < p.plan.seqs ? q.columns * p.cache.heads : 0;
     }
 };
 
@@ -226,8 +233,9 @@ struct List {
         for (int b = 256; b < p.plan.seqs; b += 256) sum += from_lane(scan64(all_of(Quad(p, b))), 63);
     }
     __device__ __forceinline__ int64_t all_of(const Quad& q) const {
-        return count(q.real[0], q.segs[0]) + count(q.real[1], q.segs[1]) + count(q.real[2], q.segs[2]) +
-               count(q.real[3], q.segs[3]);
+        int64_t n = count(q.real[0], q.segs[0]);
+        if (Quad::each(p) == 4) n += count(q.real[1], q.segs[1]) + count(q.real[2], q.segs[2]) + count(q.real[3], q.segs[3]);
+        return n;
     }
     __device__ __forceinline__ int find(int64_t u, int64_t& first) const {
         int64_t before = 0, upto = upto0;
@@ -236,14 +244,16 @@ struct List {
             const int64_t all = from_lane(upto, 63);
             if (u < before + all) {
                 const int l = __builtin_ctzll(__ballot(u < before + upto));
-                int s = b + 4 * l;
+                int s = b + Quad::each(p) * l;
                 first = before + from_lane(upto - all_of(q), l);
+                if (Quad::each(p) == 4) {
 #pragma unroll
-                for (int i = 0; i < 3; ++i) {
-                    const int64_t n = from_lane(count(q.real[i], q.segs[i]), l);
-                    if (s == b + 4 * l + i && u >= first + n) {
-                        first += n;
-                        ++s;
+                    for (int i = 0; i < 3; ++i) {
+                        const int64_t n = from_lane(count(q.real[i], q.segs[i]), l);
+                        if (s == b + 4 * l + i && u >= first + n) {
+                            first += n;
+                            ++s;
+                        }
                     }
                 }
                 return __builtin_amdgcn_readfirstlane(s);
@@ -277,7 +287,7 @@ constexpr int kShares = D == 256 ? 512 : F32 && D == 128 ? 768 : 1024;
 //              cost.
 // (Parts end with their segment where shares would have a second one to begin,
 // which costs some 5 us; many steps are better divided evenly.)
-constexpr int kShort = 16, kManySegments = 512, kLeast = 2 * kWaves, kMostPart = 32, kExtra = 4;
+constexpr int kShort = 16, kManySegments = 512, kLeast = kWaves, kMostPart = 32, kExtra = 4;
 struct Division {
     bool by_wave;
     int part;           // 0: in shares
