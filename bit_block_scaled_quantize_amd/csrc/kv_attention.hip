@@ -276,8 +276,9 @@ template <bool F32, int D>
 constexpr int kShares = D == 256 ? 512 : F32 && D == 128 ? 768 : 1024;
 
 // How the segments are divided, by what they are on the device:
-//   by wave    no segment has more than kShort steps, and there are kManySegments
-//              at least: each wave has whole segments of its own;
+//   by team    no segment has more than kShort steps, and there are kManySegments
+//              at least: teams of 4, 2 or 1 waves, as many as there are segments or
+//              nearly, have whole ones;
 //   in parts   of `part` steps (kLeast at least), as many as there are workgroups
 //              or fewer, if that takes no more than kMostPart steps: a workgroup
 //              has one part;
@@ -289,7 +290,7 @@ constexpr int kShares = D == 256 ? 512 : F32 && D == 128 ? 768 : 1024;
 // which costs some 5 us; many steps are better divided evenly.)
 constexpr int kShort = 16, kManySegments = 512, kLeast = kWaves, kMostPart = 32, kExtra = 4;
 struct Division {
-    bool by_wave;
+    int team;           // waves of a team; 0: not by team
     int part;           // 0: in shares
     int64_t sum;        // segments, parts or units of the list
     int64_t each, rest; // shares: the first `rest` have a unit more
@@ -301,7 +302,7 @@ struct Division {
     }
     // entries of a sequence
     __device__ __forceinline__ int64_t operator()(int real, int segs) const {
-        return by_wave ? segs : part ? (int64_t)segs * ((uint32_t)(real + part - 1) / (uint32_t)part)
+        return team ? segs : part ? (int64_t)segs * ((uint32_t)(real + part - 1) / (uint32_t)part)
                                      : segs * ((int64_t)real + kExtra);
     }
 };
@@ -321,8 +322,8 @@ __device__ __forceinline__ Division divide(const KvAttention& p, const Quad& fir
     steps = sum64(steps);
     segments = sum64(segments);
     Division d = {};
-    d.by_wave = !__any(longer) && segments >= kManySegments;
-    if (d.by_wave || segments == 0) {
+    if (!__any(longer) && segments >= kManySegments) d.team = segments <= most ? 4 : segments <= 2 * most ? 2 : 1;
+    if (d.team || segments == 0) {
         d.sum = segments;
         return d;
     }
@@ -461,34 +462,38 @@ __global__ void __launch_bounds__(kThreads, (kShares<F32, D> / 256)) k_kv_attent
 
     const Quad first256(p, 0);
     const Division d = divide(p, first256, kShares<F32, D>);
-    int64_t u = d.by_wave ? (int64_t)blockIdx.x * kWaves + wave : blockIdx.x, u_end = d.sum;
-    if (!d.by_wave && !d.part) {
+    const int team = d.team ? d.team : kWaves, teams = kWaves / team, member = wave & (team - 1), mine0 = wave - member;
+    // the workgroup's first entry; its team's is `team_u` further on
+    const int team_u = d.team ? wave / team : 0;
+    int64_t u = d.team ? (int64_t)blockIdx.x * teams : blockIdx.x, u_end = d.sum;
+    if (!d.team && !d.part) {
         if (u >= d.shares) return;
         u_end = d.begin(u + 1);
         u = d.begin(u);
     }
     if (u >= u_end) return;
     int64_t seq_first;
-    int s = list_of(p, first256, d).find(u, seq_first);
+    int s = list_of(p, first256, d).find(min(u + team_u, u_end - 1), seq_first);
     Seq q = seq_of(p, s);
     const int slot_mask = (1 << p.plan.page_shift) - 1;
-    const int stride = d.by_wave ? 1 : kWaves;
 
     while (u < u_end) {
+        const bool idle = u + team_u >= u_end;  // (a team past the last segment has its barriers alone)
+        const int64_t own = min(u + team_u, u_end - 1);
         for (;;) {
             const int64_t n = d(q.real, q.columns * p.cache.heads);
-            if (u < seq_first + n) break;
+            if (own < seq_first + n) break;
             seq_first += n;
             q = seq_of(p, ++s);
         }
-        const Segment g = segment_at(p, d, q, seq_first, u);
+        const Segment g = segment_at(p, d, q, seq_first, own);
         // steps [from, to) of the segment's
-        int from = 0, to = q.real;
+        int from = 0, to = idle ? 0 : q.real;
         if (d.part) {
             from = (int)(u - g.begin) * d.part;
             to = min(q.real, from + d.part);
             u_end = 0;
-        } else if (!d.by_wave) {
+        } else if (!d.team) {
             from = (int)min(u - g.begin, (int64_t)q.real);
             to = (int)min(u_end - g.begin, (int64_t)q.real);
             if (from > 0 && from >= to) {  // (an end that counts but has no steps)
@@ -509,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, (kShares<F32, D> / 256)) k_kv_attent
 
         // steps of 32 keys that some column sees
         const int j1 = min(q.first_step + to, pos_last < 0 ? 0 : pos_last / kStep + 1);
-        int j = max(q.first_step + from, low_first / kStep) + (d.by_wave ? 0 : wave);
+        int j = max(q.first_step + from, low_first / kStep) + member;
 
         const auto find_page = [&](int at, int t) {
             const int k16 = at * kStep + 16 * t;
@@ -531,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, (kShares<F32, D> / 256)) k_kv_attent
             page[t] = __builtin_amdgcn_readfirstlane(find_page(j, t));
             st.k[t] = load(j, t, page[t], p.cache.k_codes, p.cache.k_scales);
             st.v[t] = load(j, t, page[t], p.cache.v_codes, p.cache.v_scales);
-            next[t] = find_page(j + stride, t);
+            next[t] = find_page(j + team, t);
         }
 
         // q, its row scaled into FP16's range
@@ -579,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, (kShares<F32, D> / 256)) k_kv_attent
 
         // Codes are loaded again as soon as they are converted: the next step's
         // are under way while one is multiplied, and the pages of the one after.
-        for (; j < j1; j += stride) {
+        for (; j < j1; j += team) {
             const int k32 = j * kStep;
             const bool holes[2] = {page[0] < 0, page[1] < 0};
 #pragma unroll
@@ -602,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, (kShares<F32, D> / 256)) k_kv_attent
                 }
             }
 #pragma unroll
-            for (int t = 0; t < 2; ++t) st.k[t] = load(j + stride, t, page[t], p.cache.k_codes, p.cache.k_scales);
+            for (int t = 0; t < 2; ++t) st.k[t] = load(j + team, t, page[t], p.cache.k_codes, p.cache.k_scales);
             // V to LDS
 #pragma unroll
             for (int t = 0; t < 2; ++t)
@@ -611,8 +616,8 @@ __global__ void __launch_bounds__(kThreads, (kShares<F32, D> / 256)) k_kv_attent
                     *reinterpret_cast<v8*>(lds + (16 * t + col) * kRowBytes<D> + g4 * (D / 2) + 16 * i) = values8<D, MX>(st.v[t], i);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                st.v[t] = load(j + stride, t, page[t], p.cache.v_codes, p.cache.v_scales);
-                next[t] = find_page(j + 2 * stride, t);
+                st.v[t] = load(j + team, t, page[t], p.cache.v_codes, p.cache.v_scales);
+                next[t] = find_page(j + 2 * team, t);
             }
             __builtin_amdgcn_sched_barrier(0);
             if (k32 + kStep - 1 > pos_first || k32 < low_last || holes[0] || holes[1]) {
@@ -677,8 +682,8 @@ __global__ void __launch_bounds__(kThreads, (kShares<F32, D> / 256)) k_kv_attent
             l = a + b;
         }
         const float v_scale = MX ? 1.0f : p.cache.v_scale[g.head];
-        if (d.by_wave) {
-            if (col < g.count) {
+        if (d.team == 1) {
+            if (col < g.count && !idle) {
                 const float f = l > 0.0f ? v_scale / l : 0.0f;
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i)
@@ -698,20 +703,18 @@ __global__ void __launch_bounds__(kThreads, (kShares<F32, D> / 256)) k_kv_attent
             stats[1][wave][col] = l;
         }
         __syncthreads();
-        const bool whole = from == 0 && to == q.real;
+        const bool whole = d.team || (from == 0 && to == q.real);
         float* slot = slot_of<D>(p, blockIdx.x, from == 0 ? 1 : 0);
-        for (int i = threadIdx.x; i < g.count * (D / 4); i += kThreads) {
-            const int cc = i / (D / 4), d = 4 * (i % (D / 4));
+        for (int i = 64 * member + lane; i < (idle ? 0 : g.count * (D / 4)); i += 64 * team) {
+            const int cc = i / (D / 4), d4 = 4 * (i % (D / 4));
             float top = kLowest;
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) top = fmaxf(top, stats[0][w][cc]);
+            for (int w = mine0; w < mine0 + team; ++w) top = fmaxf(top, stats[0][w][cc]);
             float total = 0.0f;
             v4f_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) {
+            for (int w = mine0; w < mine0 + team; ++w) {
                 const float f = __builtin_amdgcn_exp2f(stats[0][w][cc] - top);
                 const v4f_t x = *reinterpret_cast<const v4f_t*>(reinterpret_cast<const float*>(kv_lds + w * kWaveBytes<D>) +
-                                                                cc * kMergeStride<D> + d);
+                                                                cc * kMergeStride<D> + d4);
                 total += f * stats[1][w][cc];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) sum[r] += f * x[r];
@@ -720,18 +723,18 @@ __global__ void __launch_bounds__(kThreads, (kShares<F32, D> / 256)) k_kv_attent
                 const float f = total > 0.0f ? v_scale / total : 0.0f;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) sum[r] *= f;
-                store_out<F32>(p, q, g, cc, d, sum);
-                if (p.lse && d == 0) store_lse(p, q, g, cc, top, total);
+                store_out<F32>(p, q, g, cc, d4, sum);
+                if (p.lse && d4 == 0) store_lse(p, q, g, cc, top, total);
             } else {
-                *reinterpret_cast<v4f_t*>(slot + cc * D + d) = sum;
-                if (d == 0) {
+                *reinterpret_cast<v4f_t*>(slot + cc * D + d4) = sum;
+                if (d4 == 0) {
                     slot[kCols * D + cc] = top;
                     slot[kCols * D + kCols + cc] = total;
                 }
             }
         }
         __syncthreads();
-        u = g.begin + g.entries;
+        u = d.team ? u + (int64_t)gridDim.x * teams : g.begin + g.entries;
     }
 }
 
@@ -784,7 +787,7 @@ __global__ void __launch_bounds__(kThreads) k_kv_join(const KvAttention p) {
     const Quad first256(p, 0);
     const Division d = divide(p, first256, kShares<F32, D>);
     const int64_t w = blockIdx.x + 1;
-    if (d.by_wave || w >= (d.part ? d.sum : d.shares)) return;
+    if (d.team || w >= (d.part ? d.sum : d.shares)) return;
     const int64_t u = d.part ? w : d.begin(w);
     int64_t seq_first;
     const Seq q = seq_of(p, list_of(p, first256, d).find(u, seq_first));

@@ -112,13 +112,17 @@ def test_holes_under_many_rows(nv):
         assert bool((o[150:] == 0).all()) and bool(torch.isinf(lse[150:]).all())
 
 
-@pytest.mark.parametrize("seqs", [65, 200, 1030])
+@pytest.mark.parametrize("seqs", [65, 200, 301, 700, 1030])
 def test_many_sequences(nv, seqs):
     lengths = [(37 * i * i + 11 * i) % 90 for i in range(seqs)]
     run_and_check(nv, lengths, None, 2, 2, 64, 16, False, "bf16", seed=7)
+    run_and_check(nv, lengths, None, 2, 5, 128, 16, seqs % 2 == 0, "f32", seed=7)
     if seqs < 1000:
         new = [min(l, (5 * i) % 4) for i, l in enumerate(lengths)]
         run_and_check(nv, lengths, new, 1, 3, 64, 16, True, "f32", seed=8)
+    # with one longer sequence among them
+    lengths[seqs // 2] = 2500
+    run_and_check(nv, lengths, None, 2, 2, 64, 16, False, "bf16", seed=9, window=seqs % 2 * 1000)
 
 
 def test_scales_and_large_scores(nv):
