@@ -23,6 +23,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "kv_device.hpp"
 #include "launch.hpp"
@@ -516,10 +517,12 @@ __global__ void __launch_bounds__(kThreads, (kShares<F32, D> / 256)) k_kv_attent
         const int j1 = min(q.first_step + to, pos_last < 0 ? 0 : pos_last / kStep + 1);
         int j = max(q.first_step + from, low_first / kStep) + member;
 
-        const auto find_page = [&](int at, int t) {
+        // (the table's entries are looked at a step later)
+        const auto find_entry = [&](int at, int t) {
             const int k16 = at * kStep + 16 * t;
-            return at < j1 && k16 < q.length ? kv_page(p.plan, p.cache.pages, s, k16) : -1;
+            return at < j1 && k16 < q.length ? kv_entry(p.plan, s, k16) : -1;
         };
+        const auto page_of = [&](int entry) { return kv_page_of(__builtin_amdgcn_readfirstlane(entry), p.cache.pages); };
         const auto load = [&](int at, int t, int page, const uint8_t* codes, const uint8_t* scales) {
             Codes<D> c = {};
             if (page >= 0) {
@@ -533,10 +536,10 @@ __global__ void __launch_bounds__(kThreads, (kShares<F32, D> / 256)) k_kv_attent
         int page[2], next[2];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            page[t] = __builtin_amdgcn_readfirstlane(find_page(j, t));
+            page[t] = page_of(find_entry(j, t));
             st.k[t] = load(j, t, page[t], p.cache.k_codes, p.cache.k_scales);
             st.v[t] = load(j, t, page[t], p.cache.v_codes, p.cache.v_scales);
-            next[t] = find_page(j + team, t);
+            next[t] = find_entry(j + team, t);
         }
 
         // q, its row scaled into FP16's range
@@ -592,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, (kShares<F32, D> / 256)) k_kv_attent
                 const uint32_t there = k32 + 16 * t + col < q.length ? ~0u : 0u;  // (behind the end is no number)
                 st.k[t].s &= there;
                 st.v[t].s &= there;
-                page[t] = __builtin_amdgcn_readfirstlane(next[t]);
+                page[t] = page_of(next[t]);
             }
             // scores: register r of sub-tile t is key 16 t + 4 g4 + r of the column
             v4f_t sc[2];
@@ -617,15 +620,17 @@ __global__ void __launch_bounds__(kThreads, (kShares<F32, D> / 256)) k_kv_attent
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 st.v[t] = load(j + team, t, page[t], p.cache.v_codes, p.cache.v_scales);
-                next[t] = find_page(j + 2 * team, t);
+                next[t] = find_entry(j + 2 * team, t);
             }
             __builtin_amdgcn_sched_barrier(0);
             if (k32 + kStep - 1 > pos_first || k32 < low_last || holes[0] || holes[1]) {
+                int first = k32;
+                asm volatile("" : "+v"(first));  // (so that the compiler keeps the branch, and compares in few steps)
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const int key = k32 + 16 * t + 4 * g4 + r;
+                        const int key = first + 16 * t + 4 * g4 + r;
                         sc[t][r] = key <= pos && key >= low && !holes[t] ? sc[t][r] : -INFINITY;
                     }
             }
@@ -809,10 +814,16 @@ __global__ void __launch_bounds__(kThreads) k_kv_join(const KvAttention p) {
 
 // ---------------------------------------------------------------- many rows
 // k_kv_prefill: a workgroup has 32 columns to a wave and goes over 64 keys at a
-// time, converted once for all of them into LDS (two buffers; codes are loaded
-// two tiles ahead, their pages three).  S^T = K Q^T and O^T = V^T P^T by
+// time, converted once for all of them into LDS.  S^T = K Q^T and O^T = V^T P^T by
 // 32x32x16 MFMA; as in k_kv_attention the first product's sums are the second's
 // operand as they lie.
+//
+// A wave alternates between two phases, with a barrier after each: the products of
+// the tile before with V and of this one with K (matrix instructions), and this
+// one's softmax and the conversion of a later tile (vector instructions).  The two
+// waves of a SIMD are a phase apart, so that one's matrix instructions go with the
+// other's vector instructions.  Keys are then converted two tiles ahead, values one,
+// into three buffers each (D 256 has one wave to a SIMD: one tile ahead, one buffer).
 template <int D>
 constexpr int kPreWaves = D == 256 ? 4 : 8;
 template <int D>
@@ -823,8 +834,13 @@ template <int D>
 constexpr int kPreK = 2 * D + 16;
 template <int D>
 constexpr int kPreV = 2 * D + 64;
+// Of a buffer; K's ends with 16 bytes, whether its keys 16 i and on have no page.
 template <int D>
-constexpr int kPreBytes = kTile * (kPreK<D> + kPreV<D>) + 16;
+constexpr int kPreKBytes = kTile * kPreK<D> + 16;
+template <int D>
+constexpr int kPreVBytes = kTile * kPreV<D>;
+template <int D>
+constexpr int kPreBuffers = D == 256 ? 1 : 3;
 
 typedef float v16f_t __attribute__((ext_vector_type(16)));
 
@@ -833,6 +849,15 @@ __device__ __forceinline__ v16f_t mfma32(v8h_t a, v8h_t b, v16f_t c) {
 }
 __device__ __forceinline__ v16f_t mfma32(v8b_t a, v8b_t b, v16f_t c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+// f(0) .. f(N - 1), each with its number as a constant.
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void in_order(F f) {
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>());
+        in_order<N, I + 1>(f);
+    }
 }
 
 // Blocks of kPreCols columns of sequence s for a kv head.
@@ -961,115 +986,123 @@ __global__ void __launch_bounds__(64 * kPreWaves<D>, kPreWaves<D> / 4) k_kv_pref
     const int lkey = threadIdx.x / W, part = threadIdx.x % W;
     struct Raw {
         uint32_t w[EPT / 8], s;
-    } rk, rv;
-    int page_next;
+    };
     const int slot_mask = (1 << p.plan.page_shift) - 1;
     const int j0 = work.from, j1 = work.to;
-    const auto find_page = [&](int j) {
+    // (the table's entries are looked at a tile later)
+    const auto find_entry = [&](int j) {
         const int key = j * kTile + lkey;
-        return j < j1 && key < q.length ? kv_page(p.plan, p.cache.pages, work.s, key) : -1;
+        return j < j1 && key < q.length ? kv_entry(p.plan, work.s, key) : -1;
     };
-    bool hole;  // of the codes loaded
-    const auto load = [&](int j, int page) {
-        const int key = j * kTile + lkey;
-        hole = j < j1 && key < q.length && page < 0;
+    const auto load = [&](int j, int page, const uint8_t* codes, const uint8_t* scales) {
+        Raw r = {};
+        if (page >= 0) {
+            const int64_t slot = (((int64_t)page * p.cache.heads + g.head) << p.plan.page_shift) + ((j * kTile + lkey) & slot_mask);
+            const uint8_t* c = codes + slot * (D / 2) + part * (EPT / 2);
+            if constexpr (EPT == 8) {
+                r.w[0] = *reinterpret_cast<const uint32_t*>(c);
+            } else if constexpr (EPT == 16) {
+                const uint2 x = *reinterpret_cast<const uint2*>(c);
+                r.w[0] = x.x;
+                r.w[1] = x.y;
+            } else {
 #pragma unroll
-        for (int i = 0; i < EPT / 8; ++i) rk.w[i] = rv.w[i] = 0;
-        rk.s = rv.s = 0;
-        if (page < 0) return;
-        const int64_t slot = (((int64_t)page * p.cache.heads + g.head) << p.plan.page_shift) + (key & slot_mask);
-        const uint8_t* kc = p.cache.k_codes + slot * (D / 2) + part * (EPT / 2);
-        const uint8_t* vc = p.cache.v_codes + slot * (D / 2) + part * (EPT / 2);
-        if constexpr (EPT == 8) {
-            rk.w[0] = *reinterpret_cast<const uint32_t*>(kc);
-            rv.w[0] = *reinterpret_cast<const uint32_t*>(vc);
-        } else if constexpr (EPT == 16) {
-            const uint2 a = *reinterpret_cast<const uint2*>(kc), b = *reinterpret_cast<const uint2*>(vc);
-            rk.w[0] = a.x, rk.w[1] = a.y;
-            rv.w[0] = b.x, rv.w[1] = b.y;
-        } else {
+                for (int i = 0; i < EPT / 32; ++i) {
+                    const u4_t x = *reinterpret_cast<const u4_t*>(c + 16 * i);
 #pragma unroll
-            for (int i = 0; i < EPT / 32; ++i) {
-                const u4_t a = *reinterpret_cast<const u4_t*>(kc + 16 * i), b = *reinterpret_cast<const u4_t*>(vc + 16 * i);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    rk.w[4 * i + k] = a[k];
-                    rv.w[4 * i + k] = b[k];
+                    for (int k = 0; k < 4; ++k) r.w[4 * i + k] = x[k];
                 }
             }
+            const uint8_t* at = scales + slot * (D / per) + part * EPT / per;
+            constexpr int n = EPT / per;
+            if constexpr (n <= 1) r.s = *at;
+            else if constexpr (n == 2) r.s = *reinterpret_cast<const h_align1*>(at);
+            else r.s = *reinterpret_cast<const w_align1*>(at);
         }
-        const int64_t at = slot * (D / per) + part * EPT / per;
-        constexpr int n = EPT / per;
-        if constexpr (n <= 1) {
-            rk.s = p.cache.k_scales[at];
-            rv.s = p.cache.v_scales[at];
-        } else if constexpr (n == 2) {
-            rk.s = *reinterpret_cast<const h_align1*>(p.cache.k_scales + at);
-            rv.s = *reinterpret_cast<const h_align1*>(p.cache.v_scales + at);
-        } else {
-            rk.s = *reinterpret_cast<const w_align1*>(p.cache.k_scales + at);
-            rv.s = *reinterpret_cast<const w_align1*>(p.cache.v_scales + at);
-        }
+        return r;
     };
-    // converts what is loaded into buffer b; word i of its last 16 bytes: whether
-    // its keys 16 i and on have no page
-    const auto stage = [&](int b) {
-        char* k = kv_lds + b * kPreBytes<D>;
-        char* v = k + kTile * kPreK<D>;
+    char* const k_lds = kv_lds;
+    char* const v_lds = kv_lds + kPreBuffers<D> * kPreKBytes<D>;
+    const auto stage = [&](const Raw& r, char* to) {
 #pragma unroll
-        for (int i = 0; i < EPT / 8; ++i) {
-            *reinterpret_cast<v8*>(k + lkey * kPreK<D> + part * (2 * EPT) + 16 * i) =
-                F::values(rk.w[i], (rk.s >> (8 * (8 * i / per))) & 0xFFu);
-            *reinterpret_cast<v8*>(v + lkey * kPreV<D> + part * (2 * EPT) + 16 * i) =
-                F::values(rv.w[i], (rv.s >> (8 * (8 * i / per))) & 0xFFu);
-        }
-        if (part == 0 && (lkey & 15) == 0) *reinterpret_cast<int*>(v + kTile * kPreV<D> + lkey / 4) = hole;
+        for (int i = 0; i < EPT / 8; ++i)
+            *reinterpret_cast<v8*>(to + part * (2 * EPT) + 16 * i) = F::values(r.w[i], (r.s >> (8 * (8 * i / per))) & 0xFFu);
     };
+    const auto stage_k = [&](const Raw& r, int j, int page, int b) {
+        char* to = k_lds + b * kPreKBytes<D>;
+        stage(r, to + lkey * kPreK<D>);
+        if (part == 0 && (lkey & 15) == 0)
+            *reinterpret_cast<int*>(to + kTile * kPreK<D> + lkey / 4) = page < 0 && j * kTile + lkey < q.length;
+    };
+    const auto stage_v = [&](const Raw& r, int b) { stage(r, v_lds + b * kPreVBytes<D> + lkey * kPreV<D>); };
 
     float m = kLowest, l = 0.0f;
-    v16f_t o[DB];
+    v16f_t o[DB], sc[2];
+    v8 pf[4][PP];
+    uint32_t holes = 0;  // bit i: keys 16 i and on of the tile have no page
 #pragma unroll
     for (int i = 0; i < DB; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r) o[i][r] = 0.0f;
 
-    if (j0 < j1) {
-        load(j0, find_page(j0));
-        page_next = find_page(j0 + 1);
-        stage(0);
-        load(j0 + 1, page_next);
-        page_next = find_page(j0 + 2);
-    }
-    for (int j = j0; j < j1; ++j) {
-        lds_barrier();
-        const int b = (j - j0) & 1;
-        if (j + 1 < j1) {
-            stage(b ^ 1);
-            load(j + 2, page_next);
-            page_next = find_page(j + 3);
-        }
+    // The operands of the products are read from LDS kDepth products ahead, in the
+    // order that is written here: left to itself the compiler reads each right before
+    // its product, which then waits for it.
+    constexpr int kDepth = 4;
+    const auto pipelined = [&](auto count, auto read, auto product) {
+        constexpr int N = decltype(count)::value;
+        v8 a[N];
+        in_order<kDepth>([&](auto n) { a[n] = read(n); });
+        in_order<N>([&](auto n) {
+            if constexpr (n + kDepth < N) a[n + kDepth] = read(std::integral_constant<int, n + kDepth>());
+            __builtin_amdgcn_sched_barrier(0);
+            product(n, a[n]);
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    };
+    const auto times_k = [&](int b) {
+        const char* kt = k_lds + b * kPreKBytes<D> + col * kPreK<D> + 16 * h;
+        const u4_t flags = *reinterpret_cast<const u4_t*>(k_lds + b * kPreKBytes<D> + kTile * kPreK<D>);
+        holes = __builtin_amdgcn_readfirstlane(flags[0] | flags[1] << 1 | flags[2] << 2 | flags[3] << 3);
+        // product n: keys 32 (n % 2) and on, elements 16 (n / 2) and on
+        pipelined(
+            std::integral_constant<int, 2 * KS>(),
+            [&](auto n) { return *reinterpret_cast<const v8*>(kt + 32 * (n % 2) * kPreK<D> + 32 * (n / 2)); },
+            [&](auto n, v8 x) {
+                const v16f_t zero = {};
+                sc[n % 2] = mfma32(x, qf[n / 2], n / 2 == 0 ? zero : sc[n % 2]);
+            });
+    };
+    const auto times_v = [&](int b) {
+        const char* vt = v_lds + b * kPreVBytes<D> + (4 * h + ((lane & 15) >> 2)) * kPreV<D> + 32 * ((lane >> 4) & 1) + 8 * (lane & 3);
+        // product n: keys 16 (n / DB) and on, elements 32 (n % DB) and on
+        pipelined(
+            std::integral_constant<int, 4 * DB>(),
+            [&](auto n) {
+                typedef __attribute__((address_space(3))) v4s_t lds_v4s;
+                typedef short v8s_t __attribute__((ext_vector_type(8)));
+                const char* at = vt + 16 * (n / DB) * kPreV<D> + 64 * (n % DB);
+                const v4s_t x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)at);
+                const v4s_t y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(at + 8 * kPreV<D>));
+                const v8s_t z = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+                return __builtin_bit_cast(v8, z);
+            },
+            [&](auto n, v8 x) {
+#pragma unroll
+                for (int k = PP - 1; k >= 0; --k) o[n % DB] = mfma32(x, pf[n / DB][k], o[n % DB]);
+            });
+    };
+    const auto softmax = [&](int j) {
         const int key0 = j * kTile;
-        if (key0 > wpos_last || key0 + kTile <= wlow_first) continue;
-        const char* kt = kv_lds + b * kPreBytes<D>;
-        const char* vt = kt + kTile * kPreK<D>;
-        v16f_t sc[2];
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-#pragma unroll
-            for (int r = 0; r < 16; ++r) sc[t][r] = 0.0f;
-#pragma unroll
-            for (int i = 0; i < KS; ++i)
-                sc[t] = mfma32(*reinterpret_cast<const v8*>(kt + (32 * t + col) * kPreK<D> + 32 * i + 16 * h), qf[i], sc[t]);
-        }
-        const u4_t holes = *reinterpret_cast<const u4_t*>(vt + kTile * kPreV<D>);
-        const bool none = (holes[0] | holes[1] | holes[2] | holes[3]) != 0;
-        if (none || key0 + kTile - 1 > wpos_first || key0 < wlow_last) {
+        if (holes || key0 + kTile - 1 > wpos_first || key0 < wlow_last) {
+            int first = key0;
+            asm volatile("" : "+v"(first));  // (so that the compiler keeps the branch, and compares in few tiles)
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    const int key = key0 + 32 * t + 8 * (r >> 2) + 4 * h + (r & 3);
-                    const bool seen = key <= pos && key >= low && !holes[2 * t + (r >> 3)];
+                    const int key = first + 32 * t + 8 * (r >> 2) + 4 * h + (r & 3);
+                    const bool seen = key <= pos && key >= low && !(holes >> (2 * t + (r >> 3)) & 1);
                     sc[t][r] = seen ? sc[t][r] : -INFINITY;
                 }
         }
@@ -1090,7 +1123,6 @@ __global__ void __launch_bounds__(64 * kPreWaves<D>, kPreWaves<D> / 4) k_kv_pref
                 for (int r = 0; r < 16; ++r) o[i][r] *= f;
         }
         const float base = m - kBias;
-        v8 pf[4][PP];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             float w[8];
@@ -1101,19 +1133,61 @@ __global__ void __launch_bounds__(64 * kPreWaves<D>, kPreWaves<D> / 4) k_kv_pref
             }
             split8<MX, PP>(w, pf[u]);
         }
+    };
+    // (nothing is moved over a phase's end)
+    const auto phase_end = [&]() {
+        __builtin_amdgcn_sched_barrier(0);
+        lds_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+
+    constexpr int NB = kPreBuffers<D>, KA = NB == 3 ? 2 : 1;  // tiles that keys are ahead (values: one less)
+    if (j0 < j1) {
+        int page[4];  // of the key in tiles j0 .. j0 + 3
 #pragma unroll
-        for (int i = 0; i < DB; ++i)
+        for (int i = 0; i < KA + 2; ++i) page[i] = find_entry(j0 + i);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                typedef __attribute__((address_space(3))) v4s_t lds_v4s;
-                typedef short v8s_t __attribute__((ext_vector_type(8)));
-                const char* at = vt + (16 * u + 4 * h + ((lane & 15) >> 2)) * kPreV<D> + 64 * i + 32 * ((lane >> 4) & 1) + 8 * (lane & 3);
-                const v4s_t x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)at);
-                const v4s_t y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(at + 8 * kPreV<D>));
-                const v8s_t z = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+        for (int i = 0; i < KA + 1; ++i) page[i] = kv_page_of(page[i], p.cache.pages);
+        Raw rk[KA], rv;
 #pragma unroll
-                for (int k = PP - 1; k >= 0; --k) o[i] = mfma32(__builtin_bit_cast(v8, z), pf[u][k], o[i]);
+        for (int i = 0; i < KA; ++i) rk[i] = load(j0 + i, page[i], p.cache.k_codes, p.cache.k_scales);
+        rv = load(j0, page[0], p.cache.v_codes, p.cache.v_scales);
+#pragma unroll
+        for (int i = 0; i < KA; ++i) stage_k(rk[i], j0 + i, page[i], i);
+        rk[0] = load(j0 + KA, page[KA], p.cache.k_codes, p.cache.k_scales);
+        if constexpr (KA == 2) {
+            stage_v(rv, 0);
+            rv = load(j0 + 1, page[1], p.cache.v_codes, p.cache.v_scales);
+        }
+        // what is under way: keys of tile j + KA (page k_page), values of j + KA - 1;
+        // the next keys' entry of the table
+        int k_page = page[KA], next = page[KA + 1];
+        phase_end();
+        if (NB == 3 && wave >= 4) phase_end();
+        bool weights = false;  // of the tile before
+        int b = 0;             // tile j's buffer
+        for (int j = j0; j <= j1; ++j) {
+            const bool active = j < j1 && j * kTile <= wpos_last && j * kTile + kTile > wlow_first;
+            const int before = NB == 3 ? (b == 0 ? 2 : b - 1) : 0, after = NB == 3 ? (b == 2 ? 0 : b + 1) : 0;
+            __builtin_amdgcn_s_setprio(1);
+            if (weights) times_v(before);
+            if (active) times_k(b);
+            __builtin_amdgcn_s_setprio(0);
+            phase_end();
+            weights = active;
+            if (j < j1) {
+                if (active) softmax(j);
+                stage_k(rk[0], j + KA, k_page, before);  // (of three, the buffer after the next is the one before)
+                stage_v(rv, after);
+                rv = load(j + KA, k_page, p.cache.v_codes, p.cache.v_scales);
+                k_page = kv_page_of(next, p.cache.pages);
+                rk[0] = load(j + KA + 1, k_page, p.cache.k_codes, p.cache.k_scales);
+                next = find_entry(j + KA + 2);
             }
+            phase_end();
+            b = after;
+        }
+        if (NB == 3 && wave < 4) phase_end();
     }
     {
         float a, b;
@@ -1196,7 +1270,7 @@ int pre_splits(int64_t rows, int64_t seqs, int group, int heads, int dim) {
 
 template <bool MX, int D>
 hipError_t run_prefill(KvAttention p, hipStream_t s) {
-    constexpr int bytes = 2 * kPreBytes<D>;
+    constexpr int bytes = kPreBuffers<D> * (kPreKBytes<D> + kPreVBytes<D>);
     const int64_t blocks = pre_blocks_most(p.plan.rows, p.plan.seqs, p.group, D) * p.cache.heads;
     p.splits = pre_splits(p.plan.rows, p.plan.seqs, p.group, p.cache.heads, D);
     p.pre_ws = p.ws + 2 * kShares<false, D> * kSlotFloats<D>;

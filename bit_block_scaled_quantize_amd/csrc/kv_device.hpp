@@ -29,11 +29,12 @@ __device__ __forceinline__ void kv_rows(const KvPlan& p, int s, int& first, int&
     n = max(first, min(p.offsets[s + 1], p.rows)) - first;
 }
 
-// Page of position pos of sequence s, -1 where the table names none.
-__device__ __forceinline__ int kv_page(const KvPlan& p, int pages, int s, int pos) {
-    const int page = p.table[s * p.ld_table + (pos >> p.page_shift)];
-    return (uint32_t)page < (uint32_t)pages ? page : -1;
+// What the table says for position pos of sequence s, and the page that names: -1
+// for none.  (Looking at the entry waits for its load and for all loads before it.)
+__device__ __forceinline__ int kv_entry(const KvPlan& p, int s, int pos) {
+    return p.table[s * p.ld_table + (pos >> p.page_shift)];
 }
+__device__ __forceinline__ int kv_page_of(int entry, int pages) { return (uint32_t)entry < (uint32_t)pages ? entry : -1; }
 
 // Where rows t0 .. t0 + n - 1 (n <= 64) lie: lane r has row t0 + r's position and
 // page.
@@ -67,7 +68,7 @@ __device__ __forceinline__ KvPlaces kv_places(const KvPlan& p, int pages, int t0
         kv_rows(p, s, first, count);
         if (t >= first && t - first < count) {  // (not so where offsets are out of order)
             w.pos = kv_length(p, s) - count + (t - first);
-            if (w.pos >= 0) w.page = kv_page(p, pages, s, w.pos);
+            if (w.pos >= 0) w.page = kv_page_of(kv_entry(p, s, w.pos), pages);
         }
     }
     return w;
