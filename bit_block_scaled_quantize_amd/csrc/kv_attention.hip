@@ -137,6 +137,11 @@ __device__ __forceinline__ void split8(const float v[8], typename Form<MX>::v8 o
     }
 }
 
+// The sum of 8 values, in pairs (a sum one by one waits for each addition).
+__device__ __forceinline__ float sum8(const float v[8]) {
+    return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+}
+
 // ---------------------------------------------------------------- the list of work
 // Sequence s has `columns` blocks of 16 columns for each kv head: segments of
 // `real` steps of keys from first_step (one at least, so that rows that see no
@@ -659,12 +664,10 @@ __global__ void __launch_bounds__(kThreads, (kShares<F32, D> / 256)) k_kv_attent
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    w[4 * t + r] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][r], factor, -base));
-                    l += w[4 * t + r];
-                }
+                for (int r = 0; r < 4; ++r) w[4 * t + r] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][r], factor, -base));
             v8 pf[PP];
             split8<MX, PP>(w, pf);
+            l += sum8(w);
             asm volatile("" ::: "memory");
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
@@ -916,7 +919,7 @@ __device__ __forceinline__ bool pre_work(const KvAttention& p, int64_t id, PreWo
     const int pos0 = w.q.length - w.q.rows;
     const int first = pos0 + w.g.first / p.group, last = pos0 + (w.g.first + w.g.count - 1) / p.group;
     const int low = p.window ? max(0, first - p.window + 1) / kTile : 0;
-    const int tiles = last >= 0 ? last / kTile + 1 - low : 0;
+    const int tiles = last >= 0 && p.cache.pages > 0 ? last / kTile + 1 - low : 0;  // (without a page nothing is seen)
     const int each = (tiles + p.splits - 1) / p.splits;
     w.from = low + min(tiles, w.split * each);
     w.to = low + min(tiles, (w.split + 1) * each);
@@ -989,52 +992,58 @@ __global__ void __launch_bounds__(64 * kPreWaves<D>, kPreWaves<D> / 4) k_kv_pref
     };
     const int slot_mask = (1 << p.plan.page_shift) - 1;
     const int j0 = work.from, j1 = work.to;
-    // (the table's entries are looked at a tile later)
-    const auto find_entry = [&](int j) {
-        const int key = j * kTile + lkey;
-        return j < j1 && key < q.length ? kv_entry(p.plan, work.s, key) : -1;
+    // the table's entry for the thread's key of tile j, as it is loaded (past the end
+    // the last key's), and where that key lies: some slot, and whether it is its own
+    const auto find_entry = [&](int j) { return kv_entry(p.plan, work.s, min(j * kTile + lkey, q.length - 1)); };
+    struct Place {
+        int64_t slot;
+        bool there;
     };
-    const auto load = [&](int j, int page, const uint8_t* codes, const uint8_t* scales) {
-        Raw r = {};
-        if (page >= 0) {
-            const int64_t slot = (((int64_t)page * p.cache.heads + g.head) << p.plan.page_shift) + ((j * kTile + lkey) & slot_mask);
-            const uint8_t* c = codes + slot * (D / 2) + part * (EPT / 2);
-            if constexpr (EPT == 8) {
-                r.w[0] = *reinterpret_cast<const uint32_t*>(c);
-            } else if constexpr (EPT == 16) {
-                const uint2 x = *reinterpret_cast<const uint2*>(c);
-                r.w[0] = x.x;
-                r.w[1] = x.y;
-            } else {
+    const auto place_of = [&](int j, int entry) {
+        const int key = j * kTile + lkey, page = kv_page_of(entry, p.cache.pages);
+        return Place{(((int64_t)max(page, 0) * p.cache.heads + g.head) << p.plan.page_shift) + (key & slot_mask),
+                     page >= 0 && key < q.length};
+    };
+    // (without a branch: scales of a key that is not there become zero when it is converted)
+    const auto load = [&](int64_t slot, const uint8_t* codes, const uint8_t* scales) {
+        Raw r;
+        const uint8_t* c = codes + slot * (D / 2) + part * (EPT / 2);
+        if constexpr (EPT == 8) {
+            r.w[0] = *reinterpret_cast<const uint32_t*>(c);
+        } else if constexpr (EPT == 16) {
+            const uint2 x = *reinterpret_cast<const uint2*>(c);
+            r.w[0] = x.x;
+            r.w[1] = x.y;
+        } else {
 #pragma unroll
-                for (int i = 0; i < EPT / 32; ++i) {
-                    const u4_t x = *reinterpret_cast<const u4_t*>(c + 16 * i);
+            for (int i = 0; i < EPT / 32; ++i) {
+                const u4_t x = *reinterpret_cast<const u4_t*>(c + 16 * i);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) r.w[4 * i + k] = x[k];
-                }
+                for (int k = 0; k < 4; ++k) r.w[4 * i + k] = x[k];
             }
-            const uint8_t* at = scales + slot * (D / per) + part * EPT / per;
-            constexpr int n = EPT / per;
-            if constexpr (n <= 1) r.s = *at;
-            else if constexpr (n == 2) r.s = *reinterpret_cast<const h_align1*>(at);
-            else r.s = *reinterpret_cast<const w_align1*>(at);
         }
+        const uint8_t* at = scales + slot * (D / per) + part * EPT / per;
+        constexpr int n = EPT / per;
+        if constexpr (n <= 1) r.s = *at;
+        else if constexpr (n == 2) r.s = *reinterpret_cast<const h_align1*>(at);
+        else r.s = *reinterpret_cast<const w_align1*>(at);
         return r;
     };
     char* const k_lds = kv_lds;
     char* const v_lds = kv_lds + kPreBuffers<D> * kPreKBytes<D>;
-    const auto stage = [&](const Raw& r, char* to) {
+    const auto stage = [&](Raw r, bool there, char* to) {
+        r.s = there ? r.s : 0u;
 #pragma unroll
         for (int i = 0; i < EPT / 8; ++i)
             *reinterpret_cast<v8*>(to + part * (2 * EPT) + 16 * i) = F::values(r.w[i], (r.s >> (8 * (8 * i / per))) & 0xFFu);
     };
-    const auto stage_k = [&](const Raw& r, int j, int page, int b) {
+    const auto stage_k = [&](const Raw& r, bool there, int j, int b) {
         char* to = k_lds + b * kPreKBytes<D>;
-        stage(r, to + lkey * kPreK<D>);
+        stage(r, there, to + lkey * kPreK<D>);
         if (part == 0 && (lkey & 15) == 0)
-            *reinterpret_cast<int*>(to + kTile * kPreK<D> + lkey / 4) = page < 0 && j * kTile + lkey < q.length;
+            *reinterpret_cast<int*>(to + kTile * kPreK<D> + lkey / 4) = !there && j * kTile + lkey < q.length;
     };
-    const auto stage_v = [&](const Raw& r, int b) { stage(r, v_lds + b * kPreVBytes<D> + lkey * kPreV<D>); };
+    const auto stage_v = [&](const Raw& r, bool there, int b) { stage(r, there, v_lds + b * kPreVBytes<D> + lkey * kPreV<D>); };
 
     float m = kLowest, l = 0.0f;
     v16f_t o[DB], sc[2];
@@ -1127,11 +1136,9 @@ __global__ void __launch_bounds__(64 * kPreWaves<D>, kPreWaves<D> / 4) k_kv_pref
         for (int u = 0; u < 4; ++u) {
             float w[8];
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                w[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[u >> 1][8 * (u & 1) + r], factor, -base));
-                l += w[r];
-            }
+            for (int r = 0; r < 8; ++r) w[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[u >> 1][8 * (u & 1) + r], factor, -base));
             split8<MX, PP>(w, pf[u]);
+            l += sum8(w);
         }
     };
     // (nothing is moved over a phase's end)
@@ -1143,25 +1150,29 @@ __global__ void __launch_bounds__(64 * kPreWaves<D>, kPreWaves<D> / 4) k_kv_pref
 
     constexpr int NB = kPreBuffers<D>, KA = NB == 3 ? 2 : 1;  // tiles that keys are ahead (values: one less)
     if (j0 < j1) {
-        int page[4];  // of the key in tiles j0 .. j0 + 3
+        int entry[4];  // of the key in tiles j0 .. j0 + 3
 #pragma unroll
-        for (int i = 0; i < KA + 2; ++i) page[i] = find_entry(j0 + i);
+        for (int i = 0; i < KA + 2; ++i) entry[i] = find_entry(j0 + i);
+        Place at[3];
 #pragma unroll
-        for (int i = 0; i < KA + 1; ++i) page[i] = kv_page_of(page[i], p.cache.pages);
+        for (int i = 0; i < KA + 1; ++i) at[i] = place_of(j0 + i, entry[i]);
         Raw rk[KA], rv;
 #pragma unroll
-        for (int i = 0; i < KA; ++i) rk[i] = load(j0 + i, page[i], p.cache.k_codes, p.cache.k_scales);
-        rv = load(j0, page[0], p.cache.v_codes, p.cache.v_scales);
+        for (int i = 0; i < KA; ++i) rk[i] = load(at[i].slot, p.cache.k_codes, p.cache.k_scales);
+        rv = load(at[0].slot, p.cache.v_codes, p.cache.v_scales);
+        bool v_there = at[0].there;
 #pragma unroll
-        for (int i = 0; i < KA; ++i) stage_k(rk[i], j0 + i, page[i], i);
-        rk[0] = load(j0 + KA, page[KA], p.cache.k_codes, p.cache.k_scales);
+        for (int i = 0; i < KA; ++i) stage_k(rk[i], at[i].there, j0 + i, i);
+        // what is under way: keys of tile j + KA (at `k_at`), values of j + KA - 1; the
+        // next keys' entry of the table
+        Place k_at = at[KA];
+        rk[0] = load(k_at.slot, p.cache.k_codes, p.cache.k_scales);
         if constexpr (KA == 2) {
-            stage_v(rv, 0);
-            rv = load(j0 + 1, page[1], p.cache.v_codes, p.cache.v_scales);
+            stage_v(rv, v_there, 0);
+            rv = load(at[1].slot, p.cache.v_codes, p.cache.v_scales);
+            v_there = at[1].there;
         }
-        // what is under way: keys of tile j + KA (page k_page), values of j + KA - 1;
-        // the next keys' entry of the table
-        int k_page = page[KA], next = page[KA + 1];
+        int next = entry[KA + 1];
         phase_end();
         if (NB == 3 && wave >= 4) phase_end();
         bool weights = false;  // of the tile before
@@ -1177,11 +1188,12 @@ __global__ void __launch_bounds__(64 * kPreWaves<D>, kPreWaves<D> / 4) k_kv_pref
             weights = active;
             if (j < j1) {
                 if (active) softmax(j);
-                stage_k(rk[0], j + KA, k_page, before);  // (of three, the buffer after the next is the one before)
-                stage_v(rv, after);
-                rv = load(j + KA, k_page, p.cache.v_codes, p.cache.v_scales);
-                k_page = kv_page_of(next, p.cache.pages);
-                rk[0] = load(j + KA + 1, k_page, p.cache.k_codes, p.cache.k_scales);
+                stage_k(rk[0], k_at.there, j + KA, before);  // (of three, the buffer after the next is the one before)
+                stage_v(rv, v_there, after);
+                rv = load(k_at.slot, p.cache.v_codes, p.cache.v_scales);
+                v_there = k_at.there;
+                k_at = place_of(j + KA + 1, next);
+                rk[0] = load(k_at.slot, p.cache.k_codes, p.cache.k_scales);
                 next = find_entry(j + KA + 2);
             }
             phase_end();
