@@ -382,6 +382,20 @@ __device__ __forceinline__ float* slot_of(const KvAttention& p, int64_t w, int w
     return p.ws + (2 * w + which) * kSlotFloats<D>;
 }
 
+// What the second kernel's workgroup w - 1 joins: an equal part (the rank-th of n - 1)
+// of the segment that workgroup w's share begins inside of, whose n parts are those of
+// workgroups first_share and on.  n 0: nothing.  (Found again there, it took one token
+// over 8192 positions took 15.4 us instead of 14.3.)
+struct Join {
+    int n, rank, first_share, row, head, first, count, unused;
+};
+template <int D>
+constexpr int64_t kShareFloats = 2 * kSlotFloats<D> + sizeof(Join) / sizeof(float);
+template <int D, int SHARES>
+__device__ __forceinline__ Join* join_of(const KvAttention& p, int w) {
+    return reinterpret_cast<Join*>(p.ws + (int64_t)2 * SHARES * kSlotFloats<D>) + w;
+}
+
 template <bool F32>
 __device__ __forceinline__ void store_out(const KvAttention& p, const Seq& q, const Segment& g, int c, int d, v4f_t o) {
     const int row = q.row + (g.first + c) / p.group, head = g.head * p.group + (g.first + c) % p.group;
@@ -466,6 +480,7 @@ __global__ void __launch_bounds__(kThreads, (kShares<F32, D> / 256)) k_kv_attent
     char* lds = kv_lds + wave * kWaveBytes<D>;
     __shared__ float stats[2][kWaves][kCols];
 
+    if (threadIdx.x == 0) join_of<D, kShares<F32, D>>(p, blockIdx.x)->n = 0;
     const Quad first256(p, 0);
     const Division d = divide(p, first256, kShares<F32, D>);
     const int team = d.team ? d.team : kWaves, teams = kWaves / team, member = wave & (team - 1), mine0 = wave - member;
@@ -545,6 +560,13 @@ __global__ void __launch_bounds__(kThreads, (kShares<F32, D> / 256)) k_kv_attent
             st.k[t] = load(j, t, page[t], p.cache.k_codes, p.cache.k_scales);
             st.v[t] = load(j, t, page[t], p.cache.v_codes, p.cache.v_scales);
             next[t] = find_entry(j + team, t);
+        }
+
+        if (!d.team && from > 0 && threadIdx.x == 0) {
+            const int64_t first = d.part ? g.begin : d.share_of(g.begin);
+            const int n = d.part ? (int)g.entries : (int)(d.share_of(g.begin + q.real - 1) - first) + 1;
+            *join_of<D, kShares<F32, D>>(p, blockIdx.x) =
+                Join{n, (int)(blockIdx.x - first) - 1, (int)first, q.row, g.head, g.first, g.count, 0};
         }
 
         // q, its row scaled into FP16's range
@@ -788,25 +810,20 @@ __device__ __forceinline__ void join_items(const KvAttention& p, const Seq& q, c
     }
 }
 
-// Workgroup w - 1 joins an equal part of the segment that workgroup w of
-// k_kv_attention has a later part of: as many do as have one.
 template <bool MX, bool F32, int D>
 __global__ void __launch_bounds__(kThreads) k_kv_join(const KvAttention p) {
-    const Quad first256(p, 0);
-    const Division d = divide(p, first256, kShares<F32, D>);
-    const int64_t w = blockIdx.x + 1;
-    if (d.team || w >= (d.part ? d.sum : d.shares)) return;
-    const int64_t u = d.part ? w : d.begin(w);
-    int64_t seq_first;
-    const Seq q = seq_of(p, list_of(p, first256, d).find(u, seq_first));
-    const Segment g = segment_at(p, d, q, seq_first, u);
-    if (u == g.begin || (!d.part && u >= g.begin + q.real)) return;
-    // workgroups first .. first + n - 1 have a part
-    const int64_t first = d.part ? g.begin : d.share_of(g.begin);
-    const int n = d.part ? (int)g.entries : (int)(d.share_of(g.begin + q.real - 1) - first) + 1;
-    const auto part = [&](int k) { return slot_of<D>(p, first + k, k == 0 ? 1 : 0); };
+    const Join j = *join_of<D, kShares<F32, D>>(p, blockIdx.x + 1);
+    const int n = j.n;
+    if (n == 0) return;
+    Seq q = {};
+    q.row = j.row;
+    Segment g = {};
+    g.head = j.head;
+    g.first = j.first;
+    g.count = j.count;
+    const auto part = [&](int k) { return slot_of<D>(p, j.first_share + k, k == 0 ? 1 : 0); };
     const float v_scale = MX ? 1.0f : p.cache.v_scale[g.head];
-    const int items = g.count * (D / 4), rank = (int)(w - first - 1);
+    const int items = g.count * (D / 4), rank = j.rank;
     const int i0 = (int)((int64_t)items * rank / (n - 1)), i1 = (int)((int64_t)items * (rank + 1) / (n - 1));
     // (lanes for all items at once, but no more than have a part)
     if (n < 4 || i1 - i0 > 128) join_items<F32, D, 1>(p, q, g, v_scale, i0, i1, n, part);
@@ -1277,8 +1294,9 @@ __global__ void __launch_bounds__(kThreads) k_kv_prefill_join(const KvAttention 
     }
 }
 
-// Blocks of one kv head at most, and the parts of each: with fewer than 512
-// workgroups (two for each compute unit) each block's keys are split.
+// Blocks of one kv head at most, and the parts of each: with fewer than 1024
+// workgroups (four for each compute unit) each block's keys are split.  (From 512 on
+// three chunks behind up to 16384 positions took 408 us, from 1024 399, from 1280 419.)
 int64_t pre_blocks_most(int64_t rows, int64_t seqs, int group, int dim) {
     const int64_t cols = dim == 256 ? kPreCols<256> : kPreCols<128>;
     return rows * group / cols + std::min(seqs, rows * group / (kFewColumns + 1));
@@ -1286,7 +1304,7 @@ int64_t pre_blocks_most(int64_t rows, int64_t seqs, int group, int dim) {
 
 int pre_splits(int64_t rows, int64_t seqs, int group, int heads, int dim) {
     const int64_t blocks = pre_blocks_most(rows, seqs, group, dim) * heads;
-    return (int)std::max<int64_t>(1, std::min<int64_t>(16, 512 / std::max<int64_t>(1, blocks)));
+    return (int)std::max<int64_t>(1, std::min<int64_t>(16, 1024 / std::max<int64_t>(1, blocks)));
 }
 
 template <bool MX, int D>
@@ -1294,7 +1312,7 @@ hipError_t run_prefill(KvAttention p, hipStream_t s) {
     constexpr int bytes = kPreBuffers<D> * (kPreKBytes<D> + kPreVBytes<D>);
     const int64_t blocks = pre_blocks_most(p.plan.rows, p.plan.seqs, p.group, D) * p.cache.heads;
     p.splits = pre_splits(p.plan.rows, p.plan.seqs, p.group, p.cache.heads, D);
-    p.pre_ws = p.ws + 2 * kShares<false, D> * kSlotFloats<D>;
+    p.pre_ws = p.ws + kShares<false, D> * kShareFloats<D>;
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_kv_prefill<MX, D>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != hipSuccess) return e;
@@ -1327,7 +1345,10 @@ hipError_t run(const KvAttention& p, hipStream_t s) {
 
 size_t kv_attention_workspace_bytes(int64_t rows, int64_t seqs, int q_heads, int kv_heads, int dim, bool bf16) {
     if (rows == 0) return 0;
-    int64_t floats = 2 * (dim == 256 ? kShares<false, 256> : dim == 128 && !bf16 ? kShares<true, 128> : kShares<false, 128>) * (kCols * dim + 2 * kCols);
+    int64_t floats = (dim == 256  ? kShares<false, 256> * kShareFloats<256>
+                      : dim == 64 ? kShares<false, 64> * kShareFloats<64>
+                      : bf16      ? kShares<false, 128> * kShareFloats<128>
+                                  : kShares<true, 128> * kShareFloats<128>);
     const int group = q_heads / kv_heads;
     if (bf16 && rows * group > kFewColumns) {
         const int64_t cols = dim == 256 ? kPreCols<256> : kPreCols<128>;
