@@ -1359,7 +1359,7 @@ size_t kv_attention_workspace_bytes(int64_t rows, int64_t seqs, int q_heads, int
 }
 
 hipError_t launch_kv_attention(const KvAttention& p, hipStream_t s) {
-    if (p.plan.rows == 0) return hipSuccess;
+    if (p.plan.rows == 0 || p.plan.seqs == 0) return hipSuccess;
     const auto pick = [&](auto mx, auto f32) {
         constexpr bool MX = decltype(mx)::value, F32 = decltype(f32)::value;
         if (p.cache.dim == 64) return run<MX, F32, 64>(p, s);

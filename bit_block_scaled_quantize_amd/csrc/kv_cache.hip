@@ -303,7 +303,7 @@ int divide_rows(P& p, int heads) {
 }  // namespace
 
 hipError_t launch_kv_append(KvAppend p, hipStream_t s) {
-    if (p.plan.rows == 0) return hipSuccess;
+    if (p.plan.rows == 0 || p.plan.seqs == 0) return hipSuccess;
     const dim3 grid(divide_rows(p, p.q_heads + 2 * p.cache.heads));
     const auto run = [&](auto t, auto d) {
         using T = decltype(t);
@@ -322,7 +322,7 @@ hipError_t launch_kv_append(KvAppend p, hipStream_t s) {
 }
 
 hipError_t launch_kv_gather(KvGather p, hipStream_t s) {
-    if (p.plan.rows == 0) return hipSuccess;
+    if (p.plan.rows == 0 || p.plan.seqs == 0) return hipSuccess;
     const dim3 grid(divide_rows(p, 2 * p.cache.heads));
     const auto run = [&](auto t, auto d) {
         using T = decltype(t);

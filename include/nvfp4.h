@@ -547,7 +547,8 @@ nvfp4_status nvfp4_expert_gemv(const void* x, int32_t dt /* nvfp4_dtype */, int6
  * Requirements (all calls): head_dim 64, 128 or 256, page_size a power of two
  * of 16 and more (else UNSUPPORTED); width * page_size <= 2^30, seqs <= 65536,
  * rows <= 2^30, pages < 2^31 (else UNSUPPORTED); codes 16-byte aligned.  Rows
- * of heads need only their element's alignment.  rows == 0 is a no-op.
+ * of heads need only their element's alignment.  rows == 0 or seqs == 0 is a
+ * no-op.
  * ---------------------------------------------------------------------- */
 typedef enum { NVFP4_KV_NVFP4 = 0, NVFP4_KV_MXFP4 = 1 } nvfp4_kv_format;
 

@@ -351,3 +351,32 @@ def test_blocks_at_the_ends_of_the_scales(nv):
         nv.nvfp4_kv_append(x, x if mx else x * 0.0, cache, table, L, O)
         torch.cuda.synchronize()
         same(cache, want)
+
+
+@pytest.mark.gpu
+def test_no_sequences_and_no_pages(nv):
+    """Rows of no sequence are left alone; without a page nothing is stored or seen."""
+    k = torch.ones((5, 2, 64)).cuda()
+    q = torch.ones((5, 4, 64)).cuda().bfloat16()
+    cache, _ = make(nv, [16], 2, 64, 16, False)
+    none = torch.zeros((0, 3), dtype=torch.int32).cuda(), torch.zeros(0, dtype=torch.int32).cuda()
+    O = torch.zeros(1, dtype=torch.int32).cuda()
+    out = torch.full_like(k, 3.0)
+    nv.nvfp4_kv_append(k, k, cache, *none, O, q=k[:, :1], out=out[:, :1])
+    nv.nvfp4_kv_gather(cache, *none, O, rows=5, out=(out, out))
+    o = nv.nvfp4_kv_attention(k, cache, *none, O, out=out)
+    assert bool((o == 3.0).all())
+    empty = nv.NVFP4KVCache.empty(0, 2, 64, 16)
+    table = torch.zeros((2, 3), dtype=torch.int32).cuda()
+    for rows, offsets in ((5, [0, 2, 5]), (100, [0, 70, 100])):
+        L, O = torch.tensor([40, 48], dtype=torch.int32).cuda(), torch.tensor(offsets, dtype=torch.int32).cuda()
+        kk, qq = torch.ones((rows, 2, 64)).cuda(), torch.ones((rows, 4, 64)).cuda().bfloat16()
+        nv.nvfp4_kv_append(kk, kk, empty, table, L, O)
+        assert not bool(nv.nvfp4_kv_gather(empty, table, L, O, rows=rows)[0].any())
+        o, lse = nv.nvfp4_kv_attention(qq, empty, table, L, O, lse=True)
+        assert not bool(o.any()) and bool(torch.isinf(lse).all())
+
+
+@pytest.mark.parametrize("which", [0, 1, 2])
+def test_rows_of_no_sequence_launch_nothing(nv, which):
+    assert _calls(nv)[which](_cache(nv), _plan(nv, seqs=0, rows=5, lengths=None, table=None)) == E["OK"]
