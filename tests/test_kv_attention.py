@@ -325,3 +325,86 @@ def test_a_cache_past_32_bits(nv):
     base = torch.where(table >= 0, table - (pages - small.k_codes.shape[0]), -1).to(torch.int32)
     o2, lse2 = nv.nvfp4_kv_attention(q, low, base, L, lse=True)
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_lengths_past_the_table(nv):
+    """A length past what the table's row holds counts as that, a negative one as 0."""
+    cache, table, _, _, _, q = case(nv, [160, 96, 50], None, 2, 4, 128, 16, False, "bf16", seed=28)
+    table[1, 6:] = -1
+    L = torch.tensor([100000, 96, -7], dtype=torch.int32).cuda()
+    o, lse = nv.nvfp4_kv_attention(q, cache, table, L, lse=True)
+    want = P.attention(q, cache, table, [160, 96, 0], None, 128 ** -0.5, 0, cache.k_codes.shape[0], 16)
+    P.check_attention(o, lse, want, "bf16", False)
+    offsets = [0, 90, 100, 103]
+    O = torch.tensor(offsets, dtype=torch.int32).cuda()
+    many = torch.randn((103, 8, 128), generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+    o, lse = nv.nvfp4_kv_attention(many, cache, table, L, O, lse=True)
+    want = P.attention(many, cache, table, [160, 96, 0], offsets, 128 ** -0.5, 0, cache.k_codes.shape[0], 16)
+    P.check_attention(o, lse, want, "bf16", False)
+
+
+@pytest.mark.parametrize("dim,mx", [(64, True), (128, False), (256, False), (256, True)])
+def test_captured_chunks(nv, dim, mx):
+    """Chunks of prompts of changing lengths in a graph, replayed with eager work between."""
+    page, heads, group, rows = 32, 2, 4, 150
+    cache, table = make(nv, [400, 300], heads, dim, page, mx, seed=29)
+    fill(nv, cache, table, [400, 300], 29)
+    g = torch.Generator(device="cuda").manual_seed(30)
+    q = torch.zeros((rows, heads * group, dim), device="cuda").bfloat16()
+    L = torch.tensor([400, 300], dtype=torch.int32).cuda()
+    O = torch.tensor([0, 100, 150], dtype=torch.int32).cuda()
+    ws = torch.empty(nv.nvfp4_kv_attention_workspace_size(rows, 2, heads * group, heads, dim), dtype=torch.uint8, device="cuda")
+    nv.nvfp4_kv_attention(q, cache, table, L, O, workspace=ws)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = nv.nvfp4_kv_attention(q, cache, table, L, O, workspace=ws)
+    for lengths, offsets in (([400, 300], [0, 100, 150]), ([150, 10], [0, 140, 150]), ([399, 1], [0, 149, 150]),
+                             ([64, 300], [0, 3, 150])):
+        q.copy_(torch.randn(q.shape, generator=g, device="cuda"))
+        L.copy_(torch.tensor(lengths, dtype=torch.int32))
+        O.copy_(torch.tensor(offsets, dtype=torch.int32))
+        graph.replay()
+        ref = nv.nvfp4_kv_attention(q, cache, table, L, O)
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref), (lengths, offsets)
+
+
+def test_two_calls_at_once(nv):
+    """Two streams, each with its own workspace, on one cache."""
+    cache, table, L, O, offsets, q = case(nv, [5000, 700], [1, 1], 2, 4, 128, 64, False, "bf16", seed=31)
+    many = torch.randn((200, 8, 128), generator=torch.Generator().manual_seed(3)).bfloat16().cuda()
+    OM = torch.tensor([0, 120, 200], dtype=torch.int32).cuda()
+    ref = nv.nvfp4_kv_attention(q, cache, table, L, O), nv.nvfp4_kv_attention(many, cache, table, L, OM)
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for _ in range(5):
+        got.append((nv.nvfp4_kv_attention(q, cache, table, L, O, stream=a), nv.nvfp4_kv_attention(many, cache, table, L, OM, stream=b)))
+    torch.cuda.synchronize()
+    for x, y in got:
+        assert torch.equal(x, ref[0]) and torch.equal(y, ref[1])
+
+
+def test_a_row_that_is_not_finite(nv):
+    """It is unspecified; the others are theirs."""
+    for lengths, offsets in (([300, 64], [0, 4, 9]), ([300, 200], [0, 100, 150])):
+        cache, table = make(nv, lengths, 2, 128, 16, False, seed=32)
+        fill(nv, cache, table, lengths, 32)
+        L, O = torch.tensor(lengths, dtype=torch.int32).cuda(), torch.tensor(offsets, dtype=torch.int32).cuda()
+        q = torch.randn((offsets[-1], 8, 128), generator=torch.Generator().manual_seed(4)).bfloat16().cuda()
+        ref = nv.nvfp4_kv_attention(q, cache, table, L, O)
+        bad = q.clone()
+        bad[1, 2, 5] = float("inf")
+        bad[3, 4] = float("nan")
+        got = nv.nvfp4_kv_attention(bad, cache, table, L, O)
+        keep = torch.ones(q.shape[:2], dtype=torch.bool)
+        keep[1, 2] = keep[3, 4] = False
+        # (a block's rescaling may come earlier for its other columns: the last bits)
+        off = (got.double() - ref.double()).abs()[keep]
+        assert bool((off <= 2.0 ** -7 * ref.double().abs()[keep] + 1e-4).all())
+
+
+@pytest.mark.parametrize("page", [16, 1024, 4096])
+def test_page_sizes(nv, page):
+    run_and_check(nv, [1500, 17, 4096], None, 2, 4, 128, page, False, "bf16", seed=33)
+    run_and_check(nv, [1500, 60], [130, 60], 2, 4, 128, page, True, "bf16", seed=34)
