@@ -920,24 +920,29 @@ __device__ __forceinline__ bool pre_find(const KvAttention& p, int64_t index, in
     }
 }
 
-// What workgroup `id` of k_kv_prefill does: columns of a kv head (neighbouring
+// What a workgroup of k_kv_prefill does: columns `id` of a kv head (neighbouring
 // workgroups have different heads, so that with 8 of them one head's keys stay
-// in one XCD's L2) and the split-th part of its tiles.
+// in one XCD's L2) and the split-th of `parts` equal parts of its tiles, of which
+// there are as many as leave each kLeastTiles; a workgroup past them has none.
+// (40 heads of 128, 8 kv heads: 2048 rows take 91 us, 130 with parts of any size,
+// which cost a slot's bytes each; 512 rows behind 3584 74 and 131; 64 behind 8128 56
+// and 75.  Least parts of 8 or 24 tiles: 112 and 91, 105 and 89, 48 and 71.  A block's
+// parts beside each other: 1024 rows 61 instead of 57, 512 behind 3584 105, three
+// chunks behind up to 16384 402 instead of 408.)
+constexpr int kLeastTiles = 16;
 struct PreWork {
     Seq q;
     Segment g;
-    int s, split, from, to;  // tiles of keys
+    int s, parts, from, to;  // tiles of keys
     int64_t slot;  // of the workspace
 };
 
 template <int D>
-__device__ __forceinline__ bool pre_work(const KvAttention& p, int64_t id, PreWork& w) {
-    w.slot = id;
+__device__ __forceinline__ bool pre_work(const KvAttention& p, int64_t id, int split, PreWork& w) {
+    w.slot = id + split * p.blocks;
     w.g.head = (int)(id % p.cache.heads);
-    id /= p.cache.heads;
-    w.split = (int)(id % p.splits);
     int block;
-    if (!pre_find<D>(p, id / p.splits, w.s, block)) return false;
+    if (!pre_find<D>(p, id / p.cache.heads, w.s, block)) return false;
     kv_rows(p.plan, w.s, w.q.row, w.q.rows);
     w.q.length = kv_length(p.plan, w.s);
     w.g.first = block * kPreCols<D>;
@@ -946,9 +951,11 @@ __device__ __forceinline__ bool pre_work(const KvAttention& p, int64_t id, PreWo
     const int first = pos0 + w.g.first / p.group, last = pos0 + (w.g.first + w.g.count - 1) / p.group;
     const int low = p.window ? max(0, first - p.window + 1) / kTile : 0;
     const int tiles = last >= 0 && p.cache.pages > 0 ? last / kTile + 1 - low : 0;  // (without a page nothing is seen)
-    const int each = (tiles + p.splits - 1) / p.splits;
-    w.from = low + min(tiles, w.split * each);
-    w.to = low + min(tiles, (w.split + 1) * each);
+    w.parts = max(1, min(p.splits, tiles / kLeastTiles));
+    if (split >= w.parts) return false;
+    const int each = (tiles + w.parts - 1) / w.parts;
+    w.from = low + min(tiles, split * each);
+    w.to = low + min(tiles, (split + 1) * each);
     return true;
 }
 
@@ -965,7 +972,10 @@ __global__ void __launch_bounds__(64 * kPreWaves<D>, kPreWaves<D> / 4) k_kv_pref
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 31, h = lane >> 5;
     PreWork work;
-    if (!pre_work<D>(p, blockIdx.x, work)) return;
+    // (the last parts first: the first ones, which every block has, fill up behind them)
+    const int split = p.splits - 1 - (int)(blockIdx.x / p.blocks);
+    const int64_t id = blockIdx.x % p.blocks;
+    if (!pre_work<D>(p, id, split, work)) return;
     const Seq& q = work.q;
     const Segment& g = work.g;
     const int pos0 = q.length - q.rows;
@@ -1243,7 +1253,7 @@ __global__ void __launch_bounds__(64 * kPreWaves<D>, kPreWaves<D> / 4) k_kv_pref
     }
     const int lc = 32 * wave + col;  // column of the block
     if (lc >= g.count) return;
-    if (p.splits > 1) {
+    if (work.parts > 1) {
         float* slot = p.pre_ws + work.slot * kPreSlotFloats<D>;
         if (j0 < j1)
 #pragma unroll
@@ -1274,8 +1284,8 @@ template <bool MX, int D>
 __global__ void __launch_bounds__(kThreads) k_kv_prefill_join(const KvAttention p) {
     constexpr int pieces = kPreCols<D> / kJoinCols;
     PreWork work;
-    const int64_t id = blockIdx.x / pieces, first = id / p.cache.heads * p.splits * p.cache.heads + id % p.cache.heads;
-    if (!pre_work<D>(p, first, work)) return;
+    const int64_t id = blockIdx.x / pieces;
+    if (!pre_work<D>(p, id, 0, work) || work.parts == 1) return;
     const float v_scale = MX ? 1.0f : p.cache.v_scale[work.g.head];
     const int c0 = (int)(blockIdx.x % pieces) * kJoinCols;
     for (int i = threadIdx.x; i < kJoinCols * (D / 4); i += kThreads) {
@@ -1283,13 +1293,15 @@ __global__ void __launch_bounds__(kThreads) k_kv_prefill_join(const KvAttention 
         if (cc >= work.g.count) return;
         float top = kLowest, total = 0.0f;
         v4f_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int k = 0; k < p.splits; ++k) {
-            const float* slot = p.pre_ws + (first + (int64_t)k * p.cache.heads) * kPreSlotFloats<D>;
+#pragma unroll 4
+        for (int k = 0; k < work.parts; ++k) {
+            const float* slot = p.pre_ws + (id + k * p.blocks) * kPreSlotFloats<D>;
             const float l = slot[kPreCols<D> * (D + 1) + cc];
-            if (!(l > 0.0f)) continue;  // (an empty part has written no sums)
             const float m = slot[kPreCols<D> * D + cc], next = fmaxf(top, m);
             const float f = __builtin_amdgcn_exp2f(top - next), e = __builtin_amdgcn_exp2f(m - next);
-            const v4f_t x = *reinterpret_cast<const v4f_t*>(slot + cc * D + d);
+            v4f_t x = *reinterpret_cast<const v4f_t*>(slot + cc * D + d);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[r] = l > 0.0f ? x[r] : 0.0f;  // (an empty part has written no sums)
             total = total * f + l * e;
 #pragma unroll
             for (int r = 0; r < 4; ++r) sum[r] = sum[r] * f + x[r] * e;
@@ -1303,9 +1315,10 @@ __global__ void __launch_bounds__(kThreads) k_kv_prefill_join(const KvAttention 
     }
 }
 
-// Blocks of one kv head at most, and the parts of each: with fewer than 1024
-// workgroups (four for each compute unit) each block's keys are split.  (From 512 on
-// three chunks behind up to 16384 positions took 408 us, from 1024 399, from 1280 419.)
+// Blocks of one kv head at most, and the most parts of each: with fewer than 1024
+// workgroups (four for each compute unit) a block's keys may be split.  (With up to 512
+// three chunks behind up to 16384 positions took 408 us, with 1024 399, with 1280 419;
+// with 1536, which splits the blocks of 4096 rows, these took 270 instead of 229.)
 int64_t pre_blocks_most(int64_t rows, int64_t seqs, int group, int dim) {
     const int64_t cols = dim == 256 ? kPreCols<256> : kPreCols<128>;
     return rows * group / cols + std::min(seqs, rows * group / (kFewColumns + 1));
@@ -1320,6 +1333,7 @@ template <bool MX, int D>
 hipError_t run_prefill(KvAttention p, hipStream_t s) {
     constexpr int bytes = kPreBuffers<D> * (kPreKBytes<D> + kPreVBytes<D>);
     const int64_t blocks = pre_blocks_most(p.plan.rows, p.plan.seqs, p.group, D) * p.cache.heads;
+    p.blocks = blocks;
     p.splits = pre_splits(p.plan.rows, p.plan.seqs, p.group, p.cache.heads, D);
     p.pre_ws = p.ws + kShares<false, D> * kShareFloats<D>;
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_kv_prefill<MX, D>),

@@ -267,8 +267,9 @@ struct KvAttention {
     float scale;
     bool bf16;
     float* ws;
-    int splits;     // of the keys of many rows; set by the launcher, as
-    float* pre_ws;  // its part of ws
+    int64_t blocks;  // of many rows, in all kv heads, and the most parts that each
+    int splits;      // one's keys are split into; set by the launcher, as
+    float* pre_ws;   // their part of ws
 };
 size_t kv_attention_workspace_bytes(int64_t rows, int64_t seqs, int q_heads, int kv_heads, int dim, bool bf16);
 hipError_t launch_kv_attention(const KvAttention& p, hipStream_t s);

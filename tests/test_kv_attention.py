@@ -408,3 +408,12 @@ def test_a_row_that_is_not_finite(nv):
 def test_page_sizes(nv, page):
     run_and_check(nv, [1500, 17, 4096], None, 2, 4, 128, page, False, "bf16", seed=33)
     run_and_check(nv, [1500, 60], [130, 60], 2, 4, 128, page, True, "bf16", seed=34)
+
+
+@pytest.mark.parametrize("dim,mx", [(64, False), (128, True), (256, False)])
+def test_parts_of_chunks(nv, dim, mx):
+    """Blocks whose keys are split beside ones that are not, and one row more or less
+    than a part's least."""
+    run_and_check(nv, [2100, 300, 1023, 1024, 1025, 2047, 2048, 2049], [70, 300, 40, 40, 40, 33, 33, 33], 1, 4, dim, 64, mx,
+                  "bf16", seed=35)
+    run_and_check(nv, [4000, 65], [65, 65], 2, 2, dim, 32, mx, "bf16", window=1500, seed=36)
