@@ -62,10 +62,8 @@ constexpr int kStep = 32;     // keys of a unit of work
 constexpr int kTile = 64;     // keys of a tile of k_kv_prefill
 constexpr float kLowest = -3.402823466e38f;
 // Weights are taken over a maximum that may lie up to kSlack (in powers of two)
-// below the true one, so that the sums are rescaled seldom, and times 2^kBias,
-// so that they reach FP16's largest: half a step of its subnormal numbers is
-// then 2^-36 of the largest weight.
-constexpr float kBias = 11.0f, kSlack = 4.0f;
+// below the true one, so that the sums are rescaled seldom.
+constexpr float kSlack = 4.0f;
 // Sequences of more columns than this for a kv head are k_kv_prefill's (BF16 q).  (64
 // sequences of 4096 positions, by k_kv_attention and k_kv_prefill: 40 columns 174 and
 // 202 us, 60 columns 199 and 204, 80 columns 266 and 208; 4 sequences, 60 columns 34
@@ -119,7 +117,7 @@ struct Form<true> {
 // Parts of q: a BF16 value fits FP16 once its row is scaled to [2^14, 2^15) (an
 // element below 2^-29 of the row's largest keeps 2^-25 of 2^14, past the
 // products' binary32 sums), a binary32 one two FP16 or three BF16 parts.  Parts
-// of a weight in [0, 2^kBias]: one FP16 part is off by 2^-12, two BF16 parts by
+// of a weight: one FP16 part is off by 2^-12, two BF16 parts by
 // 2^-17, of binary32 results two FP16 parts by 2^-23, three BF16 parts by 2^-25.
 template <bool MX, bool F32>
 constexpr int kQParts = F32 ? (MX ? 3 : 2) : 1;
@@ -147,6 +145,19 @@ __device__ __forceinline__ void split8(const float v[8], typename Form<MX>::v8 o
         }
         out[i] = __builtin_bit_cast(typename Form<MX>::v8, r);
     }
+}
+
+// Weights are taken times 2^bias.  FP16: so that they reach its largest; half a step
+// of its subnormal numbers is then 2^-36 of the largest weight.  BF16 has no such
+// limit, but MXFP4's values go up to binary32's own: the weights of all keys that a
+// row sees add up to at most one (and some 9% that rounding far scores may add), so
+// that no sum of products passes 1.1 x 6 x 2^125.  (The matrix cores keep subnormal
+// numbers: results of small values lose bits below 2^-126 / 2^bias, but not at once.)
+template <bool MX>
+__device__ __forceinline__ float weight_bias(const KvAttention& p, int length) {
+    if constexpr (!MX) return 11.0f;
+    const int keys = p.window ? min(length, p.window) : length;
+    return -kSlack - (float)(keys > 1 ? 32 - __clz(keys - 1) : 0);
 }
 
 // The sum of 8 values, in pairs (a sum one by one waits for each addition).
@@ -403,7 +414,8 @@ __device__ __forceinline__ float* slot_of(const KvAttention& p, int64_t w, int w
 // workgroups first_share and on.  n 0: nothing.  (Found again there, it took one token
 // over 8192 positions took 15.4 us instead of 14.3.)
 struct Join {
-    int n, rank, first_share, row, head, first, count, unused;
+    int n, rank, first_share, row, head, first, count;
+    float bias;
 };
 template <int D>
 constexpr int64_t kShareFloats = 2 * kSlotFloats<D> + sizeof(Join) / sizeof(float);
@@ -426,10 +438,11 @@ __device__ __forceinline__ void store_out(const KvAttention& p, const Seq& q, co
     }
 }
 
-__device__ __forceinline__ void store_lse(const KvAttention& p, const Seq& q, const Segment& g, int c, float m, float l) {
+__device__ __forceinline__ void store_lse(const KvAttention& p, const Seq& q, const Segment& g, int c, float m, float bias,
+                                          float l) {
     const int64_t row = q.row + (g.first + c) / p.group;
     const int head = g.head * p.group + (g.first + c) % p.group;
-    p.lse[row * p.q_heads + head] = l > 0.0f ? (m - kBias + __builtin_log2f(l)) * 0.6931471805599453f : -INFINITY;
+    p.lse[row * p.q_heads + head] = l > 0.0f ? (m - bias + __builtin_log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
 // Keys of a sub-tile of 16 in a lane: codes and scale bytes.
@@ -549,6 +562,8 @@ __global__ void __launch_bounds__(kThreads, (kShares<F32, D> / 256)) k_kv_attent
         const int low_first = p.window ? max(0, pos_first - p.window + 1) : 0;
         const int low_last = p.window ? max(0, pos_last - p.window + 1) : 0;
 
+        const float bias = weight_bias<MX>(p, q.length);
+
         // steps of 32 keys that some column sees
         const int j1 = min(q.first_step + to, pos_last < 0 ? 0 : pos_last / kStep + 1);
         int j = max(q.first_step + from, low_first / kStep) + member;
@@ -582,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, (kShares<F32, D> / 256)) k_kv_attent
             const int64_t first = d.part ? g.begin : d.share_of(g.begin);
             const int n = d.part ? (int)g.entries : (int)(d.share_of(g.begin + q.real - 1) - first) + 1;
             *join_of<D, kShares<F32, D>>(p, blockIdx.x) =
-                Join{n, (int)(blockIdx.x - first) - 1, (int)first, q.row, g.head, g.first, g.count, 0};
+                Join{n, (int)(blockIdx.x - first) - 1, (int)first, q.row, g.head, g.first, g.count, bias};
         }
 
         // q, its row scaled into FP16's range
@@ -697,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, (kShares<F32, D> / 256)) k_kv_attent
 #pragma unroll
                     for (int r = 0; r < 4; ++r) o[i][r] *= f;
             }
-            const float base = m - kBias;
+            const float base = m - bias;
             float w[8];
 #pragma unroll
             for (int t = 0; t < 2; ++t)
@@ -734,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, (kShares<F32, D> / 256)) k_kv_attent
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i)
                     store_out<F32>(p, q, g, col, 16 * i + 4 * g4, v4f_t{o[i][0] * f, o[i][1] * f, o[i][2] * f, o[i][3] * f});
-                if (p.lse && g4 == 0) store_lse(p, q, g, col, m, l);
+                if (p.lse && g4 == 0) store_lse(p, q, g, col, m, bias, l);
             }
             u += (int64_t)gridDim.x * kWaves;
             continue;
@@ -770,7 +785,7 @@ __global__ void __launch_bounds__(kThreads, (kShares<F32, D> / 256)) k_kv_attent
 #pragma unroll
                 for (int r = 0; r < 4; ++r) sum[r] *= f;
                 store_out<F32>(p, q, g, cc, d4, sum);
-                if (p.lse && d4 == 0) store_lse(p, q, g, cc, top, total);
+                if (p.lse && d4 == 0) store_lse(p, q, g, cc, top, bias, total);
             } else {
                 *reinterpret_cast<v4f_t*>(slot + cc * D + d4) = sum;
                 if (d4 == 0) {
@@ -796,8 +811,8 @@ __device__ __forceinline__ float reduce_lanes(float x, Op op) {
 }
 
 template <bool F32, int D, int LANES, typename Part>
-__device__ __forceinline__ void join_items(const KvAttention& p, const Seq& q, const Segment& g, float v_scale, int i0, int i1,
-                                           int n, Part part) {
+__device__ __forceinline__ void join_items(const KvAttention& p, const Seq& q, const Segment& g, float bias, float v_scale, int i0,
+                                           int i1, int n, Part part) {
     const int at = threadIdx.x / LANES, k0 = threadIdx.x % LANES;
     for (int b = i0; b < i1; b += kThreads / LANES) {  // (the same in all lanes)
         const int i = min(b + at, i1 - 1), c = i / (D / 4), d = 4 * (i % (D / 4));
@@ -821,7 +836,7 @@ __device__ __forceinline__ void join_items(const KvAttention& p, const Seq& q, c
         for (int r = 0; r < 4; ++r) sum[r] = reduce_lanes<LANES>(sum[r] * e, AddOp()) * f;
         if (k0 == 0 && b + at < i1) {
             store_out<F32>(p, q, g, c, d, sum);
-            if (p.lse && d == 0) store_lse(p, q, g, c, most, total);
+            if (p.lse && d == 0) store_lse(p, q, g, c, most, bias, total);
         }
     }
 }
@@ -842,10 +857,10 @@ __global__ void __launch_bounds__(kThreads) k_kv_join(const KvAttention p) {
     const int items = g.count * (D / 4), rank = j.rank;
     const int i0 = (int)((int64_t)items * rank / (n - 1)), i1 = (int)((int64_t)items * (rank + 1) / (n - 1));
     // (lanes for all items at once, but no more than have a part)
-    if (n < 4 || i1 - i0 > 128) join_items<F32, D, 1>(p, q, g, v_scale, i0, i1, n, part);
-    else if (n < 16 || i1 - i0 > 32) join_items<F32, D, 4>(p, q, g, v_scale, i0, i1, n, part);
-    else if (n < 64 || i1 - i0 > 8) join_items<F32, D, 16>(p, q, g, v_scale, i0, i1, n, part);
-    else join_items<F32, D, 64>(p, q, g, v_scale, i0, i1, n, part);
+    if (n < 4 || i1 - i0 > 128) join_items<F32, D, 1>(p, q, g, j.bias, v_scale, i0, i1, n, part);
+    else if (n < 16 || i1 - i0 > 32) join_items<F32, D, 4>(p, q, g, j.bias, v_scale, i0, i1, n, part);
+    else if (n < 64 || i1 - i0 > 8) join_items<F32, D, 16>(p, q, g, j.bias, v_scale, i0, i1, n, part);
+    else join_items<F32, D, 64>(p, q, g, j.bias, v_scale, i0, i1, n, part);
 }
 
 // ---------------------------------------------------------------- many rows
@@ -999,6 +1014,8 @@ __global__ void __launch_bounds__(64 * kPreWaves<D>, kPreWaves<D> / 4) k_kv_pref
     const int wpos_first = pos0 + wfirst / p.group, wpos_last = idle ? -1 : pos0 + wlast / p.group;
     const int wlow_first = p.window ? max(0, wpos_first - p.window + 1) : 0;
     const int wlow_last = p.window ? max(0, wpos_last - p.window + 1) : 0;
+
+    const float bias = weight_bias<MX>(p, q.length);
 
     v8 qf[KS];
     float factor = fabsf(p.scale) * kLog2e;
@@ -1183,7 +1200,7 @@ __global__ void __launch_bounds__(64 * kPreWaves<D>, kPreWaves<D> / 4) k_kv_pref
 #pragma unroll
                 for (int r = 0; r < 16; ++r) o[i][r] *= f;
         }
-        const float base = m - kBias;
+        const float base = m - bias;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             float w[8];
@@ -1286,7 +1303,7 @@ __global__ void __launch_bounds__(64 * kPreWaves<D>, kPreWaves<D> / 4) k_kv_pref
         for (int r = 0; r < 4; ++r)
             store_out<false>(p, q, g, lc, 32 * i + 8 * r + 4 * h,
                              v4f_t{o[i][4 * r] * f, o[i][4 * r + 1] * f, o[i][4 * r + 2] * f, o[i][4 * r + 3] * f});
-    if (p.lse && h == 0) store_lse(p, q, g, lc, m, l);
+    if (p.lse && h == 0) store_lse(p, q, g, lc, m, bias, l);
 }
 
 // The parts of a block, joined in order: kJoinCols of its columns.
@@ -1297,7 +1314,7 @@ __global__ void __launch_bounds__(kThreads) k_kv_prefill_join(const KvAttention 
     PreWork work;
     const int64_t id = blockIdx.x / pieces;
     if (!pre_work<D>(p, id, 0, work) || work.parts == 1) return;
-    const float v_scale = MX ? 1.0f : p.cache.v_scale[work.g.head];
+    const float v_scale = MX ? 1.0f : p.cache.v_scale[work.g.head], bias = weight_bias<MX>(p, work.q.length);
     const int c0 = (int)(blockIdx.x % pieces) * kJoinCols;
     for (int i = threadIdx.x; i < kJoinCols * (D / 4); i += kThreads) {
         const int cc = c0 + i / (D / 4), d = 4 * (i % (D / 4));
@@ -1322,7 +1339,7 @@ __global__ void __launch_bounds__(kThreads) k_kv_prefill_join(const KvAttention 
 #pragma unroll
         for (int r = 0; r < 4; ++r) sum[r] *= f;
         store_out<false>(p, work.q, work.g, cc, d, sum);
-        if (p.lse && d == 0) store_lse(p, work.q, work.g, cc, top, total);
+        if (p.lse && d == 0) store_lse(p, work.q, work.g, cc, top, bias, total);
     }
 }
 
