@@ -64,6 +64,12 @@ constexpr float kLowest = -3.402823466e38f;
 // Weights are taken over a maximum that may lie up to kSlack (in powers of two)
 // below the true one, so that the sums are rescaled seldom.
 constexpr float kSlack = 4.0f;
+// exp2(score - maximum + bias) is one multiply-add before the exponential while the
+// maxima are no further than this from 0: what m - bias and the product round is then
+// below 2^-3 in the exponent, and the weight below 2^15.2.  Further away that rounding
+// would pass FP16's largest (or all bounds), so scores are rounded to binary32 first
+// and the maximum, the true one of all keys so far, taken off exactly.
+constexpr float kFar = 1048576.0f;
 // Sequences of more columns than this for a kv head are k_kv_prefill's (BF16 q).  (64
 // sequences of 4096 positions, by k_kv_attention and k_kv_prefill: 40 columns 174 and
 // 202 us, 60 columns 199 and 204, 80 columns 266 and 208; 4 sequences, 60 columns 34
@@ -639,6 +645,8 @@ __global__ void __launch_bounds__(kThreads, (kShares<F32, D> / 256)) k_kv_attent
         }
 
         float m = kLowest, l = 0.0f;
+        // weights are exp2(score x times - base) of scores up to `limit`
+        float limit = m, times = factor, base = m - bias;
         v4f_t o[D / 16];
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) o[i] = v4f_t{0.0f, 0.0f, 0.0f, 0.0f};
@@ -703,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, (kShares<F32, D> / 256)) k_kv_attent
                 half_pair(fmaxf(a, b), a, b);
                 top = fmaxf(a, b) * factor;
             }
-            if (__any(top > m + kSlack)) {
+            if (__any(top > limit)) {
                 const float next = fmaxf(m, top), f = __builtin_amdgcn_exp2f(m - next);
                 m = next;
                 l *= f;
@@ -711,13 +719,24 @@ __global__ void __launch_bounds__(kThreads, (kShares<F32, D> / 256)) k_kv_attent
                 for (int i = 0; i < D / 16; ++i)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) o[i][r] *= f;
+                limit = m + kSlack;
+                times = factor;
+                base = m - bias;
+                if (__any(fabsf(m) > kFar && m > kLowest)) {
+                    limit = -INFINITY;
+                    times = 1.0f;
+                    base = -bias;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) sc[t][r] = sc[t][r] * factor - m;
+                }
             }
-            const float base = m - bias;
             float w[8];
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) w[4 * t + r] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][r], factor, -base));
+                for (int r = 0; r < 4; ++r) w[4 * t + r] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][r], times, -base));
             v8 pf[PP];
             split8<MX, PP>(w, pf);
             l += sum8(w);
@@ -1109,14 +1128,10 @@ __global__ void __launch_bounds__(64 * kPreWaves<D>, kPreWaves<D> / 4) k_kv_pref
     };
     const auto stage_v = [&](const Raw& r, bool there, int b) { stage(r, there, v_lds + b * kPreVBytes<D> + lkey * kPreV<D>); };
 
-    float m = kLowest, l = 0.0f;
+    float m, l;
     v16f_t o[DB], sc[2];
     v8 pf[4][PP];
     uint32_t holes = 0;  // bit i: keys 16 i and on of the tile have no page
-#pragma unroll
-    for (int i = 0; i < DB; ++i)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) o[i][r] = 0.0f;
 
     // The operands of the products are read from LDS kDepth products ahead, in the
     // order that is written here: left to itself the compiler reads each right before
@@ -1167,7 +1182,8 @@ __global__ void __launch_bounds__(64 * kPreWaves<D>, kPreWaves<D> / 4) k_kv_pref
     };
     // (`also`: the rest of the phase, where the compiler mixes its instructions in: 704
     // us instead of 730 after it, 766 before the exponentials; prefill of 8192 rows)
-    const auto softmax = [&](int j, auto also) {
+    const auto softmax = [&](int j, auto exact, auto also) {
+        constexpr bool kExact = decltype(exact)::value;
         const int key0 = j * kTile;
         if (holes || key0 + kTile - 1 > wpos_first || key0 < wlow_last) {
             int first = key0;
@@ -1191,7 +1207,7 @@ __global__ void __launch_bounds__(64 * kPreWaves<D>, kPreWaves<D> / 4) k_kv_pref
         float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
         half_pair(top, a0, a1);
         top = fmaxf(a0, a1) * factor;
-        if (__any(top > m + kSlack)) {
+        if (__any(top > (kExact ? m : m + kSlack))) {
             const float next = fmaxf(m, top), f = __builtin_amdgcn_exp2f(m - next);
             m = next;
             l *= f;
@@ -1205,7 +1221,10 @@ __global__ void __launch_bounds__(64 * kPreWaves<D>, kPreWaves<D> / 4) k_kv_pref
         for (int u = 0; u < 4; ++u) {
             float w[8];
 #pragma unroll
-            for (int r = 0; r < 8; ++r) w[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[u >> 1][8 * (u & 1) + r], factor, -base));
+            for (int r = 0; r < 8; ++r) {
+                const float x = sc[u >> 1][8 * (u & 1) + r];
+                w[r] = __builtin_amdgcn_exp2f(kExact ? (x * factor - m) + bias : __builtin_fmaf(x, factor, -base));
+            }
             split8<MX, PP>(w, pf[u]);
             l += sum8(w);
         }
@@ -1219,7 +1238,14 @@ __global__ void __launch_bounds__(64 * kPreWaves<D>, kPreWaves<D> / 4) k_kv_pref
     };
 
     constexpr int NB = kPreBuffers<D>, KA = NB == 3 ? 2 : 1;  // tiles that keys are ahead (values: one less)
-    if (j0 < j1) {
+    const auto all_tiles = [&](auto exact) {
+        m = kLowest;
+        l = 0.0f;
+#pragma unroll
+        for (int i = 0; i < DB; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) o[i][r] = 0.0f;
+        if (j0 >= j1) return;
         int entry[4];  // of the key in tiles j0 .. j0 + 3
 #pragma unroll
         for (int i = 0; i < KA + 2; ++i) entry[i] = find_entry(j0 + i);
@@ -1266,14 +1292,25 @@ __global__ void __launch_bounds__(64 * kPreWaves<D>, kPreWaves<D> / 4) k_kv_pref
                     rk[0] = load(k_at.slot, p.cache.k_codes, p.cache.k_scales);
                     next = find_entry(j + KA + 2);
                 };
-                if (active) softmax(j, convert);
+                if (active) softmax(j, exact, convert);
                 else convert();
             }
             phase_end();
             b = after;
         }
         if (NB == 3 && wave < 4) phase_end();
-    }
+    };
+    // Where some score was far the tiles are gone over again, with exact differences: the
+    // maximum is still far, or a weight that passed its type's largest has left what is no
+    // number, which no later rescaling takes away.  (A choice between the two in every tile
+    // cost 1 to 5% of the time, as one more branch or as scores that two branches write.)
+    __shared__ int some_far;
+    if (threadIdx.x == 0) some_far = 0;
+    all_tiles(std::false_type());
+    const float seen_of_all = fabsf(l) + fabsf(o[0][0]);
+    if ((fabsf(m) > kFar && m > kLowest) || !(seen_of_all < INFINITY)) some_far = 1;
+    __syncthreads();
+    if (some_far) all_tiles(std::true_type());
     {
         float a, b;
         half_pair(l, a, b);

@@ -88,3 +88,86 @@ def test_many_equal_values_at_mxfp4s_largest(nv, dtype, rows):
     assert off <= 1e-5 + torch.finfo(DT[dtype]).eps / 2 + 2.0 ** -17, off
     want = torch.log(torch.arange(n - rows + 1, n + 1, dtype=torch.float64)).view(-1, 1).cuda()
     assert (lse.double() - want).abs().max().item() <= 2e-5 * math.log(n)
+
+
+# ---------------------------------------------------------------- scores
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("e", [20, 22, 24, 25, 26, 27, 28, 30, 40, 100])
+@pytest.mark.parametrize("dim,dtype,new", FORMS)
+def test_scores_of_any_size(nv, dim, dtype, new, e, mx):
+    n = sum(LENGTHS)
+    cache, table = held(nv, LENGTHS, normal(5, n, 2, dim), normal(6, n, 2, dim), 32, mx)
+    q = normal(7, rows_of(new), 6, dim).to(DT[dtype])
+    attend_and_check(nv, LENGTHS, new, q, cache, table, 32, mx, dtype, dim ** -0.5 * 2.0 ** e)
+
+
+def steps(nv, n, dim, mx, v, t):
+    """Keys whose products with q = (2^14, 2^-6, 0 ...) are 6 x 2^14 + 2^-6 t: neighbouring
+    binary32 numbers for neighbouring t."""
+    k = torch.zeros((n, 1, dim), device="cuda")
+    k[:, 0, 0] = 6.0
+    k[:, 0, 1] = t
+    cache, table = held(nv, [n], k, v, 64, mx, k_scale=1.0, v_scale=0.01)
+    got = nv.nvfp4_kv_gather(cache, table, ints([n]), ints([0, n]), rows=n, dtype=torch.float32)
+    assert torch.equal(got[0], k)
+    return cache, table, got[1].double()
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("most", [2.0 ** 21, 1.2 * 2.0 ** 25, 1.5 * 2.0 ** 26, 1.5 * 2.0 ** 27, 1.9 * 2.0 ** 29, 2.0 ** 60])
+@pytest.mark.parametrize("dtype,rows", [("bf16", 1), ("f32", 1), ("bf16", 70)])
+def test_a_maximum_that_grows_by_a_unit_in_the_last_place(nv, dtype, rows, most, mx):
+    """Scores (in powers of two) of `most` that rise along the sequence by steps of the last
+    bit.  Values of one: whatever the weights, their mean is one; its weights add up to at
+    least that of the last key and at most that of all keys at the last score."""
+    n, dim = 500, 64
+    t = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6], device="cuda")[torch.arange(n, device="cuda") // 64]
+    cache, table, v = steps(nv, n, dim, mx, torch.ones((n, 1, dim), device="cuda"), t)
+    q = torch.zeros((rows, 1, dim), device="cuda")
+    q[..., 0] = 2.0 ** 14
+    q[..., 1] = 2.0 ** -6
+    scale = most / (6 * 2.0 ** 14) * math.log(2.0)
+    o, lse = nv.nvfp4_kv_attention(q.to(DT[dtype]), cache, table, ints([n]), ints([0, rows]), scale=scale, lse=True)
+    off = (o.double() / v[0, 0] - 1.0).abs().max().item()
+    assert off <= P.WEIGHT[dtype, mx] + 1e-5 + torch.finfo(DT[dtype]).eps / 2, off
+    # 2^-24 each: the scale in binary32, log2(e), their product, the sum of products, the score's product, the sum with
+    # the weights' logarithm, log(2), its product
+    top = scale * (6 * 2.0 ** 14 + 2.0 ** -6 * 6)
+    tol = 8 * 2.0 ** -24 * top + 1e-4
+    assert bool((lse.double() >= top - tol).all()) and bool((lse.double() <= top + math.log(n) + tol).all())
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("most", [2.0 ** 21, 1.2 * 2.0 ** 25, 1.5 * 2.0 ** 27, 2.0 ** 60])
+@pytest.mark.parametrize("dtype,rows", [("bf16", 1), ("f32", 1), ("bf16", 70)])
+def test_equal_scores_of_any_size_give_the_mean(nv, dtype, rows, most, mx):
+    n, dim = 500, 64
+    cache, table, v = steps(nv, n, dim, mx, normal(8, n, 1, dim), 3.0)
+    q = torch.zeros((rows, 1, dim), device="cuda")
+    q[..., 0] = 2.0 ** 14
+    scale = -most / (6 * 2.0 ** 14) if rows == 1 else most / (6 * 2.0 ** 14)
+    o = nv.nvfp4_kv_attention(q.to(DT[dtype]), cache, table, ints([n]), ints([0, rows]), scale=scale)
+    for r in range(rows):
+        seen = v[:n - rows + 1 + r, 0]
+        want, size = seen.mean(dim=0), seen.abs().mean(dim=0)
+        tol = (P.WEIGHT[dtype, mx] + 1e-5) * size + torch.finfo(DT[dtype]).eps / 2 * want.abs()
+        assert bool(((o[r, 0].double() - want).abs() <= 1.01 * tol).all()), r
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("most", [2.0 ** 18, 1.2 * 2.0 ** 25, 1.5 * 2.0 ** 27, 1.9 * 2.0 ** 28, 2.0 ** 60])
+@pytest.mark.parametrize("dtype,rows", [("bf16", 1), ("f32", 1), ("bf16", 70)])
+def test_scores_far_below_others_leave_nothing(nv, dtype, rows, most, mx):
+    """300 keys at -most, 130 at 0, 70 at -most: the mean of the 130."""
+    n, dim = 500, 64
+    k = torch.zeros((n, 1, dim), device="cuda")
+    k[:, 0, 0] = -6.0
+    k[300:430] = 0.0
+    cache, table = held(nv, [n], k, normal(22, n, 1, dim), 64, mx, k_scale=1.0)
+    v = nv.nvfp4_kv_gather(cache, table, ints([n]), ints([0, n]), rows=n, dtype=torch.float32)[1].double()
+    q = torch.zeros((rows, 1, dim), device="cuda")
+    q[..., 0] = 2.0 ** 14
+    o = nv.nvfp4_kv_attention(q.to(DT[dtype]), cache, table, ints([n]), ints([0, rows]), scale=most / (6 * 2.0 ** 14))
+    want, size = v[300:430, 0].mean(dim=0), v[300:430, 0].abs().mean(dim=0)
+    tol = (P.WEIGHT[dtype, mx] + 1e-5) * size + torch.finfo(DT[dtype]).eps / 2 * want.abs()
+    assert bool(((o[:, 0].double() - want).abs() <= 1.01 * tol).all())
