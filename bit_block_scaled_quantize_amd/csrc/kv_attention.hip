@@ -430,6 +430,25 @@ __device__ __forceinline__ Join* join_of(const KvAttention& p, int w) {
     return reinterpret_cast<Join*>(p.ws + (int64_t)2 * SHARES * kSlotFloats<D>) + w;
 }
 
+// What a sum of weighted values is multiplied by for the result: 2^-exponent, then
+// v_scale over l's significand, since v_scale / l may lie below the normal numbers where
+// the result does not.  The significand is in [1, 2) over NVFP4, whose values are at most
+// 2688 until v_scale comes in, and in [1/2, 1) over MXFP4, where the first product may
+// then not pass the result.  Without weights: 0.
+template <bool MX>
+struct Mean {
+    float factor;
+    int exponent;
+    __device__ __forceinline__ Mean(float l, float v_scale) {
+        exponent = __builtin_amdgcn_frexp_expf(l) - (MX ? 0 : 1);
+        factor = l > 0.0f ? v_scale / ldexpf(l, -exponent) : 0.0f;
+    }
+    __device__ __forceinline__ float operator()(float x) const { return ldexpf(x, -exponent) * factor; }
+    __device__ __forceinline__ v4f_t operator()(float a, float b, float c, float d) const {
+        return v4f_t{(*this)(a), (*this)(b), (*this)(c), (*this)(d)};
+    }
+};
+
 template <bool F32>
 __device__ __forceinline__ void store_out(const KvAttention& p, const Seq& q, const Segment& g, int c, int d, v4f_t o) {
     const int row = q.row + (g.first + c) / p.group, head = g.head * p.group + (g.first + c) % p.group;
@@ -764,10 +783,10 @@ __global__ void __launch_bounds__(kThreads, (kShares<F32, D> / 256)) k_kv_attent
         const float v_scale = MX ? 1.0f : p.cache.v_scale[g.head];
         if (d.team == 1) {
             if (col < g.count && !idle) {
-                const float f = l > 0.0f ? v_scale / l : 0.0f;
+                const Mean<MX> mean(l, v_scale);
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i)
-                    store_out<F32>(p, q, g, col, 16 * i + 4 * g4, v4f_t{o[i][0] * f, o[i][1] * f, o[i][2] * f, o[i][3] * f});
+                    store_out<F32>(p, q, g, col, 16 * i + 4 * g4, mean(o[i][0], o[i][1], o[i][2], o[i][3]));
                 if (p.lse && g4 == 0) store_lse(p, q, g, col, m, bias, l);
             }
             u += (int64_t)gridDim.x * kWaves;
@@ -800,10 +819,7 @@ __global__ void __launch_bounds__(kThreads, (kShares<F32, D> / 256)) k_kv_attent
                 for (int r = 0; r < 4; ++r) sum[r] += f * x[r];
             }
             if (whole) {
-                const float f = total > 0.0f ? v_scale / total : 0.0f;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) sum[r] *= f;
-                store_out<F32>(p, q, g, cc, d4, sum);
+                store_out<F32>(p, q, g, cc, d4, Mean<MX>(total, v_scale)(sum[0], sum[1], sum[2], sum[3]));
                 if (p.lse && d4 == 0) store_lse(p, q, g, cc, top, bias, total);
             } else {
                 *reinterpret_cast<v4f_t*>(slot + cc * D + d4) = sum;
@@ -829,7 +845,7 @@ __device__ __forceinline__ float reduce_lanes(float x, Op op) {
     return x;
 }
 
-template <bool F32, int D, int LANES, typename Part>
+template <bool MX, bool F32, int D, int LANES, typename Part>
 __device__ __forceinline__ void join_items(const KvAttention& p, const Seq& q, const Segment& g, float bias, float v_scale, int i0,
                                            int i1, int n, Part part) {
     const int at = threadIdx.x / LANES, k0 = threadIdx.x % LANES;
@@ -850,9 +866,9 @@ __device__ __forceinline__ void join_items(const KvAttention& p, const Seq& q, c
         }
         const float most = reduce_lanes<LANES>(top, MaxOp()), e = __builtin_amdgcn_exp2f(top - most);
         total = reduce_lanes<LANES>(total * e, AddOp());
-        const float f = total > 0.0f ? v_scale / total : 0.0f;
+        const Mean<MX> mean(total, v_scale);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) sum[r] = reduce_lanes<LANES>(sum[r] * e, AddOp()) * f;
+        for (int r = 0; r < 4; ++r) sum[r] = mean(reduce_lanes<LANES>(sum[r] * e, AddOp()));
         if (k0 == 0 && b + at < i1) {
             store_out<F32>(p, q, g, c, d, sum);
             if (p.lse && d == 0) store_lse(p, q, g, c, most, bias, total);
@@ -876,10 +892,10 @@ __global__ void __launch_bounds__(kThreads) k_kv_join(const KvAttention p) {
     const int items = g.count * (D / 4), rank = j.rank;
     const int i0 = (int)((int64_t)items * rank / (n - 1)), i1 = (int)((int64_t)items * (rank + 1) / (n - 1));
     // (lanes for all items at once, but no more than have a part)
-    if (n < 4 || i1 - i0 > 128) join_items<F32, D, 1>(p, q, g, j.bias, v_scale, i0, i1, n, part);
-    else if (n < 16 || i1 - i0 > 32) join_items<F32, D, 4>(p, q, g, j.bias, v_scale, i0, i1, n, part);
-    else if (n < 64 || i1 - i0 > 8) join_items<F32, D, 16>(p, q, g, j.bias, v_scale, i0, i1, n, part);
-    else join_items<F32, D, 64>(p, q, g, j.bias, v_scale, i0, i1, n, part);
+    if (n < 4 || i1 - i0 > 128) join_items<MX, F32, D, 1>(p, q, g, j.bias, v_scale, i0, i1, n, part);
+    else if (n < 16 || i1 - i0 > 32) join_items<MX, F32, D, 4>(p, q, g, j.bias, v_scale, i0, i1, n, part);
+    else if (n < 64 || i1 - i0 > 8) join_items<MX, F32, D, 16>(p, q, g, j.bias, v_scale, i0, i1, n, part);
+    else join_items<MX, F32, D, 64>(p, q, g, j.bias, v_scale, i0, i1, n, part);
 }
 
 // ---------------------------------------------------------------- many rows
@@ -1333,13 +1349,13 @@ __global__ void __launch_bounds__(64 * kPreWaves<D>, kPreWaves<D> / 4) k_kv_pref
         }
         return;
     }
-    const float f = l > 0.0f ? (MX ? 1.0f : p.cache.v_scale[g.head]) / l : 0.0f;
+    const Mean<MX> mean(l, MX ? 1.0f : p.cache.v_scale[g.head]);
 #pragma unroll
     for (int i = 0; i < DB; ++i)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
             store_out<false>(p, q, g, lc, 32 * i + 8 * r + 4 * h,
-                             v4f_t{o[i][4 * r] * f, o[i][4 * r + 1] * f, o[i][4 * r + 2] * f, o[i][4 * r + 3] * f});
+                             mean(o[i][4 * r], o[i][4 * r + 1], o[i][4 * r + 2], o[i][4 * r + 3]));
     if (p.lse && h == 0) store_lse(p, q, g, lc, m, bias, l);
 }
 
@@ -1372,10 +1388,7 @@ __global__ void __launch_bounds__(kThreads) k_kv_prefill_join(const KvAttention 
             for (int r = 0; r < 4; ++r) sum[r] = sum[r] * f + x[r] * e;
             top = next;
         }
-        const float f = total > 0.0f ? v_scale / total : 0.0f;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) sum[r] *= f;
-        store_out<false>(p, work.q, work.g, cc, d, sum);
+        store_out<false>(p, work.q, work.g, cc, d, Mean<MX>(total, v_scale)(sum[0], sum[1], sum[2], sum[3]));
         if (p.lse && d == 0) store_lse(p, work.q, work.g, cc, top, bias, total);
     }
 }

@@ -171,3 +171,26 @@ def test_scores_far_below_others_leave_nothing(nv, dtype, rows, most, mx):
     want, size = v[300:430, 0].mean(dim=0), v[300:430, 0].abs().mean(dim=0)
     tol = (P.WEIGHT[dtype, mx] + 1e-5) * size + torch.finfo(DT[dtype]).eps / 2 * want.abs()
     assert bool(((o[:, 0].double() - want).abs() <= 1.01 * tol).all())
+
+
+# ---------------------------------------------------------------- head scales of values
+@pytest.mark.parametrize("e", [-124, -110, -60, 60, 114])
+@pytest.mark.parametrize("dim,dtype,new", FORMS)
+def test_value_scales_of_any_size(nv, dim, dtype, new, e):
+    n = sum(LENGTHS)
+    v = torch.ldexp(normal(9, n, 2, dim).clamp(-5, 5) * 400.0, torch.tensor(e))
+    cache, table = held(nv, LENGTHS, normal(10, n, 2, dim), v, 32, False, v_scale=2.0 ** e)
+    q = normal(11, rows_of(new), 6, dim).to(DT[dtype])
+    attend_and_check(nv, LENGTHS, new, q, cache, table, 32, False, dtype, dim ** -0.5)
+
+
+@pytest.mark.parametrize("dtype,rows", [("bf16", 1), ("f32", 1), ("bf16", 70)])
+def test_the_mean_of_many_small_values(nv, dtype, rows):
+    """65536 equal keys: their weights' sum is far above the value scale's reciprocal."""
+    n, dim = 65536, 64
+    v = torch.full((n, 1, dim), 2688 * 2.0 ** -124, device="cuda")
+    cache, table = held(nv, [n], torch.zeros_like(v), v, 256, False, v_scale=2.0 ** -124)
+    q = torch.ones((rows, 1, dim), device="cuda").to(DT[dtype])
+    o = nv.nvfp4_kv_attention(q, cache, table, ints([n]), ints([0, rows]))
+    off = (o.double() / (2688 * 2.0 ** -124) - 1.0).abs().max().item()
+    assert off <= 1e-5 + torch.finfo(DT[dtype]).eps / 2, off
