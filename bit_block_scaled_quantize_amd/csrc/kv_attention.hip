@@ -166,6 +166,24 @@ __device__ __forceinline__ float weight_bias(const KvAttention& p, int length) {
     return -kSlack - (float)(keys > 1 ? 32 - __clz(keys - 1) : 0);
 }
 
+// Scores in powers of two for a product of q, times 2^(15 - e), with a head's keys:
+// |scale| log2(e) (NVFP4: times k_scale, 2^(e - 15)).  The significands are multiplied
+// and the exponents added, since scale x k_scale alone may leave the normal numbers where
+// the scores do not.  (At least the least normal number: 0 times a hidden score's -inf is
+// no number.)
+template <bool MX>
+__device__ __forceinline__ float score_factor(const KvAttention& p, int head, int e) {
+    const float scale = fabsf(p.scale);
+    int exponent = __builtin_amdgcn_frexp_expf(scale);
+    float f = __builtin_amdgcn_frexp_mantf(scale) * kLog2e;
+    if constexpr (!MX) {
+        const float k = p.cache.k_scale[head];
+        exponent += __builtin_amdgcn_frexp_expf(k) + e - 15;
+        f *= __builtin_amdgcn_frexp_mantf(k);
+    }
+    return fmaxf(ldexpf(f, exponent), 1.1754944e-38f);
+}
+
 // The sum of 8 values, in pairs (a sum one by one waits for each addition).
 __device__ __forceinline__ float sum8(const float v[8]) {
     return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
@@ -627,8 +645,7 @@ __global__ void __launch_bounds__(kThreads, (kShares<F32, D> / 256)) k_kv_attent
 
         // q, its row scaled into FP16's range
         v8 qf[KD][QP];
-        float factor = fabsf(p.scale) * kLog2e;
-        if constexpr (!MX) factor *= p.cache.k_scale[g.head];
+        float factor;
         {
             float v[KD][8];
             const int64_t at = (q.row + qrow) * p.q.row + qhead * p.q.head + g4 * (D / 4);
@@ -648,8 +665,8 @@ __global__ void __launch_bounds__(kThreads, (kShares<F32, D> / 256)) k_kv_attent
                 row_pair(top, a, b);
                 half_pair(fmaxf(a, b), a, b);
                 e = __builtin_amdgcn_frexp_expf(fmaxf(a, b));  // 0 for 0
-                factor = ldexpf(factor, e - 15);
             }
+            factor = score_factor<MX>(p, g.head, e);
             // (the scale's sign goes with q, so that larger sums are larger scores)
 #pragma unroll
             for (int i = 0; i < KD; ++i) {
@@ -660,7 +677,6 @@ __global__ void __launch_bounds__(kThreads, (kShares<F32, D> / 256)) k_kv_attent
                 }
                 split8<MX, QP>(v[i], qf[i]);
             }
-            factor = fmaxf(factor, 1.1754944e-38f);  // (0 times a hidden score's -inf is no number)
         }
 
         float m = kLowest, l = 0.0f;
@@ -1053,8 +1069,7 @@ __global__ void __launch_bounds__(64 * kPreWaves<D>, kPreWaves<D> / 4) k_kv_pref
     const float bias = weight_bias<MX>(p, q.length);
 
     v8 qf[KS];
-    float factor = fabsf(p.scale) * kLog2e;
-    if constexpr (!MX) factor *= p.cache.k_scale[g.head];
+    float factor;
     {
         float v[KS][8];
         const uint16_t* src = static_cast<const uint16_t*>(p.q.data) + (q.row + qrow) * p.q.row + qhead * p.q.head + 8 * h;
@@ -1069,8 +1084,8 @@ __global__ void __launch_bounds__(64 * kPreWaves<D>, kPreWaves<D> / 4) k_kv_pref
                 for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(v[i][k]));
             half_pair(top, a, b);
             e = __builtin_amdgcn_frexp_expf(fmaxf(a, b));
-            factor = ldexpf(factor, e - 15);
         }
+        factor = score_factor<MX>(p, g.head, e);
         // (the scale's sign goes with q, so that larger sums are larger scores)
 #pragma unroll
         for (int i = 0; i < KS; ++i) {
@@ -1081,7 +1096,6 @@ __global__ void __launch_bounds__(64 * kPreWaves<D>, kPreWaves<D> / 4) k_kv_pref
             }
             split8<MX, 1>(v[i], &qf[i]);
         }
-        factor = fmaxf(factor, 1.1754944e-38f);  // (0 times a hidden score's -inf is no number)
     }
 
     // what a thread loads of a tile: EPT elements of a key

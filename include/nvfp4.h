@@ -638,8 +638,8 @@ size_t nvfp4_kv_attention_workspace_size(int64_t rows, int64_t seqs, int32_t q_h
  * below it), as two BF16 parts over MXFP4 (2^-17), and as two FP16 or three BF16
  * parts for binary32 q.  MXFP4 elements below 2^-126 may count as zero, and
  * results over MXFP4 below 2^-121 times the number of positions seen lose bits.
- * Scores must stay in binary32's range.  A row of q that is not finite gives
- * unspecified results, the other rows theirs.
+ * Scores, and over MXFP4 the sums <q, k>, must stay in binary32's range.  A row
+ * of q that is not finite gives unspecified results, the other rows theirs.
  * ws 16-byte aligned, ws_bytes >= nvfp4_kv_attention_workspace_size(...); it is
  * scratch for this call only: calls that overlap must not share it.
  * q_heads % kv_heads == 0; rows * q_heads <= 2^28 (else UNSUPPORTED).  Results

@@ -194,3 +194,23 @@ def test_the_mean_of_many_small_values(nv, dtype, rows):
     o = nv.nvfp4_kv_attention(q, cache, table, ints([n]), ints([0, rows]))
     off = (o.double() / (2688 * 2.0 ** -124) - 1.0).abs().max().item()
     assert off <= 1e-5 + torch.finfo(DT[dtype]).eps / 2, off
+
+
+# ---------------------------------------------------------------- head scales of keys
+@pytest.mark.parametrize("large", [False, True])
+@pytest.mark.parametrize("dim,dtype,new", FORMS)
+def test_key_scales_of_any_size(nv, dim, dtype, new, large):
+    """Scores of ordinary size where the scale times the key scale alone leaves binary32's
+    normal numbers (small keys, large rows of q) or its range (the other way round)."""
+    n, rows = sum(LENGTHS), rows_of(new)
+    g = torch.Generator().manual_seed(12)
+    if large:
+        e, scale = 118, 2.0 ** 11
+        k = torch.ldexp(normal(13, n, 2, dim), torch.tensor(118))
+        q = torch.ldexp(normal(14, rows, 6, dim), torch.tensor(-127))
+    else:
+        e, scale = -124, 8.0 / (dim * 0.5625 * 2600 * 8)
+        k, q = (0.5 + 0.5 * torch.rand(size, generator=g).cuda() for size in ((n, 2, dim), (rows, 6, dim)))
+        k, q = k * 2600 * 2.0 ** -124, torch.ldexp(q, torch.tensor(127))
+    cache, table = held(nv, LENGTHS, k, normal(15, n, 2, dim), 32, False, k_scale=2.0 ** e)
+    attend_and_check(nv, LENGTHS, new, q.to(DT[dtype]), cache, table, 32, False, dtype, scale)
