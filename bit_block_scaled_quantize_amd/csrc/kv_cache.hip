@@ -32,12 +32,14 @@ __device__ __forceinline__ int64_t slot_at(const KvCache& c, int page_shift, int
 }
 
 // The block's scale byte and the multiplier of its elements (rules of
-// include/nvfp4.h; NVFP4 with the head's float as tensor scale).
+// include/nvfp4.h; NVFP4 with the head's float as tensor scale).  A block that is not
+// finite gets the largest scale that a finite one may have, so that its elements are
+// numbers (6 x 2^126 is none) for the rows that attend to others beside them.
 template <bool MX>
 __device__ __forceinline__ BlockScale kv_block_scale(float amax, float head_scale) {
     BlockScale bs;
     if constexpr (MX) {
-        const int s = max((int)(__float_as_uint(amax) >> 23) - 127 - 2, -127);
+        const int s = max(min((int)(__float_as_uint(amax) >> 23), 254) - 127 - 2, -127);
         bs.byte = (uint32_t)(s + 127);
         bs.R = __uint_as_float((uint32_t)(127 - s) << 23);
     } else {

@@ -606,7 +606,8 @@ typedef struct {
  * the head's float as s_t, or of nvfp4_mx_quantize.  q (nullable, rows x q_heads
  * x head_dim) is rotated alike into q_out (rounded once to dt), which may be q
  * itself.  A row whose position is negative or past the table of angles is not
- * stored, and its row of q_out is zero.  Within one call no slot may have two
+ * stored, and its row of q_out is zero.  A block with an element that is not
+ * finite has unspecified but finite values.  Within one call no slot may have two
  * rows (a page that is written to belongs to one sequence): such a slot's
  * contents are unspecified. */
 nvfp4_status nvfp4_kv_append(const nvfp4_kv_rows* k, const nvfp4_kv_rows* v, int32_t dt /* nvfp4_dtype */,

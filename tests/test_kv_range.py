@@ -214,3 +214,43 @@ def test_key_scales_of_any_size(nv, dim, dtype, new, large):
         k, q = k * 2600 * 2.0 ** -124, torch.ldexp(q, torch.tensor(127))
     cache, table = held(nv, LENGTHS, k, normal(15, n, 2, dim), 32, False, k_scale=2.0 ** e)
     attend_and_check(nv, LENGTHS, new, q.to(DT[dtype]), cache, table, 32, False, dtype, scale)
+
+
+# ---------------------------------------------------------------- what was not finite
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("dim,dtype,rows", [(128, "bf16", 120), (64, "f32", 120), (256, "bf16", 120), (128, "bf16", 12)])
+def test_appended_values_that_are_not_finite(nv, dim, dtype, rows, mx):
+    """They are unspecified; rows that do not see them have their results, bit for bit."""
+    n, bad = 120, 113
+    k, v, q = normal(16, n, 2, dim), normal(17, n, 2, dim), normal(18, rows, 8, dim).to(DT[dtype])
+    L, O = ints([n]), ints([0, rows])
+    got = []
+    for x in (1.0, math.inf, -math.inf, math.nan):
+        v[bad, :, 3] = x
+        v[bad, 1, :] = x
+        cache, table = held(nv, [n], k, v, 32, mx)
+        rest = torch.ones(n, dtype=torch.bool)
+        rest[bad] = False
+        read = nv.nvfp4_kv_gather(cache, table, L, ints([0, n]), rows=n, dtype=torch.float32)[1]
+        assert bool(read.isfinite().all())
+        got.append((read[rest], nv.nvfp4_kv_attention(q, cache, table, L, O)[:bad - n],
+                    nv.nvfp4_kv_attention(q, cache, table, L, O, window=3)[-3:]))
+    for other in got[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(got[0], other))
+    assert all(bool(x.isfinite().all()) for x in got[0])
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("dim,dtype,rows", [(128, "bf16", 120), (64, "f32", 120), (256, "bf16", 120), (128, "bf16", 12)])
+def test_appended_keys_that_are_not_finite(nv, dim, dtype, rows, mx):
+    """Rows that do not see them have their results to the bounds."""
+    n, bad = 120, 113
+    k, v, q = normal(19, n, 2, dim), normal(20, n, 2, dim), normal(21, rows, 8, dim).to(DT[dtype])
+    clean, table = held(nv, [n], k, v, 32, mx)
+    want = P.attention(q, clean, table, [n], [0, rows], dim ** -0.5, 0, clean.k_codes.shape[0], 32)
+    for x in (math.inf, -math.inf, math.nan):
+        k[bad, :, 3] = x
+        k[bad, 1, :] = x
+        cache, table = held(nv, [n], k, v, 32, mx)
+        o, lse = nv.nvfp4_kv_attention(q, cache, table, ints([n]), ints([0, rows]), lse=True)
+        P.check_attention(o, lse, want, dtype, mx, rows=slice(0, rows + bad - n))
