@@ -135,6 +135,7 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(const KvAppend p) {
     Share w;
     if (!share_of_wave(p.plan.rows, chunks, p.rows_each, p.chunks_each, w)) return;
     const KvPlaces places = kv_places(p.plan, p.cache.pages, w.t0, w.n);
+    if (places.owned == 0) return;
     const int rot = p.rot, half = rot / 2;
     const bool turned = li < rot / 16, halves = turned && !p.interleaved;
     const int a = halves ? 8 * li : 16 * li, b = halves ? a + half : a + 8;
@@ -145,7 +146,9 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(const KvAppend p) {
         const int h = is_q ? hd : is_k ? hd - p.q_heads : hd - p.q_heads - p.cache.heads;
         const void* data = is_q ? p.q.data : is_k ? p.k.data : p.v.data;
         const int64_t row = is_q ? p.q.row : is_k ? p.k.row : p.v.row, head = is_q ? p.q.head : is_k ? p.k.head : p.v.head;
-        const T* src = static_cast<const T*>(data) + (w.t0 + r) * row + h * head;
+        // (for a row of no sequence one that is: without a branch around loads under way)
+        const int own = places.owned >> r & 1 ? r : __builtin_ctzll(places.owned);
+        const T* src = static_cast<const T*>(data) + (w.t0 + own) * row + h * head;
         return load_raw(src + a, src + b);
     };
     Raw<T> now = load(0, w.c0);
@@ -169,7 +172,7 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(const KvAppend p) {
             // (two ahead, 15047 rows of 72 heads took 119 us instead of 114)
             if (c + 1 < w.c1) now = load(r, c + 1);
             else if (r + 1 < w.n) now = load(r + 1, w.c0);
-            if (pos == kNoRow) continue;
+            if (!(places.owned >> r & 1)) continue;
             if (turned && (is_q || is_k)) {
                 if (halves) {
 #pragma unroll
@@ -232,6 +235,7 @@ __global__ void __launch_bounds__(kThreads) k_kv_gather(const KvGather p) {
     Share w;
     if (!share_of_wave(p.plan.rows, chunks, p.rows_each, p.chunks_each, w)) return;
     const KvPlaces places = kv_places(p.plan, p.cache.pages, w.t0, w.n);
+    if (places.owned == 0) return;
     const int slot_mask = (1 << p.plan.page_shift) - 1;
 
     struct Held {
@@ -268,7 +272,7 @@ __global__ void __launch_bounds__(kThreads) k_kv_gather(const KvGather p) {
             const int pos = __builtin_amdgcn_readlane(places.pos, r), page = __builtin_amdgcn_readlane(places.page, r);
             at.next(w);
             const int hd = c * kHeads + lane / kLanes;
-            if (pos == kNoRow || hd >= heads) continue;
+            if (!(places.owned >> r & 1) || hd >= heads) continue;
             const bool is_k = hd < p.cache.heads;
             const int h = is_k ? hd : hd - p.cache.heads;
             float v[16] = {};

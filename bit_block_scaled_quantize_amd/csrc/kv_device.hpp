@@ -39,16 +39,16 @@ __device__ __forceinline__ int kv_page_of(int entry, int pages) { return (uint32
 // Where rows t0 .. t0 + n - 1 (n <= 64) lie: lane r has row t0 + r's position and
 // page.
 struct KvPlaces {
-    int pos;   // kNoRow: a row that belongs to no sequence
-    int page;  // -1: none
+    int pos;
+    int page;        // -1: none
+    uint64_t owned;  // bit r: row t0 + r belongs to a sequence (known before the rest)
 };
-constexpr int kNoRow = -0x7FFFFFFF - 1;
 
 // A row's sequence is the number of offsets[1 ...] that are <= it; 64 offsets are
 // compared at a time.
 __device__ __forceinline__ KvPlaces kv_places(const KvPlan& p, int pages, int t0, int n) {
     const int lane = threadIdx.x & 63, t = t0 + lane;
-    KvPlaces w = {kNoRow, -1};
+    KvPlaces w = {-1, -1, 0};
     int s = t;
     if (p.offsets) {
         s = 0;
@@ -63,13 +63,13 @@ __device__ __forceinline__ KvPlaces kv_places(const KvPlan& p, int pages, int t0
             if (more < 64) break;
         }
     }
-    if (lane < n && s < p.seqs && (!p.offsets || t >= p.offsets[0])) {
-        int first, count;
-        kv_rows(p, s, first, count);
-        if (t >= first && t - first < count) {  // (not so where offsets are out of order)
-            w.pos = kv_length(p, s) - count + (t - first);
-            if (w.pos >= 0) w.page = kv_page_of(kv_entry(p, s, w.pos), pages);
-        }
+    int first = 0, count = 0;
+    if (lane < n && s < p.seqs && (!p.offsets || t >= p.offsets[0])) kv_rows(p, s, first, count);
+    const bool own = t >= first && t - first < count;  // (else also where offsets are out of order)
+    w.owned = __ballot(own);
+    if (own) {
+        w.pos = kv_length(p, s) - count + (t - first);
+        if (w.pos >= 0) w.page = kv_page_of(kv_entry(p, s, w.pos), pages);
     }
     return w;
 }

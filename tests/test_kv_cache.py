@@ -380,3 +380,62 @@ def test_no_sequences_and_no_pages(nv):
 @pytest.mark.parametrize("which", [0, 1, 2])
 def test_rows_of_no_sequence_launch_nothing(nv, which):
     assert _calls(nv)[which](_cache(nv), _plan(nv, seqs=0, rows=5, lengths=None, table=None)) == E["OK"]
+
+
+@pytest.mark.gpu
+def test_rows_of_no_sequence_are_not_read(nv):
+    """A call whose rows are all but padding takes no time for them: reading their 1.3 GB
+    alone takes 43% of what appending them does."""
+    rows, dim, page = 65536, 128, 64
+    cache, table = make(nv, [rows], 8, dim, page, False)
+    k, v = (torch.randn((rows, 8, dim), device="cuda") for _ in range(2))
+    q = torch.randn((rows, 24, dim), device="cuda")
+    out = torch.empty_like(q)
+
+    def least(lengths, offsets):
+        L, O = torch.tensor(lengths, dtype=torch.int32).cuda(), torch.tensor(offsets, dtype=torch.int32).cuda()
+        times = []
+        for _ in range(8):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            nv.nvfp4_kv_append(k, v, cache, table, L, O, q=q, out=out)
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times)
+
+    whole = least([rows], [0, rows])
+    for offsets in ([0, 16], [rows - 16, rows], [rows // 2, rows // 2]):
+        part = least([rows], offsets)
+        assert part < 0.3 * whole, (offsets, part, whole)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_padding_beside_rows_of_a_wave(nv, dtype):
+    """Many rows, a few to a wave, of which some belong to no sequence: what they hold
+    reaches nothing."""
+    rows, dim, page, lengths = 20000, 64, 64, [9000, 9500]
+    offsets = [700, 9003, 18001]
+    cache, table = make(nv, lengths, 8, dim, page, False)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    k, v, q = (torch.randn((rows, h, dim), generator=g, device="cuda").to(DT[dtype]) for h in (8, 8, 16))
+    L, O = torch.tensor(lengths, dtype=torch.int32).cuda(), torch.tensor(offsets, dtype=torch.int32).cuda()
+    rope = rope_table(9500, 64)
+    own = slice(offsets[0], offsets[-1])
+    nv.nvfp4_kv_append(k[own], v[own], cache, table, L, O - offsets[0], q=q[own], rope=rope, out=(want := q[own].clone()))
+    arrays = {n: getattr(cache, n).cpu() for n in ("k_codes", "k_scales", "v_codes", "v_scales")}
+    for n in arrays:
+        getattr(cache, n).fill_(255)
+    for x in (k, v, q):
+        x[:offsets[0]] = float("nan")
+        x[offsets[-1]:] = float("inf")
+    out = torch.full_like(q, 5.0)
+    nv.nvfp4_kv_append(k, v, cache, table, L, O, q=q, rope=rope, out=out)
+    same(cache, arrays)
+    assert torch.equal(out[own], want) and bool((out[:offsets[0]] == 5).all()) and bool((out[offsets[-1]:] == 5).all())
+    pair = tuple(torch.full((rows, 8, dim), 5.0, device="cuda") for _ in range(2))
+    nv.nvfp4_kv_gather(cache, table, L, O, rows=rows, out=pair)
+    ref = nv.nvfp4_kv_gather(cache, table, L, O - offsets[0], rows=offsets[-1] - offsets[0], dtype=torch.float32)
+    for x, y in zip(pair, ref):
+        assert torch.equal(x[own], y) and bool((x[:offsets[0]] == 5).all()) and bool((x[offsets[-1]:] == 5).all())
