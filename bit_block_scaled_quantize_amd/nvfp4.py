@@ -692,11 +692,16 @@ def nvfp4_kv_append(k, v, cache, page_table, lengths, offsets=None, q=None, rope
 @_launches_on_stream
 def nvfp4_kv_gather(cache, page_table, lengths, offsets=None, rows=None, dtype=torch.bfloat16, out=None, stream=None):
     """(k, v), each rows x kv_heads x head_dim, of the cache's positions that
-    the plan names (as nvfp4_kv_append); rows: their number (one a sequence
-    unless given).  out: a pair of tensors to fill."""
+    the plan names (as nvfp4_kv_append); rows: their number (without offsets one
+    a sequence; with offsets that of out unless given).  out: a pair of tensors
+    to fill."""
     if out is not None:
         dtype = out[0].dtype
-    return _native.kv_gather(*cache.args(), page_table, lengths, offsets, page_table.shape[0] if rows is None else rows,
+    if rows is None:
+        if offsets is not None and out is None:
+            raise ValueError("rows must be given where offsets are")  # (they lie on the device)
+        rows = page_table.shape[0] if offsets is None else out[0].shape[0]
+    return _native.kv_gather(*cache.args(), page_table, lengths, offsets, rows,
                              _dtype_code(dtype), *((None, None) if out is None else out), _handle(stream))
 
 

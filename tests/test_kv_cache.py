@@ -439,3 +439,28 @@ def test_padding_beside_rows_of_a_wave(nv, dtype):
     ref = nv.nvfp4_kv_gather(cache, table, L, O - offsets[0], rows=offsets[-1] - offsets[0], dtype=torch.float32)
     for x, y in zip(pair, ref):
         assert torch.equal(x[own], y) and bool((x[:offsets[0]] == 5).all()) and bool((x[offsets[-1]:] == 5).all())
+
+
+def test_gather_by_offsets_needs_its_rows(nv):
+    """Their number lies on the device: taken as one a sequence, other rows would come back."""
+    cache = nv.NVFP4KVCache.empty(4, 2, 64, page_size=16, device="cpu")
+    table, lengths = torch.zeros((3, 2), dtype=torch.int32), torch.ones(3, dtype=torch.int32)
+    offsets = torch.tensor([0, 4, 5, 9], dtype=torch.int32)
+    with pytest.raises(ValueError, match="rows"):
+        nv.nvfp4_kv_gather(cache, table, lengths, offsets)
+    pair = torch.zeros((9, 2, 64)), torch.zeros((9, 2, 64))
+    for args in (dict(rows=9), dict(out=pair), dict(rows=9, out=pair)):  # (as far as the tensors' device)
+        with pytest.raises(ValueError, match="GPU"):
+            nv.nvfp4_kv_gather(cache, table, lengths, offsets, **args)
+
+
+@pytest.mark.gpu
+def test_gather_by_offsets_into_given_rows(nv):
+    lengths, offsets = [30, 7], [0, 20, 27]
+    cache, table = make(nv, lengths, 2, 64, 16, False)
+    k, v = torch.randn((27, 2, 64)).cuda(), torch.randn((27, 2, 64)).cuda()
+    L, O = torch.tensor(lengths, dtype=torch.int32).cuda(), torch.tensor(offsets, dtype=torch.int32).cuda()
+    nv.nvfp4_kv_append(k, v, cache, table, L, O)
+    pair = torch.empty_like(k), torch.empty_like(v)
+    nv.nvfp4_kv_gather(cache, table, L, O, out=pair)
+    assert all(torch.equal(x, y) for x, y in zip(pair, nv.nvfp4_kv_gather(cache, table, L, O, rows=27, dtype=torch.float32)))
