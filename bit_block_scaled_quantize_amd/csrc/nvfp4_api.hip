@@ -653,8 +653,14 @@ nvfp4_status check_heads(const nvfp4_kv_rows* r, int64_t rows, int64_t heads, in
     if (r->row_stride < 0 || r->head_stride < 0) return NVFP4_ERR_SHAPE;
     if (rows > 0 && !r->data) return NVFP4_ERR_NULL;
     if (written && rows > 0) {
-        const bool by_row = (heads == 1 || r->head_stride >= dim) && (rows == 1 || r->row_stride / heads >= (heads == 1 ? dim : r->head_stride));
-        const bool by_head = (rows == 1 || r->row_stride >= dim) && (heads == 1 || r->head_stride / rows >= (rows == 1 ? dim : r->row_stride));
+        // `inner` pieces of dim, `stride` apart, end before the next one of `outer`
+        const auto apart = [dim](int64_t inner, int64_t stride, int64_t outer, int64_t outer_stride) {
+            if (inner > 1 && stride < dim) return false;
+            if (outer == 1) return true;
+            return outer_stride >= dim && (inner == 1 || (outer_stride - dim) / stride >= inner - 1);
+        };
+        const bool by_row = apart(heads, r->head_stride, rows, r->row_stride);
+        const bool by_head = apart(rows, r->row_stride, heads, r->head_stride);
         if (!by_row && !by_head) return NVFP4_ERR_SHAPE;
     }
     return aligned(r->data, dtype_size(dt)) ? NVFP4_OK : NVFP4_ERR_ALIGN;

@@ -578,7 +578,8 @@ typedef struct {
 
 /* rows x heads of head_dim consecutive elements each; strides in elements, not
  * negative.  Where it is written, heads must not overlap: head_stride >=
- * head_dim and row_stride >= heads * head_stride, or the other way round. */
+ * head_dim and row_stride >= (heads - 1) * head_stride + head_dim, or the other
+ * way round. */
 typedef struct {
     void* data;
     int64_t row_stride;

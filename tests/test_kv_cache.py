@@ -464,3 +464,46 @@ def test_gather_by_offsets_into_given_rows(nv):
     pair = torch.empty_like(k), torch.empty_like(v)
     nv.nvfp4_kv_gather(cache, table, L, O, out=pair)
     assert all(torch.equal(x, y) for x, y in zip(pair, nv.nvfp4_kv_gather(cache, table, L, O, rows=27, dtype=torch.float32)))
+
+
+# (row stride, head stride) of 5 rows of 2 heads of 128 (attention: 4 heads), apart or not
+APART = [(256, 128), (384, 256), (128, 640), (256, 1152), (1 << 62, 128), (128, 1 << 62)]
+TOGETHER = [(255, 128), (383, 256), (256, 127), (128, 639), (256, 1151), (127, 1 << 62), (1 << 62, 127), (0, 128), (128, 0)]
+
+
+def test_heads_written_to_are_refused_only_where_they_overlap(nv):
+    """(A misaligned address comes after the strides: nothing is launched.)"""
+    append, gather, attention = _calls(nv)
+    c, p = _cache(nv), _plan(nv)
+    for strides, want in [(x, "ALIGN") for x in APART] + [(x, "SHAPE") for x in TOGETHER]:
+        out = _rows(nv, 65537, *strides)
+        assert gather(c, p, k=out) == E[want] and gather(c, p, v=out) == E[want], strides
+        assert append(c, p, q=_rows(nv), hq=2, qo=out) == E[want], strides
+        assert attention(c, p, q=_rows(nv), hq=2, out=out) == E[want], strides
+    one = _plan(nv, seqs=1, rows=1, offsets=None)
+    for strides, want in (((0, 128), "ALIGN"), ((0, 1 << 62), "ALIGN"), ((0, 127), "SHAPE")):
+        assert gather(c, one, k=_rows(nv, 65537, *strides)) == E[want], strides
+    single = _cache(nv, heads=1)
+    for strides, want in (((128, 0), "ALIGN"), ((127, 0), "SHAPE"), ((127, 1 << 62), "SHAPE")):
+        assert gather(single, p, k=_rows(nv, 65537, *strides)) == E[want], strides
+
+
+@pytest.mark.gpu
+def test_results_into_every_second_head(nv):
+    """Heads 0 and 2 of a tensor of three: the last row ends where the tensor does."""
+    lengths, offsets, rows, dim = [30, 7], [0, 20, 27], 27, 64
+    cache, table = make(nv, lengths, 2, dim, 16, False)
+    g = torch.Generator().manual_seed(7)
+    k, v, q = (torch.randn((rows, 2, dim), generator=g).cuda() for _ in range(3))
+    L, O = torch.tensor(lengths, dtype=torch.int32).cuda(), torch.tensor(offsets, dtype=torch.int32).cuda()
+    rope = rope_table(30, dim)
+    wide = [torch.full((rows, 3, dim), 7.0, device="cuda") for _ in range(4)]
+    turned = nv.nvfp4_kv_append(k, v, cache, table, L, O, q=q, rope=rope)
+    nv.nvfp4_kv_append(k, v, cache, table, L, O, q=q, rope=rope, out=wide[0][:, ::2])
+    nv.nvfp4_kv_attention(q, cache, table, L, O, out=wide[1][:, ::2])
+    nv.nvfp4_kv_gather(cache, table, L, O, out=(wide[2][:, ::2], wide[3][:, ::2]))
+    want = [turned, nv.nvfp4_kv_attention(q, cache, table, L, O),
+            *nv.nvfp4_kv_gather(cache, table, L, O, rows=rows, dtype=torch.float32)]
+    for x, y in zip(wide, want):
+        # (bits: the first sequence's first ten slots hold no numbers)
+        assert torch.equal(x[:, ::2].contiguous().view(torch.int32), y.view(torch.int32)) and bool((x[:, 1] == 7.0).all())
