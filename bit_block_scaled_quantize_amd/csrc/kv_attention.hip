@@ -1006,7 +1006,8 @@ __device__ __forceinline__ bool pre_find(const KvAttention& p, int64_t index, in
 // and 75.  Least parts of 8 or 24 tiles: 112 and 91, 105 and 89, 48 and 71.  A block's
 // parts beside each other: 1024 rows 61 instead of 57, 512 behind 3584 105, three
 // chunks behind up to 16384 402 instead of 408.)
-constexpr int kLeastTiles = 16;
+constexpr int kLeastTiles = 16, kMostParts = 16;
+static_assert(kLeastTiles >= kMostParts);  // so that parts of ceil(tiles / parts) tiles leave none without any
 struct PreWork {
     Seq q;
     Segment g;
@@ -1350,13 +1351,12 @@ __global__ void __launch_bounds__(64 * kPreWaves<D>, kPreWaves<D> / 4) k_kv_pref
     if (lc >= g.count) return;
     if (work.parts > 1) {
         float* slot = p.pre_ws + work.slot * kPreSlotFloats<D>;
-        if (j0 < j1)
 #pragma unroll
-            for (int i = 0; i < DB; ++i)
+        for (int i = 0; i < DB; ++i)
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    *reinterpret_cast<v4f_t*>(slot + lc * D + 32 * i + 8 * r + 4 * h) =
-                        v4f_t{o[i][4 * r], o[i][4 * r + 1], o[i][4 * r + 2], o[i][4 * r + 3]};
+            for (int r = 0; r < 4; ++r)
+                *reinterpret_cast<v4f_t*>(slot + lc * D + 32 * i + 8 * r + 4 * h) =
+                    v4f_t{o[i][4 * r], o[i][4 * r + 1], o[i][4 * r + 2], o[i][4 * r + 3]};
         if (h == 0) {
             slot[kPreCols<D> * D + lc] = m;
             slot[kPreCols<D> * (D + 1) + lc] = l;
@@ -1394,9 +1394,7 @@ __global__ void __launch_bounds__(kThreads) k_kv_prefill_join(const KvAttention 
             const float l = slot[kPreCols<D> * (D + 1) + cc];
             const float m = slot[kPreCols<D> * D + cc], next = fmaxf(top, m);
             const float f = __builtin_amdgcn_exp2f(top - next), e = __builtin_amdgcn_exp2f(m - next);
-            v4f_t x = *reinterpret_cast<const v4f_t*>(slot + cc * D + d);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) x[r] = l > 0.0f ? x[r] : 0.0f;  // (an empty part has written no sums)
+            const v4f_t x = *reinterpret_cast<const v4f_t*>(slot + cc * D + d);
             total = total * f + l * e;
 #pragma unroll
             for (int r = 0; r < 4; ++r) sum[r] = sum[r] * f + x[r] * e;
@@ -1418,7 +1416,7 @@ int64_t pre_blocks_most(int64_t rows, int64_t seqs, int group, int dim) {
 
 int pre_splits(int64_t rows, int64_t seqs, int group, int heads, int dim) {
     const int64_t blocks = pre_blocks_most(rows, seqs, group, dim) * heads;
-    return (int)std::max<int64_t>(1, std::min<int64_t>(16, 1024 / std::max<int64_t>(1, blocks)));
+    return (int)std::max<int64_t>(1, std::min<int64_t>(kMostParts, 1024 / std::max<int64_t>(1, blocks)));
 }
 
 template <bool MX, int D>
