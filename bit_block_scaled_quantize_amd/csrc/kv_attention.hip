@@ -123,7 +123,7 @@ struct Form<true> {
 // Parts of q: a BF16 value fits FP16 once its row is scaled to [2^14, 2^15) (an
 // element below 2^-29 of the row's largest keeps 2^-25 of 2^14, past the
 // products' binary32 sums), a binary32 one two FP16 or three BF16 parts.  Parts
-// of a weight: one FP16 part is off by 2^-12, two BF16 parts by
+// of a weight: one FP16 part is off by 2^-11, two BF16 parts by
 // 2^-17, of binary32 results two FP16 parts by 2^-23, three BF16 parts by 2^-25.
 template <bool MX, bool F32>
 constexpr int kQParts = F32 ? (MX ? 3 : 2) : 1;

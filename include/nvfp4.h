@@ -636,7 +636,7 @@ size_t nvfp4_kv_attention_workspace_size(int64_t rows, int64_t seqs, int32_t q_h
  * Products are exact (of binary32 q: of its two FP16 parts for NVFP4, 22
  * bits, or three BF16 parts for MXFP4), sums and the softmax's statistics
  * binary32; the weights w_j go into the second product rounded to FP16 for
- * BF16 q over NVFP4 (2^-12, and 2^-36 of the row's largest weight for those far
+ * BF16 q over NVFP4 (2^-11, and 2^-36 of the row's largest weight for those far
  * below it), as two BF16 parts over MXFP4 (2^-17), and as two FP16 or three BF16
  * parts for binary32 q.  MXFP4 elements below 2^-126 may count as zero, and
  * results over MXFP4 below 2^-121 times the number of positions seen lose bits.

@@ -140,3 +140,18 @@ def check_attention(got, got_lse, want, dtype, mx, rows=None):
         lim = weight.squeeze(2) + 2.0 ** -21 * torch.where(empty, 0.0, lse).abs()
         d = torch.where(empty, 0.0, got_lse.double() - lse).abs()
         assert bool((d <= lim)[keep].all()), (d / lim)[keep].max().item()
+
+
+#: As WEIGHT, with the whole half step of FP16: of 11 significant bits, a weight in [2^k, 2^(k + 1)) is rounded by up to
+#: 2^(k - 11), which is 2^-11 of it at the lower end.  (Two parts: the first leaves up to 2^(k - 11), the second's half step
+#: is then 2^(k - 23); BF16's 8 bits leave 2^(k - 8), then 2^(k - 17).)
+HALF_STEP = {**WEIGHT, ("bf16", False): 2.0 ** -11}
+
+
+def check(got, got_lse, want, dtype, mx, rows=None):
+    """check_attention with weights off by HALF_STEP in the results (the sums are of unrounded ones)."""
+    out, lse, mean_abs, weight, lost = want
+    more = HALF_STEP[dtype, mx] - WEIGHT[dtype, mx]
+    check_attention(got, None, (out, lse, mean_abs, weight + more, lost), dtype, mx, rows)
+    if got_lse is not None:
+        check_attention(out, got_lse, want, dtype, mx, rows)

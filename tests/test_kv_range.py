@@ -50,7 +50,7 @@ def attend_and_check(nv, lengths, new, q, cache, table, page, mx, dtype, scale, 
                                    window=window, lse=True)
     torch.cuda.synchronize()
     want = P.attention(q, cache, table, lengths, offsets, scale, window, cache.k_codes.shape[0], page)
-    P.check_attention(o, lse, want, dtype, mx)
+    P.check(o, lse, want, dtype, mx)
     return o, lse
 
 
@@ -129,7 +129,7 @@ def test_a_maximum_that_grows_by_a_unit_in_the_last_place(nv, dtype, rows, most,
     scale = most / (6 * 2.0 ** 14) * math.log(2.0)
     o, lse = nv.nvfp4_kv_attention(q.to(DT[dtype]), cache, table, ints([n]), ints([0, rows]), scale=scale, lse=True)
     off = (o.double() / v[0, 0] - 1.0).abs().max().item()
-    assert off <= P.WEIGHT[dtype, mx] + 1e-5 + torch.finfo(DT[dtype]).eps / 2, off
+    assert off <= P.HALF_STEP[dtype, mx] + 1e-5 + torch.finfo(DT[dtype]).eps / 2, off
     # 2^-24 each: the scale in binary32, log2(e), their product, the sum of products, the score's product, the sum with
     # the weights' logarithm, log(2), its product
     top = scale * (6 * 2.0 ** 14 + 2.0 ** -6 * 6)
@@ -150,7 +150,7 @@ def test_equal_scores_of_any_size_give_the_mean(nv, dtype, rows, most, mx):
     for r in range(rows):
         seen = v[:n - rows + 1 + r, 0]
         want, size = seen.mean(dim=0), seen.abs().mean(dim=0)
-        tol = (P.WEIGHT[dtype, mx] + 1e-5) * size + torch.finfo(DT[dtype]).eps / 2 * want.abs()
+        tol = (P.HALF_STEP[dtype, mx] + 1e-5) * size + torch.finfo(DT[dtype]).eps / 2 * want.abs()
         assert bool(((o[r, 0].double() - want).abs() <= 1.01 * tol).all()), r
 
 
@@ -169,7 +169,7 @@ def test_scores_far_below_others_leave_nothing(nv, dtype, rows, most, mx):
     q[..., 0] = 2.0 ** 14
     o = nv.nvfp4_kv_attention(q.to(DT[dtype]), cache, table, ints([n]), ints([0, rows]), scale=most / (6 * 2.0 ** 14))
     want, size = v[300:430, 0].mean(dim=0), v[300:430, 0].abs().mean(dim=0)
-    tol = (P.WEIGHT[dtype, mx] + 1e-5) * size + torch.finfo(DT[dtype]).eps / 2 * want.abs()
+    tol = (P.HALF_STEP[dtype, mx] + 1e-5) * size + torch.finfo(DT[dtype]).eps / 2 * want.abs()
     assert bool(((o[:, 0].double() - want).abs() <= 1.01 * tol).all())
 
 
@@ -253,4 +253,4 @@ def test_appended_keys_that_are_not_finite(nv, dim, dtype, rows, mx):
         k[bad, 1, :] = x
         cache, table = held(nv, [n], k, v, 32, mx)
         o, lse = nv.nvfp4_kv_attention(q, cache, table, ints([n]), ints([0, rows]), lse=True)
-        P.check_attention(o, lse, want, dtype, mx, rows=slice(0, rows + bad - n))
+        P.check(o, lse, want, dtype, mx, rows=slice(0, rows + bad - n))
