@@ -330,8 +330,8 @@ constexpr int kShares = D == 256 ? 512 : F32 && D == 128 ? 768 : 1024;
 
 // How the segments are divided, by what they are on the device:
 //   by team    no segment has more than kShort steps, and there are kManySegments
-//              at least: teams of 4, 2 or 1 waves, as many as there are segments or
-//              nearly, have whole ones;
+//              at least and no more than all waves: teams of 4, 2 or 1 waves, as many
+//              as there are segments or nearly, have one each;
 //   in parts   of `part` steps (kLeast at least), as many as there are workgroups
 //              or fewer, if that takes no more than kMostPart steps: a workgroup
 //              has one part;
@@ -341,8 +341,9 @@ constexpr int kShares = D == 256 ? 512 : F32 && D == 128 ? 768 : 1024;
 //              cost.
 // (Parts end with their segment where shares would have a second one to begin,
 // which costs some 5 us; many steps are better divided evenly.  40 heads, 8 kv heads of
-// 128: 256 sequences of up to 500 positions, their pages scattered, by team 46 us,
-// else 59; one token over 8192 in parts 14.9, in shares 15.7; 16 sequences of up to
+// 128: 256 sequences of up to 500 positions by team 28.4 us, in shares 43.5, 512 of them
+// 51.8 and 76; past all waves, where teams went round again, 520 took 166 and 79, 4096
+// 1897 and 460; one token over 8192 in parts 14.9, in shares 15.7; 16 sequences of up to
 // 2000 with kExtra 22.6, without 24.7; one over 2048 with parts of 4 steps and more
 // 11.6, of 8 12.7, over 8192 14.9 and 14.1.)
 constexpr int kShort = 16, kManySegments = 512, kLeast = kWaves, kMostPart = 32, kExtra = 4;
@@ -379,7 +380,7 @@ __device__ __forceinline__ Division divide(const KvAttention& p, const Quad& fir
     steps = sum64(steps);
     segments = sum64(segments);
     Division d = {};
-    if (!__any(longer) && segments >= kManySegments) d.team = segments <= most ? 4 : segments <= 2 * most ? 2 : 1;
+    if (!__any(longer) && segments >= kManySegments) d.team = segments <= most ? 4 : segments <= 2 * most ? 2 : segments <= 4 * most ? 1 : 0;
     if (d.team || segments == 0) {
         d.sum = segments;
         return d;
@@ -582,10 +583,10 @@ __global__ void __launch_bounds__(kThreads, (kShares<F32, D> / 256)) k_kv_attent
         const Segment g = segment_at(p, d, q, seq_first, own);
         // steps [from, to) of the segment's
         int from = 0, to = idle ? 0 : q.real;
+        if (d.team || d.part) u_end = 0;  // (a team or a workgroup has one entry)
         if (d.part) {
             from = (int)(u - g.begin) * d.part;
             to = min(q.real, from + d.part);
-            u_end = 0;
         } else if (!d.team) {
             from = (int)min(u - g.begin, (int64_t)q.real);
             to = (int)min(u_end - g.begin, (int64_t)q.real);
@@ -805,7 +806,6 @@ __global__ void __launch_bounds__(kThreads, (kShares<F32, D> / 256)) k_kv_attent
                     store_out<F32>(p, q, g, col, 16 * i + 4 * g4, mean(o[i][0], o[i][1], o[i][2], o[i][3]));
                 if (p.lse && g4 == 0) store_lse(p, q, g, col, m, bias, l);
             }
-            u += (int64_t)gridDim.x * kWaves;
             continue;
         }
         // the waves' sums, joined in order
@@ -846,7 +846,7 @@ __global__ void __launch_bounds__(kThreads, (kShares<F32, D> / 256)) k_kv_attent
             }
         }
         __syncthreads();
-        u = d.team ? u + (int64_t)gridDim.x * teams : g.begin + g.entries;
+        u = g.begin + g.entries;
     }
 }
 

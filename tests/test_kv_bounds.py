@@ -118,3 +118,11 @@ def test_more_short_sequences_than_waves(nv, seqs, heads, dim, dtype):
     attend(nv, lengths, None, heads, dim, False, dtype, 37)
     new = [min(l, (3 * i) % 4) for i, l in enumerate(lengths)]
     attend(nv, lengths, new, heads, dim, True, dtype, 38)
+
+
+@pytest.mark.parametrize("dim,dtype,teams", [(64, "bf16", 1024), (128, "f32", 768), (256, "bf16", 512)])
+def test_as_many_short_sequences_as_teams(nv, dim, dtype, teams):
+    """One segment more and less than workgroups, pairs of waves and waves there are."""
+    for count in (teams, 2 * teams, 4 * teams):
+        for seqs in (count // 8, count // 8 + 1):
+            attend(nv, [1 + (31 * i) % 45 for i in range(seqs)], None, 8, dim, False, dtype, 39)
