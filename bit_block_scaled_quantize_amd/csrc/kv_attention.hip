@@ -70,10 +70,11 @@ constexpr float kSlack = 4.0f;
 // would pass FP16's largest (or all bounds), so scores are rounded to binary32 first
 // and the maximum, the true one of all keys so far, taken off exactly.
 constexpr float kFar = 1048576.0f;
-// Sequences of more columns than this for a kv head are k_kv_prefill's (BF16 q).  (64
-// sequences of 4096 positions, by k_kv_attention and k_kv_prefill: 40 columns 174 and
-// 202 us, 60 columns 199 and 204, 80 columns 266 and 208; 4 sequences, 60 columns 34
-// and 43, 80 columns 39 and 45.)
+// Sequences of more columns than this for a kv head are k_kv_prefill's (BF16 q).  (Over
+// 4096 positions, by k_kv_attention and k_kv_prefill: 64 sequences of 35 columns 181 and
+// 203 us, of 60 204 and 205, of 80 266 and 212; 16 sequences of 60 67 and 80, of 80 81 and
+// 82, of 100 102 and 85.  For fewer sequences it could be more: 4 of 80 39 and 46, of 125
+// 42 and 49; one of 80 25 and 43.)
 constexpr int kFewColumns = 64;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -341,12 +342,15 @@ constexpr int kShares = D == 256 ? 512 : F32 && D == 128 ? 768 : 1024;
 //              cost.
 // (Parts end with their segment where shares would have a second one to begin,
 // which costs some 5 us; many steps are better divided evenly.  40 heads, 8 kv heads of
-// 128: 256 sequences of up to 500 positions by team 28.4 us, in shares 43.5, 512 of them
-// 51.8 and 76; past all waves, where teams went round again, 520 took 166 and 79, 4096
-// 1897 and 460; one token over 8192 in parts 14.9, in shares 15.7; 16 sequences of up to
-// 2000 with kExtra 22.6, without 24.7; one over 2048 with parts of 4 steps and more
-// 11.6, of 8 12.7, over 8192 14.9 and 14.1.)
-constexpr int kShort = 16, kManySegments = 512, kLeast = kWaves, kMostPart = 32, kExtra = 4;
+// 128, by team and in shares: 256 sequences of up to 500 positions 28.4 and 43.5 us, 512
+// of them 51.8 and 76, up to 1000 positions 45.7 and 59.8, 91 and 109; one of 1000 among
+// 256 of up to 500 29.8 and 44.0, one of 2000 (kShort 64) 46.1 and 44.2, among 512 96 and
+// 79.  Past all waves, where teams would go round again, 520 sequences 166 and 79, 4096
+// 1897 and 460.  In parts and in shares: one token over 2048 11.9 and 11.3, over 8192 14.9
+// and 15.3, 16 over up to 8000 27.6 and 28.7; with parts of 8 steps and more one over 2048
+// 13.0, over 8192 14.0, 16 over up to 2000 18.2 instead of 20.2.  kExtra: 33 sequences of
+// up to 10000 46 us, without it 92.)
+constexpr int kShort = 32, kManySegments = 512, kLeast = kWaves, kMostPart = 32, kExtra = 4;
 struct Division {
     int team;           // waves of a team; 0: not by team
     int part;           // 0: in shares

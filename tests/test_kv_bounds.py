@@ -126,3 +126,12 @@ def test_as_many_short_sequences_as_teams(nv, dim, dtype, teams):
     for count in (teams, 2 * teams, 4 * teams):
         for seqs in (count // 8, count // 8 + 1):
             attend(nv, [1 + (31 * i) % 45 for i in range(seqs)], None, 8, dim, False, dtype, 39)
+
+
+@pytest.mark.parametrize("longest", [1023, 1024, 1025])
+def test_the_longest_segment_of_a_team(nv, longest):
+    """Divided by team up to 32 steps, in shares past them."""
+    lengths = [1 + (353 * i) % 1000 for i in range(80)]
+    lengths[41] = longest
+    attend(nv, lengths, None, 8, 64, False, "bf16", 40)
+    attend(nv, lengths, None, 8, 128, True, "f32", 41)
