@@ -18,15 +18,15 @@
 // all (sequence, kv head, 16 columns) form one list that is divided by its sizes on
 // the device (Division), so the host needs no length and a captured call serves
 // changing ones; what several workgroups share of a segment is joined by a second
-// kernel, in order.  Time, of 8 kv heads of 128, BF16: one token of 40 heads over 8192
-// positions 14.3 us; 256 of 40 over up to 501 28.9 us; 64 of 56 over up to 20480 157
-// us, 4.74 TB/s of codes and scales, where a large copy reaches 5.04.  (The D 256
-// instance of binary32 over MXFP4, with three parts of both operands, keeps 12 bytes
-// a lane in scratch memory.)
+// kernel, in order.  Time, of 8 kv heads of 128, BF16, without offsets: one token of 40
+// heads over 8192 positions 14.6 us; 256 of 40 over up to 501 30.2 us; 64 of 56 over up
+// to 20480 158 us, 4.7 TB/s of codes and scales, where a large copy, read and written,
+// reaches 5.04.  (The D 256 instance of binary32 over MXFP4, with three parts of both
+// operands, keeps 24 bytes a lane in scratch memory.)
 //
-// Many columns of BF16 (k_kv_prefill; bounded by the matrix cores beside the vector
-// instructions of the softmax): 256 columns, 64 keys at a time, in two phases; 8192
-// rows of 40 heads with causal masks in 710 us, 970 TFLOP/s of the 1220 that a
+// Many columns of BF16 (k_kv_prefill; bounded by the alternation of matrix and vector
+// instructions, neither of which fills its pipe): 256 columns, 64 keys at a time, in two phases; 8192 rows of 40 heads with
+// causal masks in 731 to 766 us on several cards, 900 to 940 TFLOP/s of the 1220 that a
 // product of 8192^3 reaches.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -440,7 +440,7 @@ __device__ __forceinline__ float* slot_of(const KvAttention& p, int64_t w, int w
 
 // What the second kernel's workgroup w - 1 joins: an equal part (the rank-th of n - 1)
 // of the segment that workgroup w's share begins inside of, whose n parts are those of
-// workgroups first_share and on.  n 0: nothing.  (Found again there, it took one token
+// workgroups first_share and on.  n 0: nothing.  (With that found again there, one token
 // over 8192 positions took 15.4 us instead of 14.3.)
 struct Join {
     int n, rank, first_share, row, head, first, count;
@@ -930,10 +930,13 @@ __global__ void __launch_bounds__(kThreads) k_kv_join(const KvAttention p) {
 // waves of a SIMD are a phase apart, so that one's matrix instructions go with the
 // other's vector instructions.  Keys are then converted two tiles ahead, values one,
 // into three buffers each (D 256 has one wave to a SIMD: one tile ahead, one buffer).
-// 8192 rows of 40 heads behind nothing, a causal half: D 128 704 to 720 us (the waves'
-// phases together 804), bound by vector issue beside 80% of the matrix cores' rate;
-// over MXFP4, whose weights have two parts, 880; D 64 544, where the softmax is twice as
-// much beside a product; D 256 2175, one wave to a SIMD.
+// 8192 rows of 40 heads behind nothing, a causal half: D 128 731 to 766 us (with the
+// waves' phases together 804 instead of 723): the matrix cores are busy in 39% of the
+// cycles, vector instructions issue in 44%, both in 24%; the rest are the phases' ends and
+// what their first instructions wait for.  Over MXFP4, whose weights have two parts, 875
+// (52, 48 and 31%); D 64 532, where the softmax is twice as much beside a product (26, 49
+// and 17%); D 256 2155, one wave to a SIMD (25, 36 and 2%, and LDS busy in 39% of the
+// cycles, half of them conflicts).
 template <int D>
 constexpr int kPreWaves = D == 256 ? 4 : 8;
 template <int D>
@@ -1338,7 +1341,7 @@ __global__ void __launch_bounds__(64 * kPreWaves<D>, kPreWaves<D> / 4) k_kv_pref
     // Where some score was far the tiles are gone over again, with exact differences: the
     // maximum is still far, or a weight that passed its type's largest has left what is no
     // number, which no later rescaling takes away.  (A choice between the two in every tile
-    // cost 1 to 5% of the time, as one more branch or as scores that two branches write.)
+    // cost 1 to 13% of the time, by where it stood.)
     __shared__ int some_far;
     if (threadIdx.x == 0) some_far = 0;
     all_tiles(std::false_type());

@@ -531,7 +531,9 @@ nvfp4_status nvfp4_expert_gemv(const void* x, int32_t dt /* nvfp4_dtype */, int6
  *           tensor scale: positive and fixed while the cache is in use;
  *           MXFP4: pages x kv_heads x page_size x head_dim/32 E8M0 bytes;
  *           k_scale and v_scale are NULL.
- * What a slot holds before it is appended to is never read as a number.
+ * What a slot holds before it is appended to is never read as a number.  The
+ * slots of a sequence's positions must hold finite values (as an append writes
+ * them) also where no row sees them.
  *
  * The plan of a call says which rows it deals with.  Sequence s has the pages
  * page_table[s * ld_table + i], i < width, of which the i-th holds its positions
