@@ -25,9 +25,9 @@
 // operands, keeps 24 bytes a lane in scratch memory.)
 //
 // Many columns of BF16 (k_kv_prefill; bounded by the alternation of matrix and vector
-// instructions, neither of which fills its pipe): 256 columns, 64 keys at a time, in two phases; 8192 rows of 40 heads with
-// causal masks in 731 to 766 us on several cards, 900 to 940 TFLOP/s of the 1220 that a
-// product of 8192^3 reaches.
+// instructions, neither of which fills its pipe): 256 columns, 64 keys at a time, in
+// two phases; 8192 rows of 40 heads with causal masks in 731 to 766 us on several cards,
+// 900 to 940 TFLOP/s of the 1220 that a product of 8192^3 reaches.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -124,8 +124,8 @@ struct Form<true> {
 // Parts of q: a BF16 value fits FP16 once its row is scaled to [2^14, 2^15) (an
 // element below 2^-29 of the row's largest keeps 2^-25 of 2^14, past the
 // products' binary32 sums), a binary32 one two FP16 or three BF16 parts.  Parts
-// of a weight: one FP16 part is off by 2^-11, two BF16 parts by
-// 2^-17, of binary32 results two FP16 parts by 2^-23, three BF16 parts by 2^-25.
+// of a weight: one FP16 part is off by 2^-11, two BF16 parts by 2^-17, of binary32
+// results two FP16 parts by 2^-23, three BF16 parts by 2^-25.
 template <bool MX, bool F32>
 constexpr int kQParts = F32 ? (MX ? 3 : 2) : 1;
 template <bool MX, bool F32>
